@@ -87,7 +87,9 @@ def lib():
         except ImportError:  # pragma: no cover
             pass
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGS.items():
+        from .training_ops import SIGS
+
+        for name, (res, args) in {**_SIGS, **SIGS}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -392,3 +394,15 @@ def test_stall_next_launch(item=0):
     load of its first warp's item ``item`` never complete, so that warp's bounded wait gives up
     and sets the fault word (read by device_fault).  For tests of the failure path."""
     _check(lib().demo_test_stall_next_launch(item), "demo_test_stall_next_launch")
+
+
+_TRAINING_OPS = ("dropout", "fp8_quantize", "fp8_matmul", "fp8_linear", "Fp8Matrix")
+
+
+def __getattr__(name):
+    """The training operators (training_ops.py needs torch, which this module imports on use)."""
+    if name in _TRAINING_OPS:
+        from . import training_ops
+
+        return getattr(training_ops, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

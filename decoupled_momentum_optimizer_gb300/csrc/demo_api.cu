@@ -9,14 +9,11 @@
 #include "../../include/demo.h"
 #include "demo_common.cuh"
 #include "demo_launch.h"
+#include "train_launch.h"
 
 namespace {
 
 using namespace demo;
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxN = int64_t(1) << 35;  // keeps every row coordinate within int32
@@ -518,6 +515,17 @@ PayloadLayout payload_layout(int mode, int k, int wire) {
 
 }  // namespace
 
+namespace demo {
+
+int device_info(DeviceInfo* out) {
+  DeviceState* st = nullptr;
+  const int s = current_state(&st);
+  if (s == DEMO_OK) *out = DeviceInfo{st->sms, st->fault, g_encode};
+  return s;
+}
+
+}  // namespace demo
+
 extern "C" {
 
 const char* demo_status_string(int status) {
@@ -562,7 +570,8 @@ int demo_init(int device) {
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
     return DEMO_ECUDA;
   if (prepare_step_kernels() != cudaSuccess || prepare_encode_kernels() != cudaSuccess ||
-      prepare_decode_kernels() != cudaSuccess || prepare_dense_kernels() != cudaSuccess)
+      prepare_decode_kernels() != cudaSuccess || prepare_dense_kernels() != cudaSuccess ||
+      prepare_matmul_kernels() != cudaSuccess)
     return DEMO_ECUDA;
   void* fault = nullptr;
   if (cudaGetSymbolAddress(&fault, g_fault_word) != cudaSuccess) return DEMO_ECUDA;

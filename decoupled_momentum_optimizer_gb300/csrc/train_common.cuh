@@ -1,0 +1,105 @@
+// What the training operators (dropout, block-scaled 8-bit quantization, products) share:
+// element types, the dropout mask, and the scale and codes of a block of 128.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "demo_common.cuh"
+#include "train_launch.h"
+
+namespace demo {
+
+// ----------------------------------------------------------------------------
+// Elements in 16 or 32 bits, computed with in float32
+// ----------------------------------------------------------------------------
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+
+// N consecutive elements as one access of N * sizeof(T) bytes (at most 16, aligned to its size).
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Vec {
+  T e[N];
+};
+
+// ----------------------------------------------------------------------------
+// The dropout mask: 16 bits per element of a counter-based hash
+// ----------------------------------------------------------------------------
+
+// h(g) = sm(key ^ g) gives the four elements of group g = row * ceil(cols / 4) + col / 4 sixteen
+// bits each; an element is kept where its bits are at least `threshold` = round(65536 p).  Sixteen
+// bits keep the hash at about six integer operations per element (32 bits each would double it and
+// make the bfloat16 kernel issue-bound); p is taken to the nearest 1/65536, and the kept values'
+// factor is that of the p actually applied, so the expected value is exact.
+struct DropMask {
+  uint64_t key;
+  uint32_t threshold;  // 0 keeps everything, 65536 nothing
+  float scale;         // 65536 / (65536 - threshold)
+
+  __device__ __forceinline__ uint64_t group(uint64_t g) const { return splitmix64(key ^ g); }
+  __device__ __forceinline__ bool keep(uint64_t h, int lane) const {
+    return ((static_cast<uint32_t>(h >> (16 * lane))) & 0xffffu) >= threshold;
+  }
+  // A dropped element is 0 whatever it held, an infinity or a NaN included.
+  __device__ __forceinline__ float apply(float v, uint64_t h, int lane) const {
+    return keep(h, lane) ? v * scale : 0.0f;
+  }
+};
+
+inline __device__ DropMask drop_mask(const DropParams& d) { return DropMask{d.key, d.threshold, d.scale}; }
+
+// ----------------------------------------------------------------------------
+// Block scales and codes
+// ----------------------------------------------------------------------------
+
+// Exponent of the block scale: the smallest e >= -126 with amax <= 2^e * (largest finite code),
+// 0 for a block of zeros.  `bits` are the float32 bits of amax (finite, not negative).  Both
+// formats' largest code is 1.75 * 2^top, so e = exponent(amax) - top, one more when amax's
+// significand is above 1.75.
+__device__ __forceinline__ int scale_exponent(uint32_t bits, int top) {
+  if (bits == 0) return 0;
+  const int e = static_cast<int>(bits >> 23) - 127 - top + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return e < -126 ? -126 : e;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// A non-finite element becomes a NaN code (neither format's codes saturate silently); it does not
+// take part in its block's scale (fmaxf passes over a NaN).
+__device__ __forceinline__ float finite_or_nan(float v) {
+  return fabsf(v) <= 3.402823466e38f ? v : __uint_as_float(0x7fc00000u);
+}
+
+// Two codes, `lo` in the low byte; nearest even.  Block scaling keeps |v| at or below the largest
+// code, so saturation never applies.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, FMT == kE4M3 ? __NV_E4M3 : __NV_E5M2);
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return codes2<FMT>(a, b) | (codes2<FMT>(c, d) << 16);
+}
+
+}  // namespace demo

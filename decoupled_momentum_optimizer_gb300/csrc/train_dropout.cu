@@ -1,0 +1,180 @@
+// Dropout with a counter-based mask that is never stored, with or without a residual added:
+//
+//   out[r][c] = residual[r][c] + (keep(r, c) ? x[r][c] * 65536 / (65536 - T) : 0)
+//
+// keep(r, c) is 16 bits of a splitmix64 hash of (seed, step, site, position) compared with T (see
+// DropMask), the framework's shared-seed generator, so a backward pass, a replica or a resumed run
+// recomputes the same mask from four numbers.  The gradient with respect to x is the same map
+// applied to dy, without a residual.
+//
+// One pass, bound by HBM: 2 or 3 accesses of the element's size per element against about a dozen
+// integer and float operations.  One hash covers four elements, so every thread owns whole groups
+// of four.  Three access patterns:
+//   flat      rows end to end and whole groups per row: positions are flat, 16-byte accesses
+//   groups    a thread per group; one access of four elements where the strides and addresses
+//             allow it, else four (only for rows of less than 64 elements: see launch_dropout)
+//   segments  rows of any alignment: a warp covers 128 columns with 32-wide accesses, each lane
+//             hashes one group, and the lanes pass the hashes round
+#include "train_common.cuh"
+
+namespace demo {
+
+constexpr int kDropThreads = 256;
+
+template <typename T, bool RES>
+__device__ __forceinline__ T drop_one(const DropMask& d, T x, T res, uint64_t h, int lane) {
+  float v = d.apply(to_f32(x), h, lane);
+  if constexpr (RES) v += to_f32(res);
+  return from_f32<T>(v);
+}
+
+// Elements per 16-byte access, and accesses per thread (all loads are issued before any store).
+template <typename T>
+constexpr int kPer16 = 16 / static_cast<int>(sizeof(T));
+constexpr int kFlatUnroll = 4;
+
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kDropThreads) dropout_flat(const __grid_constant__ DropoutParams p, long long n) {
+  constexpr int N = kPer16<T>;
+  using V = Vec<T, N>;
+  const DropMask d = drop_mask(p.drop);
+  const long long units = n / N;
+  const V* x = static_cast<const V*>(p.x);
+  const V* res = static_cast<const V*>(p.residual);
+  V* out = static_cast<V*>(p.out);
+  const long long base = static_cast<long long>(blockIdx.x) * (kDropThreads * kFlatUnroll) + threadIdx.x;
+  V a[kFlatUnroll], b[kFlatUnroll];
+#pragma unroll
+  for (int j = 0; j < kFlatUnroll; ++j) {
+    const long long u = base + j * kDropThreads;
+    if (u < units) {
+      a[j] = x[u];
+      if constexpr (RES) b[j] = res[u];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kFlatUnroll; ++j) {
+    const long long u = base + j * kDropThreads;
+    if (u < units) {
+      V o;
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const uint64_t h = d.group(static_cast<uint64_t>(u) * (N / 4) + q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o.e[4 * q + e] = drop_one<T, RES>(d, a[j].e[4 * q + e], RES ? b[j].e[4 * q + e] : T(), h, e);
+      }
+      out[u] = o;
+    }
+  }
+  // The last group of a 16-bit tensor whose size is not a multiple of 8.
+  if (N > 4 && n % N != 0 && base == 0) {
+    const uint64_t h = d.group(static_cast<uint64_t>(n / 4 - 1));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const long long i = n - 4 + e;
+      static_cast<T*>(p.out)[i] = drop_one<T, RES>(
+          d, static_cast<const T*>(p.x)[i], RES ? static_cast<const T*>(p.residual)[i] : T(), h, e);
+    }
+  }
+}
+
+template <typename T, bool RES, bool VEC>
+__global__ void __launch_bounds__(kDropThreads) dropout_groups(const __grid_constant__ DropoutParams p, long long G) {
+  using V = Vec<T, 4>;
+  const DropMask d = drop_mask(p.drop);
+  const long long g = static_cast<long long>(blockIdx.x) * kDropThreads + threadIdx.x;
+  if (g >= p.rows * G) return;
+  // 64-bit division only where the group count needs it
+  const long long row = g < (1ll << 32) && G < (1ll << 32)
+                            ? static_cast<long long>(static_cast<uint32_t>(g) / static_cast<uint32_t>(G))
+                            : g / G;
+  const long long c0 = (g - row * G) * 4;
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx + c0;
+  const T* res = RES ? static_cast<const T*>(p.residual) + row * p.ldr + c0 : nullptr;
+  T* out = static_cast<T*>(p.out) + row * p.ldo + c0;
+  if (VEC && c0 + 4 <= p.cols) {
+    const V a = *reinterpret_cast<const V*>(x);
+    V b;
+    if constexpr (RES) b = *reinterpret_cast<const V*>(res);
+    const uint64_t h = d.group(static_cast<uint64_t>(g));
+    V o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o.e[e] = drop_one<T, RES>(d, a.e[e], RES ? b.e[e] : T(), h, e);
+    *reinterpret_cast<V*>(out) = o;
+    return;
+  }
+  const uint64_t h = d.group(static_cast<uint64_t>(g));
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c0 + e < p.cols) out[e] = drop_one<T, RES>(d, x[e], RES ? res[e] : T(), h, e);
+}
+
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kDropThreads)
+    dropout_segments(const __grid_constant__ DropoutParams p, long long G, long long per_row) {
+  const DropMask d = drop_mask(p.drop);
+  const int lane = threadIdx.x & 31;
+  const long long s = static_cast<long long>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5);
+  if (s >= p.rows * per_row) return;  // whole warps
+  const long long row = s < (1ll << 32) && per_row < (1ll << 32)
+                            ? static_cast<long long>(static_cast<uint32_t>(s) / static_cast<uint32_t>(per_row))
+                            : s / per_row;
+  const long long c0 = (s - row * per_row) * 128;
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx + c0;
+  const T* res = RES ? static_cast<const T*>(p.residual) + row * p.ldr + c0 : nullptr;
+  T* out = static_cast<T*>(p.out) + row * p.ldo + c0;
+  const int live = p.cols - c0 < 128 ? static_cast<int>(p.cols - c0) : 128;
+  T a[4], b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (32 * j + lane < live) {
+      a[j] = x[32 * j + lane];
+      if constexpr (RES) b[j] = res[32 * j + lane];
+    }
+  }
+  const uint64_t own = d.group(static_cast<uint64_t>(row * G + c0 / 4 + lane));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t h = __shfl_sync(0xffffffffu, own, 8 * j + (lane >> 2));
+    if (32 * j + lane < live)
+      out[32 * j + lane] = drop_one<T, RES>(d, a[j], RES ? b[j] : T(), h, lane & 3);
+  }
+}
+
+template <typename T, bool RES>
+static cudaError_t launch_dropout_t(const DropoutParams& p, cudaStream_t st) {
+  const auto at = [](const void* q, size_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; };
+  const auto all_at = [&](size_t a) { return at(p.x, a) && at(p.out, a) && (!RES || at(p.residual, a)); };
+  const long long G = (p.cols + 3) / 4;
+  const bool flat = (p.rows == 1 || (p.ldx == p.cols && p.ldo == p.cols && (!RES || p.ldr == p.cols))) &&
+                    p.cols % 4 == 0 && all_at(16);
+  const bool vec = all_at(4 * sizeof(T)) &&
+                   (p.rows == 1 || (p.ldx % 4 == 0 && p.ldo % 4 == 0 && (!RES || p.ldr % 4 == 0)));
+  const auto blocks = [](long long items, long long per) { return static_cast<unsigned>((items + per - 1) / per); };
+  if (flat) {
+    const long long n = p.rows * p.cols;
+    const long long units = n / kPer16<T> + 1;  // at least one block, for the last group
+    dropout_flat<T, RES><<<blocks(units, kDropThreads * kFlatUnroll), kDropThreads, 0, st>>>(p, n);
+  } else if (vec) {
+    dropout_groups<T, RES, true><<<blocks(p.rows * G, kDropThreads), kDropThreads, 0, st>>>(p, G);
+  } else if (p.cols < 64) {
+    // A warp per segment would leave most of its lanes idle on rows this short.
+    dropout_groups<T, RES, false><<<blocks(p.rows * G, kDropThreads), kDropThreads, 0, st>>>(p, G);
+  } else {
+    const long long per_row = (p.cols + 127) / 128;
+    dropout_segments<T, RES>
+        <<<blocks(p.rows * per_row, kDropThreads / 32), kDropThreads, 0, st>>>(p, G, per_row);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dropout(const DropoutParams& p, int dtype, cudaStream_t st) {
+  const bool res = p.residual != nullptr;
+  if (dtype == kF32) return res ? launch_dropout_t<float, true>(p, st) : launch_dropout_t<float, false>(p, st);
+  if (dtype == kBF16)
+    return res ? launch_dropout_t<__nv_bfloat16, true>(p, st) : launch_dropout_t<__nv_bfloat16, false>(p, st);
+  return res ? launch_dropout_t<__half, true>(p, st) : launch_dropout_t<__half, false>(p, st);
+}
+
+}  // namespace demo

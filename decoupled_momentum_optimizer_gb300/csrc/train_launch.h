@@ -1,0 +1,79 @@
+// Parameter blocks and launchers of the training operators' kernels (dropout, block-scaled 8-bit
+// quantization, products of quantized matrices), and what their C entry points need of the
+// library's per-device state.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace demo {
+
+enum { kF32 = 0, kBF16 = 1, kF16 = 2 };
+enum { kE4M3 = 0, kE5M2 = 1 };
+
+constexpr int kBlock = 128;  // elements that share a scale
+// Exponent of each format's largest finite code, 1.75 * 2^top (448 and 57344).
+__host__ __device__ constexpr int fmt_top(int fmt) { return fmt == kE4M3 ? 8 : 15; }
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The initialised current device; returns a status of include/demo.h.
+struct DeviceInfo {
+  int sms;
+  unsigned int* fault;
+  EncodeTiledFn encode;
+};
+int device_info(DeviceInfo* out);
+
+struct DropParams {
+  unsigned long long key;  // sm(sm(sm(seed) ^ step) ^ site)
+  unsigned int threshold;
+  float scale;
+};
+
+struct DropoutParams {
+  const void* x;
+  const void* residual;  // may be NULL
+  void* out;
+  long long rows, cols, ldx, ldr, ldo;
+  DropParams drop;
+};
+
+cudaError_t launch_dropout(const DropoutParams& p, int dtype, cudaStream_t st);
+
+struct QuantParams {
+  const void* x;
+  const void* gate;  // may be NULL
+  long long rows, cols, ldx, ldg;
+  unsigned int row_blocks, col_blocks;  // of 128; their product is the grid
+  int relu, tiles;
+  DropParams drop;
+  void* codes_rows;    // [rows][cols up to 128], may be NULL
+  float* scales_rows;  // [column blocks][rows up to 4]
+  void* codes_cols;    // [cols][rows up to 128], may be NULL
+  float* scales_cols;  // [row blocks][cols up to 4]
+};
+
+cudaError_t launch_quantize(const QuantParams& p, int dtype, int fmt, cudaStream_t st);
+
+// out = a b^T (+ out): a [m][k], b [n][k] quantized by rows.
+struct MatmulParams {
+  CUtensorMap a, b;  // codes, unused without blocks
+  const float* a_scales;
+  const float* b_scales;
+  long long m, n;
+  int kb;  // blocks of 128 along k, may be 0
+  long long ldo;
+  void* out;
+  int out_dtype, add, b_tiles;
+  int a_fmt, b_fmt;
+  unsigned int* fault;
+};
+
+cudaError_t launch_matmul(const MatmulParams& p, int sms, cudaStream_t st);
+cudaError_t prepare_matmul_kernels();
+
+}  // namespace demo

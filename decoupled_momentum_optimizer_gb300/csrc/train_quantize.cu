@@ -1,0 +1,230 @@
+// Quantization of a matrix to 8-bit floating point with one power-of-two scale for each block of
+// 128, by rows, by columns (the codes of the transpose) or both from one read of the matrix:
+//
+//   v[r][c]  = x[r][c], then relu, dropout and a gate if asked
+//   s        = the smallest power of two >= 2^-126 with max |v| over the block <= s * largest code
+//   code     = v / s rounded to nearest even      (division by a power of two is exact)
+//
+// A block is 128 consecutive elements of a row (row form) or of a column (column form), or a whole
+// 128 x 128 tile.  The feed-forward layer's relu and dropout, or their gradient (the gate h > 0 and
+// the same dropout mask), run in registers on the way, so the activation between them and the
+// quantized product is never stored in 16 or 32 bits.
+//
+// A CTA owns a 128 x 128 tile and keeps it in registers: warp w holds rows 16 w .. 16 w + 15, lane
+// l their columns 4 l .. 4 l + 3, all 16 row loads in flight at once.  A row's block is one warp's
+// 128 elements (one warp-wide maximum each), a column's block is 16 registers of a lane and the 8
+// warps' maxima in shared memory.  Row codes leave as 128 contiguous bytes per row; column codes
+// are packed 16 rows at a time from the same registers, and leave through a swizzled 16 KB tile in
+// shared memory as 128 contiguous bytes per column.  Bound by HBM: the matrix is read once and each
+// form written once.
+#include "train_common.cuh"
+
+namespace demo {
+
+constexpr int kQuantThreads = 256;
+
+struct QuantShared {
+  float colmax[8][kBlock];  // each warp's column maxima (the tile's maximum uses the first column)
+  uint32_t warpmax[8];
+  uint4 codes[kBlock * 8];  // column codes, 8 units of 16 rows per column, swizzled
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load4(const T* p, int live, float (&v)[4]) {
+  if (VEC) {
+    if (live > 0) {  // whole groups of four only: see launch_quantize
+      const Vec<T, 4> q = *reinterpret_cast<const Vec<T, 4>*>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = to_f32(q.e[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = e < live ? to_f32(p[e]) : 0.0f;
+  }
+}
+
+template <typename T, int FMT, bool VEC, bool GATE>
+__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_constant__ QuantParams p) {
+  __shared__ QuantShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned tile_r = blockIdx.x / p.col_blocks, tile_c = blockIdx.x - tile_r * p.col_blocks;
+  const long long r0 = static_cast<long long>(tile_r) * kBlock + 16 * warp;
+  const long long c0 = static_cast<long long>(tile_c) * kBlock + 4 * lane;
+  const int live_rows = p.rows - r0 >= 16 ? 16 : p.rows > r0 ? static_cast<int>(p.rows - r0) : 0;
+  const int live_cols = p.cols - c0 >= 4 ? 4 : p.cols > c0 ? static_cast<int>(p.cols - c0) : 0;
+  float v[16][4];
+  {
+    const T* x = static_cast<const T*>(p.x) + r0 * p.ldx + c0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) load4<T, VEC>(x + i * p.ldx, i < live_rows ? live_cols : 0, v[i]);
+  }
+  if constexpr (GATE) {
+    const T* g = static_cast<const T*>(p.gate) + r0 * p.ldg + c0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float h[4];
+      load4<T, VEC>(g + i * p.ldg, i < live_rows ? live_cols : 0, h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = h[e] > 0.0f ? v[i][e] : 0.0f;
+    }
+  }
+  if (p.relu) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = v[i][e] < 0.0f ? 0.0f : v[i][e];
+  }
+  if (p.drop.threshold != 0) {
+    const DropMask d = drop_mask(p.drop);
+    const unsigned long long G = static_cast<unsigned long long>((p.cols + 3) / 4);
+    unsigned long long g = static_cast<unsigned long long>(r0) * G + static_cast<unsigned long long>(c0 / 4);
+#pragma unroll
+    for (int i = 0; i < 16; ++i, g += G) {
+      const uint64_t h = d.group(g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = d.apply(v[i][e], h, e);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[i][e] = finite_or_nan(v[i][e]);
+
+  constexpr int top = fmt_top(FMT);
+  // Float bits of non-negative values order as unsigned integers.
+  uint32_t rowbits[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    rowbits[i] = __float_as_uint(
+        fmaxf(fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3]))), 0.0f));
+  int tile_e = 0;
+  if (p.tiles) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = umax32(m, rowbits[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) sh.warpmax[warp] = m;
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = umax32(m, sh.warpmax[w]);
+    tile_e = scale_exponent(m, top);
+  }
+  if (p.codes_rows != nullptr) {
+    const long long kp = static_cast<long long>(p.col_blocks) * kBlock;
+    uint8_t* dst = static_cast<uint8_t*>(p.codes_rows) + r0 * kp + c0;
+    float mine = 1.0f;  // lane i: the scale of row i
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = p.tiles ? tile_e : scale_exponent(__reduce_max_sync(0xffffffffu, rowbits[i]), top);
+      const float inv = pow2f(-e);
+      if (lane == i) mine = pow2f(e);
+      if (i < live_rows)
+        *reinterpret_cast<uint32_t*>(dst + i * kp) =
+            codes4<FMT>(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+    }
+    // rows past the matrix up to the scales' stride hold 1
+    const long long lds = (p.rows + 3) / 4 * 4;
+    if (lane < 16 && r0 + lane < lds)
+      p.scales_rows[static_cast<long long>(tile_c) * lds + r0 + lane] = r0 + lane < p.rows ? mine : 1.0f;
+  }
+  if (p.codes_cols != nullptr) {
+    float inv[4];
+    if (!p.tiles) {
+      float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        m.x = fmaxf(m.x, fabsf(v[i][0]));
+        m.y = fmaxf(m.y, fabsf(v[i][1]));
+        m.z = fmaxf(m.z, fabsf(v[i][2]));
+        m.w = fmaxf(m.w, fabsf(v[i][3]));
+      }
+      *reinterpret_cast<float4*>(&sh.colmax[warp][4 * lane]) = m;
+    }
+    __syncthreads();
+    const long long lds = (p.cols + 3) / 4 * 4;
+    {
+      float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (!p.tiles) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float4 q = *reinterpret_cast<const float4*>(&sh.colmax[w][4 * lane]);
+          m.x = fmaxf(m.x, q.x);
+          m.y = fmaxf(m.y, q.y);
+          m.z = fmaxf(m.z, q.z);
+          m.w = fmaxf(m.w, q.w);
+        }
+      }
+      const float ms[4] = {m.x, m.y, m.z, m.w};
+      float s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = p.tiles ? tile_e : scale_exponent(__float_as_uint(ms[e]), top);
+        inv[e] = pow2f(-x);
+        s[e] = e < live_cols ? pow2f(x) : 1.0f;
+      }
+      if (warp == 0 && c0 < lds)
+        *reinterpret_cast<float4*>(p.scales_cols + static_cast<long long>(tile_r) * lds + c0) =
+            make_float4(s[0], s[1], s[2], s[3]);
+    }
+    // Column 4 l + e, unit `warp` (its rows 16 w ..): stored at unit w ^ (l & 7), so that the eight
+    // lanes of a 16-byte store phase reach different banks.
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        q[i] = codes4<FMT>(v[4 * i][e] * inv[e], v[4 * i + 1][e] * inv[e], v[4 * i + 2][e] * inv[e],
+                           v[4 * i + 3][e] * inv[e]);
+      sh.codes[(4 * lane + e) * 8 + (warp ^ (lane & 7))] = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+    __syncthreads();
+    const long long rp = static_cast<long long>(p.row_blocks) * kBlock;
+    const long long col0 = static_cast<long long>(tile_c) * kBlock;
+    const int unit = threadIdx.x & 7;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = (threadIdx.x >> 3) + 32 * j;
+      if (col0 + c < p.cols)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.codes_cols) + (col0 + c) * rp +
+                                  static_cast<long long>(tile_r) * kBlock + 16 * unit) =
+            sh.codes[c * 8 + (unit ^ ((c >> 2) & 7))];
+    }
+  }
+}
+
+template <typename T, int FMT>
+static cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
+  const unsigned grid = p.row_blocks * p.col_blocks;
+  const auto at = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & (4 * sizeof(T) - 1)) == 0; };
+  // Accesses of four elements where every row's groups of four are aligned and whole.
+  const bool vec = p.cols % 4 == 0 && p.ldx % 4 == 0 && at(p.x) &&
+                   (p.gate == nullptr || (p.ldg % 4 == 0 && at(p.gate)));
+  if (p.gate != nullptr) {
+    if (vec)
+      quantize_kernel<T, FMT, true, true><<<grid, kQuantThreads, 0, st>>>(p);
+    else
+      quantize_kernel<T, FMT, false, true><<<grid, kQuantThreads, 0, st>>>(p);
+  } else if (vec) {
+    quantize_kernel<T, FMT, true, false><<<grid, kQuantThreads, 0, st>>>(p);
+  } else {
+    quantize_kernel<T, FMT, false, false><<<grid, kQuantThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_quantize(const QuantParams& p, int dtype, int fmt, cudaStream_t st) {
+  if (fmt == kE4M3) {
+    if (dtype == kF32) return launch_quantize_t<float, kE4M3>(p, st);
+    if (dtype == kBF16) return launch_quantize_t<__nv_bfloat16, kE4M3>(p, st);
+    return launch_quantize_t<__half, kE4M3>(p, st);
+  }
+  if (dtype == kF32) return launch_quantize_t<float, kE5M2>(p, st);
+  if (dtype == kBF16) return launch_quantize_t<__nv_bfloat16, kE5M2>(p, st);
+  return launch_quantize_t<__half, kE5M2>(p, st);
+}
+
+}  // namespace demo

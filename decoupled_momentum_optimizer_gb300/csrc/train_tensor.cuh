@@ -1,0 +1,80 @@
+// PTX wrappers of the fifth-generation tensor cores: tensor memory, the matrix instruction on
+// 8-bit floating point, its completion barriers and its operand descriptors.
+#pragma once
+
+#include "demo_common.cuh"
+
+namespace demo {
+
+// Tensor memory: `cols` columns (a power of two, at least 32) of 128 lanes x 32 bits.  One warp
+// allocates (the address lands in shared memory) and the same warp frees.
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+
+__device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// `bar` receives one arrival when every matrix instruction this thread has issued is complete.
+__device__ __forceinline__ void tensor_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+// D (tensor memory, float32) = A B^T (+ D if accumulate), K = 32 codes; one thread issues.
+__device__ __forceinline__ void tensor_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// 32 consecutive columns of the calling warp's 32 lanes (warp w of its group of four reads lanes
+// 32 w ..): thread l receives lane l's 32 values.  tensor_wait_load() before they are used.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr));
+}
+
+// The wait takes the loaded registers as operands so that no use of them moves above it.
+__device__ __forceinline__ void tensor_wait_load(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
+// Shared-memory operand of K-major rows of 128 bytes in TMA's 128-byte swizzle: eight rows make a
+// 1024-byte unit, units follow one another (stride 1024); `addr` is 1024-byte aligned, plus 32 bytes
+// for each step of 32 codes along the row.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  constexpr uint64_t kStride = static_cast<uint64_t>(1024 >> 4) << 32;
+  constexpr uint64_t kVersion = 1ull << 46;      // descriptor version of this architecture
+  constexpr uint64_t kSwizzle128 = 2ull << 61;
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (1ull << 16) | kStride | kVersion | kSwizzle128;
+}
+
+// Instruction descriptor of kind::f8f6f4: float32 accumulators, both operands K-major.
+__host__ __device__ constexpr uint32_t f8_instruction(int a_fmt, int b_fmt, int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(a_fmt) << 7) | (static_cast<uint32_t>(b_fmt) << 10) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+}  // namespace demo

@@ -311,6 +311,93 @@ int demo_adamw_step(float* theta, int64_t n, float beta1, float beta2, float eps
                     int R, const void* const* g, int grad_dtype, float* const* m, float* const* v, uint64_t step,
                     void* stream);
 
+/*
+ * ---- Training operators: what makes the gradient the step consumes ----
+ *
+ * Dropout, matrices in 8-bit floating point with a scale for each block of 128, and their
+ * products.  They follow the conventions above (device pointers, streams, statuses, no allocation
+ * in the calls, graph capture, no floating-point atomics) except that
+ *   - a matrix argument has a row stride `ld` in elements and needs only its element's alignment
+ *     (whole 16-byte rows are faster); rows of an input may overlap or repeat (ld < cols, 0
+ *     included), rows of an output may not (DEMO_EINVAL);
+ *   - sizes may be 0: an empty result launches nothing, a sum over nothing is 0;
+ *   - non-finite inputs have defined results, given with each call.
+ */
+enum demo_dtype { DEMO_F32 = 0, DEMO_BF16 = 1, DEMO_F16 = 2 };
+
+/* 8-bit formats: e4m3 (largest 448) and e5m2 (largest 57344), both with NaN codes. */
+enum demo_fp8_format { DEMO_E4M3 = 0, DEMO_E5M2 = 1 };
+
+/*
+ * demo_dropout -- out = residual + keep x / (1 - p) on a [rows, cols] matrix, with a mask that is
+ * a function of (seed, step, site, row, column) and never stored.
+ * The step and seed are those of the shard step; `site` tells the dropouts of a model apart.
+ * With sm the splitmix64 output function and G = ceil(cols / 4):
+ *   h = sm(sm(sm(sm(seed) ^ step) ^ site) ^ (row G + col / 4)),
+ *   keep = bits 16 (col mod 4) .. 16 (col mod 4) + 15 of h >= T,   T = 65536 p to nearest even,
+ * and kept values are multiplied by 65536 / (65536 - T).
+ *   x, residual, out   [rows, cols] of dtype; residual may be NULL.  out may be x or residual
+ *                      itself (same stride), and otherwise overlaps neither (DEMO_EINVAL)
+ *   p                  0 <= p <= 1; 0 keeps everything, 1 nothing
+ * Computed in float32, rounded once.  A dropped element is 0 (plus the residual) whatever x holds.
+ * The gradient of x is the same call on the output's gradient without a residual; that of the
+ * residual is the output's gradient itself.
+ */
+int demo_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* out, int64_t ldo, int dtype,
+                 int64_t rows, int64_t cols, double p, uint64_t seed, uint64_t step, uint64_t site, void* stream);
+
+/*
+ * A quantized matrix X [rows, k]: K = ceil(k / 128) blocks along each row,
+ *   codes   uint8 [rows][128 K], zero past k
+ *   scales  float32 [K][rows rounded up to 4]
+ *   X[r][c] = value(codes[r][c]) * scales[c / 128][r]
+ * demo_fp8_bytes returns the codes' bytes and, through scale_bytes (if not NULL), the scales' (host
+ * only; 0 for negative sizes).  Both buffers are 16-byte aligned.
+ */
+size_t demo_fp8_bytes(int64_t rows, int64_t k, size_t* scale_bytes);
+
+/*
+ * demo_fp8_quantize -- quantize a [rows, cols] matrix by rows (X itself), by columns (X
+ * transposed, [cols, rows]) or both, in one pass.
+ *   v = x, then max(v, 0) if relu; dropout as demo_dropout (p = 0: none); 0 where gate <= 0 or NaN
+ *   the scale of a block of 128 along the form's rows is the smallest power of two s >= 2^-126
+ *   with max |v| <= s * (largest code of fmt), 1 for zeros; codes = v / s to nearest even
+ *   gate    [rows, cols] of the same dtype, or NULL: quantizing dy with the relu's output as gate
+ *           and the forward's dropout arguments gives the gradient at the relu's input
+ *   tiles   1: one scale per 128 x 128 tile (both forms then hold the same values)
+ *   codes_rows, scales_rows / codes_cols, scales_cols   the forms; a pair may be NULL, not both
+ * A non-finite v becomes a NaN code and does not count in its block's scale.
+ * With rows or cols 0 nothing is written.
+ */
+int demo_fp8_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, int relu, const void* gate,
+                      int64_t ldg, double p, uint64_t seed, uint64_t step, uint64_t site, int fmt, int tiles,
+                      void* codes_rows, float* scales_rows, void* codes_cols, float* scales_cols, void* stream);
+
+/*
+ * demo_fp8_matmul -- out = A B^T (out += A B^T if add, float32 only): A [m, k] and B [n, k]
+ * quantized by rows, any finite scales (demo_fp8_quantize's are powers of two).
+ *   b_tiles   1 states that B's scales are equal within each 128 rows (tiles = 1 above)
+ *   out       [m, n] of out_dtype, apart from every input
+ * Sums within a block of 128 run in the tensor core's float32 accumulator, sums over blocks in
+ * IEEE float32.  NaN codes give NaN results.  k = 0 gives zeros (or leaves out as it is, if add).
+ */
+int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,
+                    int b_fmt, int b_tiles, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                    int add, void* stream);
+
+/*
+ * demo_fp8_linear -- out = Q(x) W^T: x [m, k] of dtype, quantized by rows to e4m3 within the call
+ * (as demo_fp8_quantize does), W [n, k] quantized by rows; out [m, n] of out_dtype.  The serving
+ * form of the product: few rows of x (one token's) are quantized by the kernel that multiplies.
+ *   workspace   device, 16-byte aligned, at least demo_fp8_linear_workspace(m, n, k) bytes (host
+ *               only; 0 for few rows, then workspace may be NULL), apart from the other buffers;
+ *               fewer bytes give DEMO_ENOSPACE.  Its contents mean nothing between calls.
+ */
+size_t demo_fp8_linear_workspace(int64_t m, int64_t n, int64_t k);
+int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, const float* w_scales, int w_fmt,
+                    int w_tiles, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* demo_status_string -- a static, human-readable name for a status code. */
 const char* demo_status_string(int status);
 
