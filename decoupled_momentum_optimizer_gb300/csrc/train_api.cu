@@ -179,11 +179,11 @@ int demo_fp8_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64
 }
 
 int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,
-                    int b_fmt, int b_tiles, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                    int b_fmt, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
                     int add, void* stream) {
   if (!valid_dtype(out_dtype) || !valid_fmt(a_fmt) || !valid_fmt(b_fmt)) return DEMO_EINVAL;
   if (m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return DEMO_EINVAL;
-  if (b_tiles < 0 || b_tiles > 1 || add < 0 || add > 1 || (add && out_dtype != DEMO_F32)) return DEMO_EINVAL;
+  if (add < 0 || add > 1 || (add && out_dtype != DEMO_F32)) return DEMO_EINVAL;
   if (m == 0 || n == 0) return DEMO_OK;
   if (m > kMaxElems / n) return DEMO_EINVAL;
   int s;
@@ -201,8 +201,8 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   MatmulParams q;
   std::memset(&q, 0, sizeof(q));
   q.kb = static_cast<int>(up(k, kBlock) / kBlock);
-  if (q.kb > 0 && (!code_map(dev.encode, &q.a, a_codes, m, up(k, kBlock), 128) ||
-                   !code_map(dev.encode, &q.b, b_codes, n, up(k, kBlock), 256)))
+  if (q.kb > 0 && (!code_map(dev.encode, &q.a, a_codes, m, up(k, kBlock), matmul_box_rows(false)) ||
+                   !code_map(dev.encode, &q.b, b_codes, n, up(k, kBlock), matmul_box_rows(true))))
     return DEMO_ECUDA;
   q.a_scales = a_scales;
   q.b_scales = b_scales;
@@ -212,7 +212,6 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   q.out = out;
   q.out_dtype = out_dtype;
   q.add = add;
-  q.b_tiles = b_tiles;
   q.a_fmt = a_fmt;
   q.b_fmt = b_fmt;
   q.fault = dev.fault;
@@ -225,11 +224,10 @@ size_t demo_fp8_linear_workspace(int64_t m, int64_t n, int64_t k) {
 }
 
 int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, const float* w_scales, int w_fmt,
-                    int w_tiles, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                    int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
                     void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_dtype(dtype) || !valid_dtype(out_dtype) || !valid_fmt(w_fmt)) return DEMO_EINVAL;
   if (m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return DEMO_EINVAL;
-  if (w_tiles < 0 || w_tiles > 1) return DEMO_EINVAL;
   if (m == 0 || n == 0) return DEMO_OK;
   if (m > kMaxElems / n || (k > 0 && m > kMaxElems / up(k, kBlock))) return DEMO_EINVAL;
   int s;
@@ -254,7 +252,7 @@ int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, 
   if (k > 0 && (s = demo_fp8_quantize(x, ldx, dtype, m, k, 0, nullptr, 0, 0.0, 0, 0, 0, DEMO_E4M3, 0, codes, scales,
                                       nullptr, nullptr, stream)) != DEMO_OK)
     return s;
-  return demo_fp8_matmul(codes, scales, DEMO_E4M3, w_codes, w_scales, w_fmt, w_tiles, m, n, k, out, ldo, out_dtype, 0,
+  return demo_fp8_matmul(codes, scales, DEMO_E4M3, w_codes, w_scales, w_fmt, m, n, k, out, ldo, out_dtype, 0,
                          stream);
 }
 

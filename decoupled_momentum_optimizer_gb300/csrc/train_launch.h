@@ -68,11 +68,13 @@ struct MatmulParams {
   int kb;  // blocks of 128 along k, may be 0
   long long ldo;
   void* out;
-  int out_dtype, add, b_tiles;
+  int out_dtype, add;
   int a_fmt, b_fmt;
   unsigned int* fault;
 };
 
+// Rows of the tensor maps' boxes.
+int matmul_box_rows(bool b);
 cudaError_t launch_matmul(const MatmulParams& p, int sms, cudaStream_t st);
 cudaError_t prepare_matmul_kernels();
 

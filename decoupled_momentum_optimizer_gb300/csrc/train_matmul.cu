@@ -1,14 +1,17 @@
-// Product of two matrices in 8-bit floating point with a scale for each block of 128 along k:
+// Product of two matrices in 8-bit floating point with a power-of-two scale for each block of 128
+// along k:
 //
 //   out[m][n] (+)= sum over blocks b of sa[b][m] sb[b][n] * (sum over k in block b of a[m][k] b[n][k])
 //
-// A CTA computes a 128 x 256 tile.  TMA brings 128 codes of k of both operands into a ring of
-// shared-memory stages; one thread issues four K = 32 tensor-core instructions per block into one
-// of two halves of tensor memory; eight warps meanwhile read the other half, apply the block's
-// scales and add it to float32 accumulators in registers.  So every sum that passes a block is an
-// IEEE float32 multiply-add, and the tensor core's own accumulator only ever holds 128 products.
-// Scales travel through a ring of their own, so that a stage of codes is free as soon as the tensor
-// core has read it.
+// A CTA computes a 128 x 224 tile.  TMA brings 128 codes of k of both operands into a ring of
+// shared-memory stages; four warps write the block's scales to tensor memory as UE8M0 bytes; one
+// thread issues four K = 32 block-scaled tensor-core instructions per block.  Four blocks run into one
+// of two halves of tensor memory, and eight warps meanwhile add the other half to float32 sums in
+// registers, so the tensor core's accumulator holds 512 products at most and every longer sum is an
+// IEEE float32 addition: its own additions drop low bits, and over a whole k of thousands that
+// showed.  (Scales in the instruction instead of in the sums: with a multiply-add per element and
+// block in the eight warps, 8192 x 2048 x 8192 took 170 us, and 250 us with a scale per row of b.)
+// 224 columns leave room in tensor memory for two halves and the scales of four stages.
 #include "train_common.cuh"
 #include "train_tensor.cuh"
 
@@ -16,26 +19,28 @@ namespace demo {
 
 namespace {
 
-constexpr int kBM = 128, kBN = 256;
-constexpr int kStages = 4, kScaleSlots = 8;
-constexpr int kPromoteWarps = 8;
-// Two groups of four warps that add up, and one whose first two warps load and multiply.  Launched
-// with 168 registers a thread; the last group gives up what the others' accumulators need:
-// 256 * 216 + 128 * 72 = 384 * 168.
-constexpr int kThreads = 32 * (kPromoteWarps + 4);
-constexpr int kPromoteRegs = 216, kFeedRegs = 72;
-static_assert(256 * kPromoteRegs + 128 * kFeedRegs == kThreads * 168, "the launch's registers");
-constexpr uint32_t kTmemCols = 2 * kBN;
+constexpr int kBM = 128, kBN = 224;
+constexpr int kStages = 4;
+constexpr int kChain = 4;  // blocks of 128 that one half of tensor memory sums
+constexpr int kSumWarps = 8, kScaleWarps = 4;
+constexpr int kLoadWarp = kSumWarps + kScaleWarps, kMmaWarp = kLoadWarp + 1;
+// Whole groups of four warps, launched with 128 registers a thread: the summing ones take 192, the
+// others keep 64.
+constexpr int kThreads = 512;
+constexpr int kSumRegs = 192, kFeedRegs = 64;
+static_assert(256 * kSumRegs + 256 * kFeedRegs == kThreads * 128, "the launch's registers");
+constexpr uint32_t kTmemCols = 512;
+// Scales of stage i: 4 columns of a's (one for 32 rows) and 8 of b's (7 used).
+constexpr uint32_t kScaleCol = 2 * kBN, kScaleCols = 12;
+static_assert(kScaleCol + kStages * kScaleCols <= kTmemCols, "tensor memory");
 constexpr uint32_t kABytes = kBM * kBlock, kBBytes = kBN * kBlock;
+constexpr int kCols = kBN / 2;  // columns of a summing warp
 
 struct Shared {
   uint8_t a[kStages][kABytes];  // 1024-byte aligned (swizzle atoms)
   uint8_t b[kStages][kBBytes];
-  float sa[kScaleSlots][kBM];
-  float sb[kScaleSlots][kBN];
-  uint4 out[kPromoteWarps][128];  // a warp's 32 rows x 64 bytes on their way out
-  uint64_t full[kStages], empty[kStages];
-  uint64_t sfull[kScaleSlots], sempty[kScaleSlots];
+  uint4 out[kSumWarps][128];  // a warp's 32 rows x 64 bytes on their way out
+  uint64_t full[kStages], empty[kStages], scaled[kStages];
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem;
@@ -109,20 +114,21 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// A warp's 32 rows (lane l holds row l) x 128 columns to out[m0 ..][n0 ..], 64 bytes of every row at
+// A warp's 32 rows (lane l holds row l) x kCols columns to out[m0 ..][n0 ..], 64 bytes of every row at
 // a time through 2 KB of shared memory: written a row per lane, read back as 8 rows x 4 units, so
 // that every store covers whole 32-byte sectors.  Unit u of row r is stored at u ^ ((r >> 1) & 3):
 // two rows span the banks once, so eight lanes of either access reach different ones.
 template <typename T, bool ADD>
-__device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint64_t (&sum)[64], const MatmulParams& p,
-                                           long long m0, long long n0) {
+__device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint64_t (&sum)[kCols / 2],
+                                           const MatmulParams& p, long long m0, long long n0) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const bool vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % E == 0;
 #pragma unroll
-  for (int c = 0; c < 128; c += 4 * E) {
+  for (int c = 0; c < kCols; c += 4 * E) {
     if (n0 + c >= p.n) break;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
+      if (c + u * E >= kCols) break;
       float v[E];
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
@@ -138,7 +144,7 @@ __device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint64_t 
       const int r = 8 * q + (lane >> 2), u = lane & 3;
       uint4 w = buf[r * 4 + (u ^ ((r >> 1) & 3))];
       const long long m = m0 + r, n = n0 + c + u * E;
-      if (m < p.m && n < p.n) {
+      if (m < p.m && n < p.n && c + u * E < kCols) {
         T* o = static_cast<T*>(p.out) + m * p.ldo + n;
         if (vec && n + E <= p.n) {
           if constexpr (ADD) {
@@ -160,8 +166,51 @@ __device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint64_t 
 
 }  // namespace
 
-// TILES: b's scales are equal within each 128 rows, that is for all columns of a promoting warp.
-template <bool TILES>
+// A power of two's exponent byte in all four bytes.
+__device__ __forceinline__ uint32_t scale_word(float s) { return ((__float_as_uint(s) >> 23) & 0xffu) * 0x01010101u; }
+
+// The scales of a CTA's blocks in order, tile after tile: lane l reads rows 32 c + l of the tile.
+struct ScaleStream {
+  static constexpr int kA = kBM / 32, kB = kBN / 32, kWords = kA + kB;
+  const MatmulParams& p;
+  long long lda, ldb, t, tiles;
+  int lane, tiles_m, tiles_n, kb = 0;
+  const float *pa, *pb;
+  int ra, rb;  // rows left from this lane's first one
+
+  __device__ __forceinline__ ScaleStream(const MatmulParams& q, int l, int tm, int tn)
+      : p(q), lda((q.m + 3) / 4 * 4), ldb((q.n + 3) / 4 * 4), t(blockIdx.x), tiles(static_cast<long long>(tm) * tn),
+        lane(l), tiles_m(tm), tiles_n(tn) {
+    if (p.kb == 0) t = tiles;
+    start();
+  }
+  __device__ __forceinline__ long long blocks(long long n) const {
+    return blockIdx.x < n ? ((n - 1 - blockIdx.x) / gridDim.x + 1) * p.kb : 0;
+  }
+  __device__ __forceinline__ void start() {
+    if (t >= tiles) return;
+    const Tile tl = tile_at(t, tiles_m, tiles_n);
+    pa = p.a_scales + tl.m0 + lane;
+    pb = p.b_scales + tl.n0 + lane;
+    ra = static_cast<int>(p.m - tl.m0 < kBM ? p.m - tl.m0 : kBM) - lane;
+    rb = static_cast<int>(p.n - tl.n0 < kBN ? p.n - tl.n0 : kBN) - lane;
+  }
+  __device__ __forceinline__ void fetch(float* w) {
+    if (t >= tiles) return;
+#pragma unroll
+    for (int c = 0; c < kA; ++c) w[c] = 32 * c < ra ? pa[32 * c] : 1.0f;
+#pragma unroll
+    for (int c = 0; c < kB; ++c) w[kA + c] = 32 * c < rb ? pb[32 * c] : 1.0f;
+    pa += lda;
+    pb += ldb;
+    if (++kb == p.kb) {
+      kb = 0;
+      t += gridDim.x;
+      start();
+    }
+  }
+};
+
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ MatmulParams p) {
   extern __shared__ uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -174,39 +223,59 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(&s.sfull[i], 1);
-      mbar_init(&s.sempty[i], kPromoteWarps);
+      mbar_init(&s.scaled[i], kScaleWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
-      mbar_init(&s.tempty[i], kPromoteWarps);
+      mbar_init(&s.tempty[i], kSumWarps);
     }
     mbar_init(&s.drain, 1);
     s.dead = 0;
     fence_mbar_init();
   }
-  if (warp == kPromoteWarps + 1) tmem_alloc(&s.tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc(&s.tmem, kTmemCols);
   tensor_fence_before();
   __syncthreads();
   tensor_fence_after();
   const uint32_t tmem = s.tmem;
-  const uint32_t idesc = f8_instruction(p.a_fmt, p.b_fmt, kBM, kBN);
 
-  if (warp >= kPromoteWarps) {
+  if (warp >= kSumWarps) {
     registers_down<kFeedRegs>();
-    if (warp == kPromoteWarps && lane == 0) {
-      // ---- loads ----
-      const long long lda = (p.m + 3) / 4 * 4, ldb = (p.n + 3) / 4 * 4;  // strides of the scales
+    if (warp < kLoadWarp) {
+      // ---- scales: warp w writes lanes 32 w .. of every column; column c of an operand holds the
+      // words of its rows 32 c .. 32 c + 31, the same in all four groups of 32 lanes ----
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp - kSumWarps)) << 16) + kScaleCol;
+      ScaleStream in(p, lane, tiles_m, tiles_n);
       Ring<kStages> st;
-      Ring<kScaleSlots> sc;
+      float next[2][ScaleStream::kWords];  // two blocks ahead: further than a read from L2 takes
+      in.fetch(next[0]);
+      in.fetch(next[1]);
+      for (long long left = in.blocks(tiles); left > 0; --left) {
+        uint32_t w[12];
+#pragma unroll
+        for (int c = 0; c < ScaleStream::kWords; ++c) {
+          w[c] = scale_word(next[0][c]);
+          next[0][c] = next[1][c];
+        }
+        w[11] = 0;
+        in.fetch(next[1]);
+        if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
+        tensor_fence_after();
+        tmem_store4(taddr + st.slot * kScaleCols, w);
+        tmem_store8(taddr + st.slot * kScaleCols + 4, w + 4);
+        tensor_wait_store();
+        tensor_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.scaled[st.slot]);
+        st.next();
+      }
+    } else if (warp == kLoadWarp && lane == 0) {
+      // ---- loads ----
+      Ring<kStages> st;
       uint32_t used = 0;  // stages that have been loaded at least once
       bool ok = true;
       for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const Tile tl = tile_at(t, tiles_m, tiles_n);
-        const uint32_t na = static_cast<uint32_t>(lda - tl.m0 < kBM ? lda - tl.m0 : kBM) * 4;
-        const uint32_t nb = static_cast<uint32_t>(ldb - tl.n0 < kBN ? ldb - tl.n0 : kBN) * 4;
         for (int kb = 0; kb < p.kb; ++kb) {
           if (!(ok = wait_or_dead(s, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
           mbar_expect_tx(&s.full[st.slot], kABytes + kBBytes);
@@ -214,92 +283,76 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           tma_load_2d(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0);
           used |= 1u << st.slot;
           st.next();
-          if (!(ok = wait_or_dead(s, &s.sempty[sc.slot], sc.phase ^ 1u, p.fault))) break;
-          mbar_expect_tx(&s.sfull[sc.slot], na + nb);
-          bulk_load(s.sa[sc.slot], p.a_scales + kb * lda + tl.m0, na, &s.sfull[sc.slot]);
-          bulk_load(s.sb[sc.slot], p.b_scales + kb * ldb + tl.n0, nb, &s.sfull[sc.slot]);
-          used |= 1u << (kStages + sc.slot);
-          sc.next();
         }
       }
       // Stopped early: copies may be in flight into this CTA's shared memory.  Wait (bounded) for
-      // the last load of every slot: the slots before the ring's position are in its current phase,
-      // the others in the one before.
+      // the last load of every stage: the stages before the ring's position are in its current
+      // phase, the others in the one before.
       if (!ok) {
         for (int i = 0; i < kStages; ++i)
           if (used >> i & 1u) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
-        for (int i = 0; i < kScaleSlots; ++i)
-          if (used >> (kStages + i) & 1u) mbar_wait_bounded(&s.sfull[i], i < sc.slot ? sc.phase : sc.phase ^ 1u);
       }
-    }
-    if (warp == kPromoteWarps + 1 && lane == 0) {
+    } else if (warp == kMmaWarp && lane == 0) {
       // ---- tensor-core instructions ----
+      const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, kBM, kBN);
       Ring<kStages> st;
       Ring<2> acc;
       bool ok = true;
       for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         for (int kb = 0; kb < p.kb; ++kb) {
-          if (!(ok = wait_or_dead(s, &s.tempty[acc.slot], acc.phase ^ 1u, p.fault))) break;
+          const bool first = kb % kChain == 0;
+          if (first && !(ok = wait_or_dead(s, &s.tempty[acc.slot], acc.phase ^ 1u, p.fault))) break;
+          if (!(ok = wait_or_dead(s, &s.scaled[st.slot], st.phase, p.fault))) break;
           if (!(ok = wait_or_dead(s, &s.full[st.slot], st.phase, p.fault))) break;
           tensor_fence_after();
           const uint64_t da = operand_desc(smem_addr(s.a[st.slot])), db = operand_desc(smem_addr(s.b[st.slot]));
+          const uint32_t sf = tmem + kScaleCol + st.slot * kScaleCols;
 #pragma unroll
           for (int k = 0; k < kBlock / 32; ++k)  // 32 bytes along the swizzled row: 2 units of 16
-            tensor_mma_f8(tmem + acc.slot * kBN, da + 2 * k, db + 2 * k, idesc, k > 0);
+            tensor_mma_mxf8(tmem + acc.slot * kBN, da + 2 * k, db + 2 * k, idesc, sf, sf + 4, !first || k > 0);
           tensor_commit(&s.empty[st.slot]);
-          tensor_commit(&s.tfull[acc.slot]);
           st.next();
-          acc.next();
+          if (kb % kChain == kChain - 1 || kb == p.kb - 1) {
+            tensor_commit(&s.tfull[acc.slot]);
+            acc.next();
+          }
         }
       }
     }
   } else {
-    registers_up<kPromoteRegs>();
-    // ---- scales and float32 sums: warp w holds rows 32 (w & 3) .., columns 128 (w >> 2) .. ----
-    const int row = 32 * (warp & 3) + lane;
-    const int col0 = kBN / 2 * (warp >> 2);
+    registers_up<kSumRegs>();
+    // ---- float32 sums: warp w holds rows 32 (w & 3) .., columns kCols (w >> 2) .. ----
+    const int col0 = kCols * (warp >> 2);
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + col0;
-    Ring<kScaleSlots> sc;
     Ring<2> acc;
     bool ok = true;
     for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const Tile tl = tile_at(t, tiles_m, tiles_n);
-      uint64_t sum[kBN / 4];  // pairs of columns
+      uint64_t sum[kCols / 2];  // pairs of columns
 #pragma unroll
-      for (int i = 0; i < kBN / 4; ++i) sum[i] = 0;
-      for (int kb = 0; kb < p.kb; ++kb) {
+      for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
+      for (int kb = 0; kb < p.kb; kb += kChain) {
         // every lane waits (each reads what the barrier guards); the warp goes on or stops as one
-        if (!(ok = __all_sync(0xffffffffu, wait_or_dead(s, &s.sfull[sc.slot], sc.phase, p.fault)))) break;
-        const float scale = TILES ? s.sa[sc.slot][row] * s.sb[sc.slot][col0] : s.sa[sc.slot][row];
-        const uint64_t scale2 = pack2(scale, scale);
-        if (!(ok = __all_sync(0xffffffffu, wait_or_dead(s, &s.tfull[acc.slot], acc.phase, p.fault)))) break;
+        ok = __all_sync(0xffffffffu, wait_or_dead(s, &s.tfull[acc.slot], acc.phase, p.fault));
+        if (!ok) break;
         tensor_fence_after();
+        // 16 columns at a time, the next ones on their way while these are added
+        uint32_t v[2][16];
+        tmem_load16(taddr + acc.slot * kBN, v[0]);
 #pragma unroll
-        for (int c = 0; c < kBN / 2; c += 32) {
-          uint32_t v[32];
-          tmem_load32(taddr + acc.slot * kBN + c, v);
-          tensor_wait_load(v);
-          if constexpr (TILES) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[c / 2 + j] = fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, sum[c / 2 + j]);
+        for (int c = 0; c < kCols / 16; ++c) {
+          tensor_wait_load(v[c & 1]);
+          if (c + 1 < kCols / 16) {
+            tmem_load16(taddr + acc.slot * kBN + 16 * (c + 1), v[(c + 1) & 1]);
           } else {
-            const ulonglong2* sb = reinterpret_cast<const ulonglong2*>(&s.sb[sc.slot][col0 + c]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const ulonglong2 q = sb[j];
-              sum[c / 2 + 2 * j] = fma2(mul2(pack2(v[4 * j], v[4 * j + 1]), q.x), scale2, sum[c / 2 + 2 * j]);
-              sum[c / 2 + 2 * j + 1] =
-                  fma2(mul2(pack2(v[4 * j + 2], v[4 * j + 3]), q.y), scale2, sum[c / 2 + 2 * j + 1]);
-            }
+            tensor_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.tempty[acc.slot]);
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sum[8 * c + j] = add2(sum[8 * c + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]));
         }
-        tensor_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s.tempty[acc.slot]);
-          mbar_arrive(&s.sempty[sc.slot]);
-        }
-        sc.next();
         acc.next();
       }
       if (!ok) break;
@@ -319,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   }
   tensor_fence_before();
   __syncthreads();
-  if (warp == kPromoteWarps + 1) {
+  if (warp == kMmaWarp) {
     // A CTA that stopped early may have matrix instructions in flight: wait (bounded) for them.
     if (s.dead && lane == 0) {
       tensor_commit(&s.drain);
@@ -331,22 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   }
 }
 
+int matmul_box_rows(bool b) { return b ? kBN : kBM; }
+
 cudaError_t launch_matmul(const MatmulParams& p, int sms, cudaStream_t st) {
   const long long tiles = ((p.m + kBM - 1) / kBM) * ((p.n + kBN - 1) / kBN);
-  const unsigned grid = static_cast<unsigned>(tiles < sms ? tiles : sms);
-  if (p.b_tiles)
-    matmul_kernel<true><<<grid, kThreads, kSmem, st>>>(p);
-  else
-    matmul_kernel<false><<<grid, kThreads, kSmem, st>>>(p);
+  matmul_kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kThreads, kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t prepare_matmul_kernels() {
-  const cudaError_t e = cudaFuncSetAttribute(matmul_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kSmem));
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(matmul_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kSmem));
+  return cudaFuncSetAttribute(matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
 }
 
 }  // namespace demo

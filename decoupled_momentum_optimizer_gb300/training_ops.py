@@ -191,8 +191,7 @@ def fp8_matmul(a, b, *, out=None, dtype=None, add=False, stream=None):
         op, ldo, _, _, dt = _matrix(out, "out", shape=(m, n))
         dm._check(dm.lib().demo_fp8_matmul(a.codes.data_ptr(), a.scales.data_ptr(), _FMT_OF[a.codes.dtype],
                                            b.codes.data_ptr(), b.scales.data_ptr(), _FMT_OF[b.codes.dtype],
-                                           int(b.tiles), m, n, k, op, ldo, dt, int(bool(add)),
-                                           dm._stream(stream, d.index)), "demo_fp8_matmul")
+                                           m, n, k, op, ldo, dt, int(bool(add)), dm._stream(stream, d.index)), "demo_fp8_matmul")
     return out
 
 
@@ -222,7 +221,7 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
         if need and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != x.device):
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
         dm._check(dm.lib().demo_fp8_linear(xp, ldx, dt, w.codes.data_ptr(), w.scales.data_ptr(), _FMT_OF[w.codes.dtype],
-                                           int(w.tiles), m, n, k, op, ldo, odt, wp, wn,
+                                           m, n, k, op, ldo, odt, wp, wn,
                                            dm._stream(stream, d.index)), "demo_fp8_linear")
     return out
 
@@ -234,9 +233,9 @@ SIGS = {
     "demo_fp8_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, ctypes.POINTER(ctypes.c_size_t)]),
     "demo_fp8_quantize": (_c_int, [_c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_f64, _c_u64,
                                    _c_u64, _c_u64, _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
-    "demo_fp8_matmul": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_int, _c_i64, _c_i64, _c_i64, _c_vp,
-                                 _c_i64, _c_int, _c_int, _c_vp]),
+    "demo_fp8_matmul": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
+                                 _c_int, _c_int, _c_vp]),
     "demo_fp8_linear_workspace": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
-    "demo_fp8_linear": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_int, _c_int, _c_i64, _c_i64, _c_i64, _c_vp,
-                                 _c_i64, _c_int, _c_vp, ctypes.c_size_t, _c_vp]),
+    "demo_fp8_linear": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
+                                 _c_int, _c_vp, ctypes.c_size_t, _c_vp]),
 }

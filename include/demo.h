@@ -375,14 +375,13 @@ int demo_fp8_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64
 
 /*
  * demo_fp8_matmul -- out = A B^T (out += A B^T if add, float32 only): A [m, k] and B [n, k]
- * quantized by rows, any finite scales (demo_fp8_quantize's are powers of two).
- *   b_tiles   1 states that B's scales are equal within each 128 rows (tiles = 1 above)
+ * quantized by rows.  The scales are powers of two from 2^-126 to 2^127, as demo_fp8_quantize
+ * writes them: the tensor core applies them (only a scale's exponent is read).
  *   out       [m, n] of out_dtype, apart from every input
- * Sums within a block of 128 run in the tensor core's float32 accumulator, sums over blocks in
- * IEEE float32.  NaN codes give NaN results.  k = 0 gives zeros (or leaves out as it is, if add).
+ * Sums over 512 of k run in the tensor core's float32 accumulator, longer ones in IEEE float32.  NaN codes give NaN results.  k = 0 gives zeros (or leaves out as it is, if add).
  */
 int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,
-                    int b_fmt, int b_tiles, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                    int b_fmt, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
                     int add, void* stream);
 
 /*
@@ -395,7 +394,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
  */
 size_t demo_fp8_linear_workspace(int64_t m, int64_t n, int64_t k);
 int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, const float* w_scales, int w_fmt,
-                    int w_tiles, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                    int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* demo_status_string -- a static, human-readable name for a status code. */

@@ -98,16 +98,16 @@ def test_quantize_refusals(L):
 
 
 def matmul(L, **kw):
-    a = dict(ac=p(0x1000000), asc=p(0x2000000), af=0, bc=p(0x3000000), bsc=p(0x4000000), bf=1, bt=0, m=100, n=200, k=300,
+    a = dict(ac=p(0x1000000), asc=p(0x2000000), af=0, bc=p(0x3000000), bsc=p(0x4000000), bf=1, m=100, n=200, k=300,
              out=p(0x5000000), ldo=200, dtype=0, add=0)
     a.update(kw)
-    return L.demo_fp8_matmul(a["ac"], a["asc"], a["af"], a["bc"], a["bsc"], a["bf"], a["bt"], a["m"], a["n"], a["k"],
-                             a["out"], a["ldo"], a["dtype"], a["add"], None)
+    return L.demo_fp8_matmul(a["ac"], a["asc"], a["af"], a["bc"], a["bsc"], a["bf"], a["m"], a["n"], a["k"], a["out"],
+                            , a["ldo"], a["dtype"], a["add"], None)
 
 
 def test_matmul_refusals(L):
     assert matmul(L) in NODEV and matmul(L, add=1) in NODEV
-    for bad in (dict(af=2), dict(bf=-1), dict(bt=2), dict(m=-1), dict(k=-1), dict(n=1 << 31), dict(m=1 << 30, n=1 << 30),
+    for bad in (dict(af=2), dict(bf=-1), dict(m=-1), dict(k=-1), dict(n=1 << 31), dict(m=1 << 30, n=1 << 30),
                 dict(add=2), dict(add=1, dtype=1), dict(dtype=3), dict(ac=None), dict(bsc=None), dict(out=None),
                 dict(ldo=199), dict(out=p(0x1000000)), dict(out=p(0x2000000)), dict(out=p(0x3000010)),
                 dict(out=p(0x4000000 - 16))):
@@ -120,18 +120,18 @@ def test_matmul_refusals(L):
 
 
 def linear(L, **kw):
-    a = dict(x=p(0x100000), ldx=300, dtype=1, wc=p(0x3000000), ws=p(0x4000000), wf=0, wt=1, m=700, n=200, k=300,
+    a = dict(x=p(0x100000), ldx=300, dtype=1, wc=p(0x3000000), ws=p(0x4000000), wf=0, m=700, n=200, k=300,
              out=p(0x5000000), ldo=200, od=1, work=p(0x6000000), bytes=None)
     a.update(kw)
     if a["bytes"] is None:
         a["bytes"] = L.demo_fp8_linear_workspace(a["m"], a["n"], a["k"])
-    return L.demo_fp8_linear(a["x"], a["ldx"], a["dtype"], a["wc"], a["ws"], a["wf"], a["wt"], a["m"], a["n"], a["k"],
+    return L.demo_fp8_linear(a["x"], a["ldx"], a["dtype"], a["wc"], a["ws"], a["wf"], a["m"], a["n"], a["k"],
                              a["out"], a["ldo"], a["od"], a["work"], a["bytes"], None)
 
 
 def test_linear_refusals(L):
     assert linear(L) in NODEV
-    for bad in (dict(dtype=3), dict(od=-1), dict(wf=2), dict(wt=2), dict(m=-1), dict(k=1 << 31), dict(x=None),
+    for bad in (dict(dtype=3), dict(od=-1), dict(wf=2), dict(m=-1), dict(k=1 << 31), dict(x=None),
                 dict(wc=None), dict(ws=None), dict(out=None), dict(work=None), dict(ldo=100), dict(ldx=-1),
                 dict(out=p(0x100000)), dict(work=p(0x100000)), dict(work=p(0x5000000)), dict(work=p(0x3000000)),
                 dict(m=1 << 30, n=1 << 20)):
