@@ -4,14 +4,14 @@
 //   out[m][n] (+)= sum over blocks b of sa[b][m] sb[b][n] * (sum over k in block b of a[m][k] b[n][k])
 //
 // A CTA computes a 128 x 224 tile.  TMA brings 128 codes of k of both operands into a ring of
-// shared-memory stages; four warps write the block's scales to tensor memory as UE8M0 bytes; one
-// thread issues four K = 32 block-scaled tensor-core instructions per block.  Four blocks run into one
-// of two halves of tensor memory, and eight warps meanwhile add the other half to float32 sums in
+// shared-memory stages; four warps pack the scales of four blocks into a 32-bit word per row (UE8M0
+// bytes), which the tensor core copies to tensor memory; one thread issues four K = 32 block-scaled
+// tensor-core instructions per block.  Four blocks run into one of two halves of tensor memory, and eight warps meanwhile add the other half to float32 sums in
 // registers, so the tensor core's accumulator holds 512 products at most and every longer sum is an
 // IEEE float32 addition: its own additions drop low bits, and over a whole k of thousands that
 // showed.  (Scales in the instruction instead of in the sums: with a multiply-add per element and
 // block in the eight warps, 8192 x 2048 x 8192 took 170 us, and 250 us with a scale per row of b.)
-// 224 columns leave room in tensor memory for two halves and the scales of four stages.
+// 224 columns leave room in tensor memory for two halves and their scales.
 #include "train_common.cuh"
 #include "train_tensor.cuh"
 
@@ -30,9 +30,11 @@ constexpr int kThreads = 512;
 constexpr int kSumRegs = 192, kFeedRegs = 64;
 static_assert(256 * kSumRegs + 256 * kFeedRegs == kThreads * 128, "the launch's registers");
 constexpr uint32_t kTmemCols = 512;
-// Scales of stage i: 4 columns of a's (one for 32 rows) and 8 of b's (7 used).
+// Scale words of a half: 4 columns of a's (one for 32 rows) and 8 of b's (7 used).
 constexpr uint32_t kScaleCol = 2 * kBN, kScaleCols = 12;
-static_assert(kScaleCol + kStages * kScaleCols <= kTmemCols, "tensor memory");
+static_assert(kScaleCol + 2 * kScaleCols <= kTmemCols, "tensor memory");
+constexpr int kScaleSlots = 4;  // chains whose words are ready in shared memory
+static_assert(kChain == 4, "a word holds the scales of a chain");
 constexpr uint32_t kABytes = kBM * kBlock, kBBytes = kBN * kBlock;
 constexpr int kCols = kBN / 2;  // columns of a summing warp
 
@@ -40,7 +42,11 @@ struct Shared {
   uint8_t a[kStages][kABytes];  // 1024-byte aligned (swizzle atoms)
   uint8_t b[kStages][kBBytes];
   uint4 out[kSumWarps][128];  // a warp's 32 rows x 64 bytes on their way out
-  uint64_t full[kStages], empty[kStages], scaled[kStages];
+  // Scale words: row 32 c + l of an operand at [l][c] of its 512-byte unit of 128 rows (a's, then
+  // b's two), as the tensor core's copy wants them.
+  uint32_t words[kScaleSlots][3][32][4];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t scaled[kScaleSlots], sfree[kScaleSlots];
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem;
@@ -166,50 +172,59 @@ __device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint64_t 
 
 }  // namespace
 
-// A power of two's exponent byte in all four bytes.
-__device__ __forceinline__ uint32_t scale_word(float s) { return ((__float_as_uint(s) >> 23) & 0xffu) * 0x01010101u; }
-
-// The scales of a CTA's blocks in order, tile after tile: lane l reads rows 32 c + l of the tile.
+// A CTA's chains in order, tile after tile: the scales of up to four blocks of three rows, row
+// 32 w + l of a's tile (warp w, lane l) and rows 32 w + l and 128 + 32 w + l of b's.
 struct ScaleStream {
-  static constexpr int kA = kBM / 32, kB = kBN / 32, kWords = kA + kB;
   const MatmulParams& p;
   long long lda, ldb, t, tiles;
-  int lane, tiles_m, tiles_n, kb = 0;
+  int row, tiles_m, tiles_n, kb = 0;
   const float *pa, *pb;
-  int ra, rb;  // rows left from this lane's first one
+  bool in_a, in_b0, in_b1;  // whether the rows exist
 
-  __device__ __forceinline__ ScaleStream(const MatmulParams& q, int l, int tm, int tn)
+  __device__ __forceinline__ ScaleStream(const MatmulParams& q, int r, int tm, int tn)
       : p(q), lda((q.m + 3) / 4 * 4), ldb((q.n + 3) / 4 * 4), t(blockIdx.x), tiles(static_cast<long long>(tm) * tn),
-        lane(l), tiles_m(tm), tiles_n(tn) {
+        row(r), tiles_m(tm), tiles_n(tn) {
     if (p.kb == 0) t = tiles;
     start();
-  }
-  __device__ __forceinline__ long long blocks(long long n) const {
-    return blockIdx.x < n ? ((n - 1 - blockIdx.x) / gridDim.x + 1) * p.kb : 0;
   }
   __device__ __forceinline__ void start() {
     if (t >= tiles) return;
     const Tile tl = tile_at(t, tiles_m, tiles_n);
-    pa = p.a_scales + tl.m0 + lane;
-    pb = p.b_scales + tl.n0 + lane;
-    ra = static_cast<int>(p.m - tl.m0 < kBM ? p.m - tl.m0 : kBM) - lane;
-    rb = static_cast<int>(p.n - tl.n0 < kBN ? p.n - tl.n0 : kBN) - lane;
+    pa = p.a_scales + tl.m0 + row;
+    pb = p.b_scales + tl.n0 + row;
+    in_a = tl.m0 + row < p.m;
+    in_b0 = tl.n0 + row < p.n;
+    in_b1 = 128 + row < kBN && tl.n0 + 128 + row < p.n;
   }
-  __device__ __forceinline__ void fetch(float* w) {
-    if (t >= tiles) return;
+  // Returns false past the last chain.
+  __device__ __forceinline__ bool fetch(float (&v)[3][4]) {
+    if (t >= tiles) return false;
 #pragma unroll
-    for (int c = 0; c < kA; ++c) w[c] = 32 * c < ra ? pa[32 * c] : 1.0f;
-#pragma unroll
-    for (int c = 0; c < kB; ++c) w[kA + c] = 32 * c < rb ? pb[32 * c] : 1.0f;
-    pa += lda;
-    pb += ldb;
-    if (++kb == p.kb) {
+    for (int j = 0; j < 4; ++j) {
+      const bool in = kb + j < p.kb;
+      v[0][j] = in && in_a ? pa[j * lda] : 1.0f;
+      v[1][j] = in && in_b0 ? pb[j * ldb] : 1.0f;
+      v[2][j] = in && in_b1 ? pb[j * ldb + 128] : 1.0f;
+    }
+    pa += 4 * lda;
+    pb += 4 * ldb;
+    kb += 4;
+    if (kb >= p.kb) {
       kb = 0;
       t += gridDim.x;
       start();
     }
+    return true;
   }
 };
+
+// The exponent bytes of four powers of two.
+__device__ __forceinline__ uint32_t scale_word(const float (&v)[4]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w |= ((__float_as_uint(v[j]) >> 23) & 0xffu) << (8 * j);
+  return w;
+}
 
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ MatmulParams p) {
   extern __shared__ uint8_t raw[];
@@ -223,7 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(&s.scaled[i], kScaleWarps);
+      mbar_init(&s.sfree[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
@@ -242,32 +260,19 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   if (warp >= kSumWarps) {
     registers_down<kFeedRegs>();
     if (warp < kLoadWarp) {
-      // ---- scales: warp w writes lanes 32 w .. of every column; column c of an operand holds the
-      // words of its rows 32 c .. 32 c + 31, the same in all four groups of 32 lanes ----
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp - kSumWarps)) << 16) + kScaleCol;
-      ScaleStream in(p, lane, tiles_m, tiles_n);
-      Ring<kStages> st;
-      float next[2][ScaleStream::kWords];  // two blocks ahead: further than a read from L2 takes
-      in.fetch(next[0]);
-      in.fetch(next[1]);
-      for (long long left = in.blocks(tiles); left > 0; --left) {
-        uint32_t w[12];
+      // ---- scales, a chain ahead of the slot that waits to be free ----
+      const int w = warp - kSumWarps;
+      ScaleStream in(p, 32 * w + lane, tiles_m, tiles_n);
+      Ring<kScaleSlots> sc;
+      float v[3][4];
+      while (in.fetch(v)) {
+        if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.sfree[sc.slot], sc.phase ^ 1u, p.fault))) break;
 #pragma unroll
-        for (int c = 0; c < ScaleStream::kWords; ++c) {
-          w[c] = scale_word(next[0][c]);
-          next[0][c] = next[1][c];
-        }
-        w[11] = 0;
-        in.fetch(next[1]);
-        if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
-        tensor_fence_after();
-        tmem_store4(taddr + st.slot * kScaleCols, w);
-        tmem_store8(taddr + st.slot * kScaleCols + 4, w + 4);
-        tensor_wait_store();
-        tensor_fence_before();
+        for (int i = 0; i < 3; ++i) s.words[sc.slot][i][lane][w] = scale_word(v[i]);
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.scaled[st.slot]);
-        st.next();
+        if (lane == 0) mbar_arrive(&s.scaled[sc.slot]);
+        sc.next();
       }
     } else if (warp == kLoadWarp && lane == 0) {
       // ---- loads ----
@@ -296,26 +301,35 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       // ---- tensor-core instructions ----
       const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, kBM, kBN);
       Ring<kStages> st;
+      Ring<kScaleSlots> sc;
       Ring<2> acc;
       bool ok = true;
       for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        for (int kb = 0; kb < p.kb; ++kb) {
-          const bool first = kb % kChain == 0;
-          if (first && !(ok = wait_or_dead(s, &s.tempty[acc.slot], acc.phase ^ 1u, p.fault))) break;
-          if (!(ok = wait_or_dead(s, &s.scaled[st.slot], st.phase, p.fault))) break;
-          if (!(ok = wait_or_dead(s, &s.full[st.slot], st.phase, p.fault))) break;
+        for (int kb = 0; ok && kb < p.kb; kb += kChain) {
+          if (!(ok = wait_or_dead(s, &s.tempty[acc.slot], acc.phase ^ 1u, p.fault))) break;
+          if (!(ok = wait_or_dead(s, &s.scaled[sc.slot], sc.phase, p.fault))) break;
           tensor_fence_after();
-          const uint64_t da = operand_desc(smem_addr(s.a[st.slot])), db = operand_desc(smem_addr(s.b[st.slot]));
-          const uint32_t sf = tmem + kScaleCol + st.slot * kScaleCols;
+          const uint32_t sf = tmem + kScaleCol + acc.slot * kScaleCols;
 #pragma unroll
-          for (int k = 0; k < kBlock / 32; ++k)  // 32 bytes along the swizzled row: 2 units of 16
-            tensor_mma_mxf8(tmem + acc.slot * kBN, da + 2 * k, db + 2 * k, idesc, sf, sf + 4, !first || k > 0);
-          tensor_commit(&s.empty[st.slot]);
-          st.next();
-          if (kb % kChain == kChain - 1 || kb == p.kb - 1) {
-            tensor_commit(&s.tfull[acc.slot]);
-            acc.next();
+          for (int i = 0; i < 3; ++i) tensor_copy_scales(sf + 4 * i, smem_addr(s.words[sc.slot][i]));
+#pragma unroll
+          for (int j = 0; j < kChain; ++j) {
+            if (kb + j >= p.kb) break;
+            if (!(ok = wait_or_dead(s, &s.full[st.slot], st.phase, p.fault))) break;
+            tensor_fence_after();
+            const uint64_t da = operand_desc(smem_addr(s.a[st.slot])), db = operand_desc(smem_addr(s.b[st.slot]));
+#pragma unroll
+            for (int k = 0; k < kBlock / 32; ++k)  // 32 bytes along the swizzled row: 2 units of 16
+              tensor_mma_mxf8(tmem + acc.slot * kBN, da + 2 * k, db + 2 * k, idesc | mxf8_scale_byte(j), sf, sf + 4,
+                              j > 0 || k > 0);
+            tensor_commit(&s.empty[st.slot]);
+            st.next();
           }
+          if (!ok) break;
+          tensor_commit(&s.sfree[sc.slot]);
+          tensor_commit(&s.tfull[acc.slot]);
+          sc.next();
+          acc.next();
         }
       }
     }

@@ -58,18 +58,15 @@ __device__ __forceinline__ void tensor_wait_load(uint32_t (&v)[16]) {
                  "+r"(v[15]));
 }
 
-// Stores to consecutive columns of the calling warp's 32 lanes; tensor_wait_store() completes them.
-__device__ __forceinline__ void tmem_store4(uint32_t addr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3])
-               : "memory");
+// 32 rows of 16 bytes in shared memory (512 contiguous bytes, 16-byte aligned) to 4 columns of tensor
+// memory, row i to lane i of each of the four groups of 32 lanes.  Ordered before the matrix
+// instructions that the same thread issues after it.
+__device__ __forceinline__ void tensor_copy_scales(uint32_t taddr, uint32_t saddr) {
+  constexpr uint64_t kStride = static_cast<uint64_t>(128 >> 4) << 32;  // eight rows of 16 bytes
+  constexpr uint64_t kVersion = 1ull << 46;
+  const uint64_t desc = static_cast<uint64_t>((saddr & 0x3ffffu) >> 4) | kStride | kVersion;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-__device__ __forceinline__ void tensor_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Two float32 at once (one instruction for both halves of a register pair).
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -109,11 +106,14 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (1ull << 16) | kStride | kVersion | kSwizzle128;
 }
 
-// Instruction descriptor of kind::mxf8f6f4: UE8M0 scales (bit 23), both operands K-major, and byte 0
-// of each row's 32-bit scale word (all four bytes hold the block's scale).
+// Instruction descriptor of kind::mxf8f6f4: UE8M0 scales (bit 23), both operands K-major, and the
+// byte (0 .. 3) of each row's 32-bit scale word that scales this instruction's 32 codes.
 __host__ __device__ constexpr uint32_t mxf8_instruction(int a_fmt, int b_fmt, int m, int n) {
   return (static_cast<uint32_t>(a_fmt) << 7) | (static_cast<uint32_t>(b_fmt) << 10) |
          (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t mxf8_scale_byte(int byte) {
+  return (static_cast<uint32_t>(byte) << 4) | (static_cast<uint32_t>(byte) << 29);
 }
 
 }  // namespace demo
