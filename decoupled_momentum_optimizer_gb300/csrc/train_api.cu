@@ -83,6 +83,19 @@ bool code_map(EncodeTiledFn encode, CUtensorMap* map, const void* codes, int64_t
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scales: [blocks][ld] float32, boxes of `box_rows` columns and `box_blocks` rows.
+bool scale_map(EncodeTiledFn encode, CUtensorMap* map, const float* scales, int64_t rows, int64_t blocks, int box_rows,
+               int box_blocks) {
+  const cuuint64_t ld = static_cast<cuuint64_t>(up(rows, 4));
+  const cuuint64_t dims[2] = {ld, static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[1] = {ld * 4};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_blocks)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(scales), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int check_quantized(const void* codes, const float* scales, int fmt) {
   if (!valid_fmt(fmt) || codes == nullptr || scales == nullptr) return DEMO_EINVAL;
   return at(codes, 16) && at(scales, 16) ? DEMO_OK : DEMO_EALIGN;
@@ -200,12 +213,13 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   if ((s = device_info(&dev)) != DEMO_OK) return s;
   MatmulParams q;
   std::memset(&q, 0, sizeof(q));
+  const MatmulPlan plan = plan_matmul(m, n, dev.sms);
   q.kb = static_cast<int>(up(k, kBlock) / kBlock);
-  if (q.kb > 0 && (!code_map(dev.encode, &q.a, a_codes, m, up(k, kBlock), matmul_box_rows(false)) ||
-                   !code_map(dev.encode, &q.b, b_codes, n, up(k, kBlock), matmul_box_rows(true))))
+  if (q.kb > 0 && (!code_map(dev.encode, &q.a, a_codes, m, up(k, kBlock), plan.box_a) ||
+                   !code_map(dev.encode, &q.b, b_codes, n, up(k, kBlock), plan.box_b) ||
+                   !scale_map(dev.encode, &q.sa, a_scales, m, q.kb, plan.box_a, plan.box_blocks) ||
+                   !scale_map(dev.encode, &q.sb, b_scales, n, q.kb, plan.box_sb, plan.box_blocks)))
     return DEMO_ECUDA;
-  q.a_scales = a_scales;
-  q.b_scales = b_scales;
   q.m = m;
   q.n = n;
   q.ldo = ldo;
@@ -215,7 +229,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   q.a_fmt = a_fmt;
   q.b_fmt = b_fmt;
   q.fault = dev.fault;
-  return to_status(launch_matmul(q, dev.sms, static_cast<cudaStream_t>(stream)));
+  return to_status(launch_matmul(q, plan, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t demo_fp8_linear_workspace(int64_t m, int64_t n, int64_t k) {

@@ -61,9 +61,8 @@ cudaError_t launch_quantize(const QuantParams& p, int dtype, int fmt, cudaStream
 
 // out = a b^T (+ out): a [m][k], b [n][k] quantized by rows.
 struct MatmulParams {
-  CUtensorMap a, b;  // codes, unused without blocks
-  const float* a_scales;
-  const float* b_scales;
+  CUtensorMap a, b;    // codes, unused without blocks
+  CUtensorMap sa, sb;  // scales
   long long m, n;
   int kb;  // blocks of 128 along k, may be 0
   long long ldo;
@@ -73,9 +72,14 @@ struct MatmulParams {
   unsigned int* fault;
 };
 
-// Rows of the tensor maps' boxes.
-int matmul_box_rows(bool b);
-cudaError_t launch_matmul(const MatmulParams& p, int sms, cudaStream_t st);
+// How a product runs: CTAs that share a tile (1 or 2), the tensor maps' boxes (rows of codes; rows and
+// blocks of scales), tiles.
+struct MatmulPlan {
+  int group, box_a, box_b, box_sb, box_blocks;
+  long long tiles;
+};
+MatmulPlan plan_matmul(long long m, long long n, int sms);
+cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, int sms, cudaStream_t st);
 cudaError_t prepare_matmul_kernels();
 
 }  // namespace demo

@@ -20,10 +20,9 @@ namespace demo {
 namespace {
 
 constexpr int kBM = 128, kBN = 224;
-constexpr int kStages = 4;
 constexpr int kChain = 4;  // blocks of 128 that one half of tensor memory sums
 constexpr int kSumWarps = 8, kScaleWarps = 4;
-constexpr int kLoadWarp = kSumWarps + kScaleWarps, kMmaWarp = kLoadWarp + 1;
+constexpr int kLoadWarp = kSumWarps + kScaleWarps, kMmaWarp = kLoadWarp + 1, kScaleLoadWarp = kLoadWarp + 2;
 // Whole groups of four warps, launched with 128 registers a thread: the summing ones take 192, the
 // others keep 64.
 constexpr int kThreads = 512;
@@ -33,32 +32,43 @@ constexpr uint32_t kTmemCols = 512;
 // Scale words of a half: 4 columns of a's (one for 32 rows) and 8 of b's (7 used).
 constexpr uint32_t kScaleCol = 2 * kBN, kScaleCols = 12;
 static_assert(kScaleCol + 2 * kScaleCols <= kTmemCols, "tensor memory");
-constexpr int kScaleSlots = 4;  // chains whose words are ready in shared memory
+constexpr int kScaleSlots = kScaleWarps;  // chains whose words are ready in shared memory
 static_assert(kChain == 4, "a word holds the scales of a chain");
-constexpr uint32_t kABytes = kBM * kBlock, kBBytes = kBN * kBlock;
 constexpr int kCols = kBN / 2;  // columns of a summing warp
 
+// G CTAs (1, or a cluster of 2) share a tile of G * 128 x 224: each loads its 128 rows of a and
+// 224 / G of b, and the rest of the shared memory is stages.
+template <int G>
 struct Shared {
+  static constexpr int kStages = G == 1 ? 4 : 6;
+  static constexpr uint32_t kABytes = kBM * kBlock, kBBytes = kBN / G * kBlock;
   uint8_t a[kStages][kABytes];  // 1024-byte aligned (swizzle atoms)
   uint8_t b[kStages][kBBytes];
   uint4 out[kSumWarps][128];  // a warp's 32 rows x 64 bytes on their way out
   // Scale words: row 32 c + l of an operand at [l][c] of its 512-byte unit of 128 rows (a's, then
   // b's two), as the tensor core's copy wants them.
   uint32_t words[kScaleSlots][3][32][4];
+  // a chain's scales as they arrive
+  float sa[kScaleSlots][kChain][kBM];
+  float sb[kScaleSlots][kChain][kBN];
   uint64_t full[kStages], empty[kStages];
-  uint64_t scaled[kScaleSlots], sfree[kScaleSlots];
+  uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // scales
+  uint64_t scaled[kScaleSlots], sfree[kScaleSlots];  // words
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem;
   volatile uint32_t dead;  // a wait gave up: everyone stops
 };
-constexpr size_t kSmem = sizeof(Shared) + 1024;
+template <int G>
+constexpr size_t kSmem = sizeof(Shared<G>) + 1024;
+static_assert(kSmem<1> <= 227 * 1024 && kSmem<2> <= 227 * 1024, "shared memory");
 
 // Phase `parity` of `bar`, or false once any wait of the CTA has given up.
-__device__ __forceinline__ bool wait_or_dead(Shared& s, uint64_t* bar, uint32_t parity, unsigned int* fault) {
+template <int G>
+__device__ __forceinline__ bool wait_or_dead(Shared<G>& s, uint64_t* bar, uint32_t parity, unsigned int* fault) {
   uint64_t t0 = 0;  // read late: the timer itself is slow to read, and most waits are short
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (G == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity)) return true;
     if ((it & 255u) == 0u) {
       if (s.dead) return false;
       const uint64_t t = global_timer_ns();
@@ -72,8 +82,18 @@ __device__ __forceinline__ bool wait_or_dead(Shared& s, uint64_t* bar, uint32_t 
   }
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+__device__ __forceinline__ void arrive_here(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// An arrival on the barrier of the CTA whose thread issues the matrix instructions.  RELEASE: it
+// publishes writes to shared memory; reads of tensor memory are ordered by the tensor-core fences
+// alone, and a release to the cluster would hold the warp up.
+template <int G, bool RELEASE>
+__device__ __forceinline__ void arrive_at_issuer(uint64_t* bar) {
+  if constexpr (G == 1)
+    arrive_here(bar);
+  else
+    mbar_arrive_at<RELEASE>(bar, 0);
 }
 
 // A position in a ring of N slots: the slot, and the parity of its current phase.
@@ -93,14 +113,16 @@ struct Tile {
   int m0, n0;
 };
 
-// Tiles in bands of 16 along m, along n within a band: the tiles that run at one time then cover
-// about as many rows of a as of b, and share both in the L2 cache.
-constexpr int kBand = 16;
-__device__ __forceinline__ Tile tile_at(long long t, int tiles_m, int tiles_n) {
-  const long long per = static_cast<long long>(kBand) * tiles_n;
-  const int band = static_cast<int>(t / per), i = static_cast<int>(t - band * per);
+// Tiles in bands of 2048 rows of m, along n within a band: the tiles that run at one time then cover
+// about as many rows of a as of b, and share both in the L2 cache.  m0 is the CTA's own first row.
+template <int G>
+__device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n, int rank) {
+  constexpr int kBand = 16 / G;
+  const int per = kBand * tiles_n;
+  const int band = t / per, i = t - band * per;
   const int height = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
-  return Tile{(band * kBand + i % height) * kBM, i / height * kBN};
+  const int col = i / height;
+  return Tile{((band * kBand + i - col * height) * G + rank) * kBM, col * kBN};
 }
 
 // Units of 16 bytes of a result row: E elements, converted from float32.
@@ -172,67 +194,42 @@ __device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint64_t 
 
 }  // namespace
 
-// A CTA's chains in order, tile after tile: the scales of up to four blocks of three rows, row
-// 32 w + l of a's tile (warp w, lane l) and rows 32 w + l and 128 + 32 w + l of b's.
-struct ScaleStream {
-  const MatmulParams& p;
-  long long lda, ldb, t, tiles;
-  int row, tiles_m, tiles_n, kb = 0;
-  const float *pa, *pb;
-  bool in_a, in_b0, in_b1;  // whether the rows exist
-
-  __device__ __forceinline__ ScaleStream(const MatmulParams& q, int r, int tm, int tn)
-      : p(q), lda((q.m + 3) / 4 * 4), ldb((q.n + 3) / 4 * 4), t(blockIdx.x), tiles(static_cast<long long>(tm) * tn),
-        row(r), tiles_m(tm), tiles_n(tn) {
-    if (p.kb == 0) t = tiles;
-    start();
-  }
-  __device__ __forceinline__ void start() {
-    if (t >= tiles) return;
-    const Tile tl = tile_at(t, tiles_m, tiles_n);
-    pa = p.a_scales + tl.m0 + row;
-    pb = p.b_scales + tl.n0 + row;
-    in_a = tl.m0 + row < p.m;
-    in_b0 = tl.n0 + row < p.n;
-    in_b1 = 128 + row < kBN && tl.n0 + 128 + row < p.n;
-  }
-  // Returns false past the last chain.
-  __device__ __forceinline__ bool fetch(float (&v)[3][4]) {
-    if (t >= tiles) return false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = kb + j < p.kb;
-      v[0][j] = in && in_a ? pa[j * lda] : 1.0f;
-      v[1][j] = in && in_b0 ? pb[j * ldb] : 1.0f;
-      v[2][j] = in && in_b1 ? pb[j * ldb + 128] : 1.0f;
-    }
-    pa += 4 * lda;
-    pb += 4 * ldb;
-    kb += 4;
-    if (kb >= p.kb) {
-      kb = 0;
-      t += gridDim.x;
-      start();
-    }
-    return true;
+// A CTA's chains (up to kChain blocks of a tile) in order, tile after tile.
+struct Chains {
+  int t, tiles, stride;
+  int c = 0, per_tile;
+  __device__ __forceinline__ Chains(int first, int n, int step, int kb)
+      : t(kb > 0 ? first : n), tiles(n), stride(step), per_tile((kb + kChain - 1) / kChain) {}
+  __device__ __forceinline__ bool more() const { return t < tiles; }
+  __device__ __forceinline__ void next(int by = 1) {
+    for (c += by; c >= per_tile && t < tiles; c -= per_tile) t += stride;
   }
 };
 
-// The exponent bytes of four powers of two.
-__device__ __forceinline__ uint32_t scale_word(const float (&v)[4]) {
-  uint32_t w = 0;
+// Up to 128 rows' scales of a chain (LD floats from block to block) as exponent bytes: word i is row
+// 32 i + lane's.
+template <int ROWS, int LD>
+__device__ __forceinline__ uint4 scale_words(const float* v, int lane) {
+  uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w |= ((__float_as_uint(v[j]) >> 23) & 0xffu) << (8 * j);
-  return w;
+  for (int i = 0; i < ROWS / 32; ++i)
+#pragma unroll
+    for (int j = 0; j < kChain; ++j)
+      w[i] |= ((__float_as_uint(v[j * LD + 32 * i + lane]) >> 23) & 0xffu) << (8 * j);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+template <int G>
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ MatmulParams p) {
   extern __shared__ uint8_t raw[];
-  Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  using S = Shared<G>;
+  constexpr int kStages = S::kStages;
+  S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tiles_m = static_cast<int>((p.m + kBM - 1) / kBM);
+  const int rank = G == 1 ? 0 : static_cast<int>(cluster_rank());
+  const int tiles_m = static_cast<int>((p.m + G * kBM - 1) / (G * kBM));
   const int tiles_n = static_cast<int>((p.n + kBN - 1) / kBN);
-  const long long tiles = static_cast<long long>(tiles_m) * tiles_n;
+  const int tiles = tiles_m * tiles_n;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -240,78 +237,113 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(&s.scaled[i], kScaleWarps);
+      mbar_init(&s.scaled[i], G);
       mbar_init(&s.sfree[i], 1);
+      mbar_init(&s.sfull[i], 1);
+      mbar_init(&s.sempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
-      mbar_init(&s.tempty[i], kSumWarps);
+      mbar_init(&s.tempty[i], G * kSumWarps);
     }
     mbar_init(&s.drain, 1);
     s.dead = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&s.tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc<G>(&s.tmem, kTmemCols);
   tensor_fence_before();
   __syncthreads();
+  if constexpr (G > 1) cluster_sync();  // the other CTA's barriers are there
   tensor_fence_after();
   const uint32_t tmem = s.tmem;
 
   if (warp >= kSumWarps) {
     registers_down<kFeedRegs>();
     if (warp < kLoadWarp) {
-      // ---- scales, a chain ahead of the slot that waits to be free ----
+      // ---- scale words: warp w makes those of every fourth chain, in slot w ----
       const int w = warp - kSumWarps;
-      ScaleStream in(p, 32 * w + lane, tiles_m, tiles_n);
-      Ring<kScaleSlots> sc;
-      float v[3][4];
-      while (in.fetch(v)) {
-        if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.sfree[sc.slot], sc.phase ^ 1u, p.fault))) break;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) s.words[sc.slot][i][lane][w] = scale_word(v[i]);
+      Chains in(blockIdx.x / G, tiles, gridDim.x / G, p.kb);
+      uint32_t phase = 0;
+      for (in.next(w); in.more(); in.next(kScaleWarps)) {
+        if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.sfull[w], phase, p.fault))) break;
+        const uint4 wa = scale_words<128, kBM>(s.sa[w][0], lane), wb = scale_words<128, kBN>(s.sb[w][0], lane),
+                    wc = scale_words<kBN - 128, kBN>(s.sb[w][0] + 128, lane);
+        __syncwarp();
+        if (lane == 0) arrive_here(&s.sempty[w]);
+        if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.sfree[w], phase ^ 1u, p.fault))) break;
+        phase ^= 1u;
+        *reinterpret_cast<uint4*>(s.words[w][0][lane]) = wa;
+        *reinterpret_cast<uint4*>(s.words[w][1][lane]) = wb;
+        *reinterpret_cast<uint4*>(s.words[w][2][lane]) = wc;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.scaled[sc.slot]);
-        sc.next();
+        if (lane == 0) arrive_at_issuer<G, true>(&s.scaled[w]);
       }
     } else if (warp == kLoadWarp && lane == 0) {
-      // ---- loads ----
+      // ---- loads of codes ----
       Ring<kStages> st;
       uint32_t used = 0;  // stages that have been loaded at least once
       bool ok = true;
-      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const Tile tl = tile_at(t, tiles_m, tiles_n);
+      for (int t = blockIdx.x / G; ok && t < tiles; t += gridDim.x / G) {
+        const Tile tl = tile_at<G>(t, tiles_m, tiles_n, rank);
         for (int kb = 0; kb < p.kb; ++kb) {
           if (!(ok = wait_or_dead(s, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
-          mbar_expect_tx(&s.full[st.slot], kABytes + kBBytes);
-          tma_load_2d(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
-          tma_load_2d(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0);
+          // a pair's loads all complete on the even CTA's barrier
+          if (rank == 0) mbar_expect_tx(&s.full[st.slot], G * (S::kABytes + S::kBBytes));
+          if constexpr (G == 1) {
+            tma_load_2d(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
+            tma_load_2d(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0);
+          } else {
+            tma_load_2d_pair(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
+            tma_load_2d_pair(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0 + rank * (kBN / G));
+          }
           used |= 1u << st.slot;
           st.next();
         }
       }
       // Stopped early: copies may be in flight into this CTA's shared memory.  Wait (bounded) for
-      // the last load of every stage: the stages before the ring's position are in its current
-      // phase, the others in the one before.
+      // the last load of every stage: those before the ring's position are in its current phase,
+      // the others in the one before.  (A pair's stages complete on the even CTA's barriers; the odd
+      // one waits for it at the end.)
       if (!ok) {
         for (int i = 0; i < kStages; ++i)
-          if (used >> i & 1u) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
+          if (rank == 0 && (used >> i & 1u)) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
       }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kScaleLoadWarp && lane == 0) {
+      // ---- loads of scales, in the same queue as the codes': a plain load would wait behind every
+      // stage that is under way.  (From the codes' thread they cost it half of its time.) ----
+      Chains in(blockIdx.x / G, tiles, gridDim.x / G, p.kb);
+      Ring<kScaleSlots> sc;
+      uint32_t used = 0;
+      bool ok = true;
+      for (; in.more(); in.next()) {
+        if (!(ok = wait_or_dead(s, &s.sempty[sc.slot], sc.phase ^ 1u, p.fault))) break;
+        const Tile tl = tile_at<G>(in.t, tiles_m, tiles_n, rank);
+        mbar_expect_tx(&s.sfull[sc.slot], kChain * (kBM + kBN) * 4);
+        tma_load_2d(s.sa[sc.slot], &p.sa, &s.sfull[sc.slot], tl.m0, kChain * in.c);
+        tma_load_2d(s.sb[sc.slot], &p.sb, &s.sfull[sc.slot], tl.n0, kChain * in.c);
+        used |= 1u << sc.slot;
+        sc.next();
+      }
+      if (!ok) {
+        for (int i = 0; i < kScaleSlots; ++i)
+          if (used >> i & 1u) mbar_wait_bounded(&s.sfull[i], i < sc.slot ? sc.phase : sc.phase ^ 1u);
+      }
+    } else if (warp == kMmaWarp && lane == 0 && rank == 0) {
       // ---- tensor-core instructions ----
-      const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, kBM, kBN);
+      const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, G * kBM, kBN);
       Ring<kStages> st;
       Ring<kScaleSlots> sc;
       Ring<2> acc;
       bool ok = true;
-      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      for (int t = blockIdx.x / G; ok && t < tiles; t += gridDim.x / G) {
         for (int kb = 0; ok && kb < p.kb; kb += kChain) {
           if (!(ok = wait_or_dead(s, &s.tempty[acc.slot], acc.phase ^ 1u, p.fault))) break;
           if (!(ok = wait_or_dead(s, &s.scaled[sc.slot], sc.phase, p.fault))) break;
           tensor_fence_after();
           const uint32_t sf = tmem + kScaleCol + acc.slot * kScaleCols;
 #pragma unroll
-          for (int i = 0; i < 3; ++i) tensor_copy_scales(sf + 4 * i, smem_addr(s.words[sc.slot][i]));
+          for (int i = 0; i < 3; ++i) tensor_copy_scales<G>(sf + 4 * i, smem_addr(s.words[sc.slot][i]));
 #pragma unroll
           for (int j = 0; j < kChain; ++j) {
             if (kb + j >= p.kb) break;
@@ -320,14 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
             const uint64_t da = operand_desc(smem_addr(s.a[st.slot])), db = operand_desc(smem_addr(s.b[st.slot]));
 #pragma unroll
             for (int k = 0; k < kBlock / 32; ++k)  // 32 bytes along the swizzled row: 2 units of 16
-              tensor_mma_mxf8(tmem + acc.slot * kBN, da + 2 * k, db + 2 * k, idesc | mxf8_scale_byte(j), sf, sf + 4,
+              tensor_mma_mxf8<G>(tmem + acc.slot * kBN, da + 2 * k, db + 2 * k, idesc | mxf8_scale_byte(j), sf, sf + 4,
                               j > 0 || k > 0);
-            tensor_commit(&s.empty[st.slot]);
+            tensor_commit<G>(&s.empty[st.slot]);
             st.next();
           }
           if (!ok) break;
-          tensor_commit(&s.sfree[sc.slot]);
-          tensor_commit(&s.tfull[acc.slot]);
+          tensor_commit<G>(&s.sfree[sc.slot]);
+          tensor_commit<G>(&s.tfull[acc.slot]);
           sc.next();
           acc.next();
         }
@@ -340,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + col0;
     Ring<2> acc;
     bool ok = true;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tl = tile_at(t, tiles_m, tiles_n);
+    for (int t = blockIdx.x / G; ok && t < tiles; t += gridDim.x / G) {
+      const Tile tl = tile_at<G>(t, tiles_m, tiles_n, rank);
       uint64_t sum[kCols / 2];  // pairs of columns
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
@@ -361,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           } else {
             tensor_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.tempty[acc.slot]);
+            if (lane == 0) arrive_at_issuer<G, false>(&s.tempty[acc.slot]);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -386,28 +418,51 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   }
   tensor_fence_before();
   __syncthreads();
+  // A CTA that stopped early may have matrix instructions in flight: wait (bounded) for them.
+  if (warp == kMmaWarp && lane == 0 && rank == 0 && s.dead) {
+    tensor_commit<G>(&s.drain);
+    mbar_wait_bounded(&s.drain, 0);
+  }
+  __syncthreads();
+  if constexpr (G > 1) cluster_sync();  // neither CTA leaves while the other may still reach its memory
   if (warp == kMmaWarp) {
-    // A CTA that stopped early may have matrix instructions in flight: wait (bounded) for them.
-    if (s.dead && lane == 0) {
-      tensor_commit(&s.drain);
-      mbar_wait_bounded(&s.drain, 0);
-    }
-    __syncwarp();
     tensor_fence_after();
-    tmem_free(tmem, kTmemCols);
+    tmem_free<G>(tmem, kTmemCols);
   }
 }
 
-int matmul_box_rows(bool b) { return b ? kBN : kBM; }
+template <int G>
+static cudaError_t launch_matmul_t(const MatmulParams& p, long long tiles, int sms, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  const long long groups = tiles < sms / G ? tiles : sms / G;
+  cfg.gridDim = dim3(static_cast<unsigned>(groups * G));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem<G>;
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = G;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = G > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<G>, p);
+}
 
-cudaError_t launch_matmul(const MatmulParams& p, int sms, cudaStream_t st) {
-  const long long tiles = ((p.m + kBM - 1) / kBM) * ((p.n + kBN - 1) / kBN);
-  matmul_kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kThreads, kSmem, st>>>(p);
-  return cudaGetLastError();
+MatmulPlan plan_matmul(long long m, long long n, int sms) {
+  const int group = m > kBM ? 2 : 1;
+  return MatmulPlan{group, kBM, kBN / group, kBN, kChain, ((m + group * kBM - 1) / (group * kBM)) * ((n + kBN - 1) / kBN)};
+}
+
+cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, int sms, cudaStream_t st) {
+  return plan.group == 1 ? launch_matmul_t<1>(p, plan.tiles, sms, st) : launch_matmul_t<2>(p, plan.tiles, sms, st);
 }
 
 cudaError_t prepare_matmul_kernels() {
-  return cudaFuncSetAttribute(matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  const cudaError_t e = cudaFuncSetAttribute(matmul_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmem<1>));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(matmul_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kSmem<2>));
 }
 
 }  // namespace demo
