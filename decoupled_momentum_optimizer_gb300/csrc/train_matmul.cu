@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   using S = Shared<G>;
   constexpr int kStages = S::kStages;
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the warp's number from one lane: the roles below are branches of whole warps
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = G == 1 ? 0 : static_cast<int>(cluster_rank());
   const int tiles_m = static_cast<int>((p.m + G * kBM - 1) / (G * kBM));
   const int tiles_n = static_cast<int>((p.n + kBN - 1) / kBN);
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) arrive_at_issuer<G, true>(&s.scaled[w]);
       }
-    } else if (warp == kLoadWarp && lane == 0) {
+    } else if (warp == kLoadWarp && elect_one()) {
       // ---- loads of codes ----
       Ring<kStages> st;
       uint32_t used = 0;  // stages that have been loaded at least once
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         for (int i = 0; i < kStages; ++i)
           if (rank == 0 && (used >> i & 1u)) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
       }
-    } else if (warp == kScaleLoadWarp && lane == 0) {
+    } else if (warp == kScaleLoadWarp && elect_one()) {
       // ---- loads of scales, in the same queue as the codes': a plain load would wait behind every
       // stage that is under way.  (From the codes' thread they cost it half of its time.) ----
       Chains in(blockIdx.x / G, tiles, gridDim.x / G, p.kb);
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         for (int i = 0; i < kScaleSlots; ++i)
           if (used >> i & 1u) mbar_wait_bounded(&s.sfull[i], i < sc.slot ? sc.phase : sc.phase ^ 1u);
       }
-    } else if (warp == kMmaWarp && lane == 0 && rank == 0) {
+    } else if (warp == kMmaWarp && rank == 0 && elect_one()) {
       // ---- tensor-core instructions ----
       const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, G * kBM, kBN);
       Ring<kStages> st;
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   tensor_fence_before();
   __syncthreads();
   // A CTA that stopped early may have matrix instructions in flight: wait (bounded) for them.
-  if (warp == kMmaWarp && lane == 0 && rank == 0 && s.dead) {
+  if (warp == kMmaWarp && rank == 0 && s.dead && elect_one()) {
     tensor_commit<G>(&s.drain);
     mbar_wait_bounded(&s.drain, 0);
   }
