@@ -96,6 +96,21 @@ bool scale_map(EncodeTiledFn encode, CUtensorMap* map, const float* scales, int6
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The result [m][n], boxes of 32 rows of `bytes` bytes.
+bool out_map(EncodeTiledFn encode, CUtensorMap* map, void* out, int64_t m, int64_t n, int64_t ldo, int dtype, int bytes) {
+  const int64_t size = elem_size(dtype);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m == 1 ? n * size : ldo * size)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(bytes / size), 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType type = dtype == DEMO_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == DEMO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return encode(map, type, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int check_quantized(const void* codes, const float* scales, int fmt) {
   if (!valid_fmt(fmt) || codes == nullptr || scales == nullptr) return DEMO_EINVAL;
   return at(codes, 16) && at(scales, 16) ? DEMO_OK : DEMO_EALIGN;
@@ -213,23 +228,29 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   if ((s = device_info(&dev)) != DEMO_OK) return s;
   MatmulParams q;
   std::memset(&q, 0, sizeof(q));
-  const MatmulPlan plan = plan_matmul(m, n, dev.sms);
   q.kb = static_cast<int>(up(k, kBlock) / kBlock);
-  if (q.kb > 0 && (!code_map(dev.encode, &q.a, a_codes, m, up(k, kBlock), plan.box_a) ||
-                   !code_map(dev.encode, &q.b, b_codes, n, up(k, kBlock), plan.box_b) ||
-                   !scale_map(dev.encode, &q.sa, a_scales, m, q.kb, plan.box_a, plan.box_blocks) ||
-                   !scale_map(dev.encode, &q.sb, b_scales, n, q.kb, plan.box_sb, plan.box_blocks)))
+  const MatmulPlan plan = plan_matmul(m, n, q.kb, dev.sms);
+  const int64_t size = elem_size(out_dtype);
+  // a bulk store writes whole units of 16 bytes, past the end of a row that is not a multiple of them
+  q.bulk_out = at(out, 16) && n * size % 16 == 0 && (m == 1 || ldo * size % 16 == 0);
+  if ((q.kb > 0 && (!code_map(dev.encode, &q.a, a_codes, m, up(k, kBlock), plan.rows_a) ||
+                    !code_map(dev.encode, &q.b, b_codes, n, up(k, kBlock), plan.rows_b) ||
+                    !scale_map(dev.encode, &q.sa, a_scales, m, q.kb, plan.rows_a, plan.chain) ||
+                    !scale_map(dev.encode, &q.sb, b_scales, n, q.kb, plan.bn, plan.chain))) ||
+      (q.bulk_out && !out_map(dev.encode, &q.o, out, m, n, ldo, out_dtype, plan.bn)))
     return DEMO_ECUDA;
   q.m = m;
   q.n = n;
   q.ldo = ldo;
   q.out = out;
+  q.bn = plan.bn;
+  q.split = plan.split;
   q.out_dtype = out_dtype;
   q.add = add;
   q.a_fmt = a_fmt;
   q.b_fmt = b_fmt;
   q.fault = dev.fault;
-  return to_status(launch_matmul(q, plan, dev.sms, static_cast<cudaStream_t>(stream)));
+  return to_status(launch_matmul(q, plan, static_cast<cudaStream_t>(stream)));
 }
 
 size_t demo_fp8_linear_workspace(int64_t m, int64_t n, int64_t k) {

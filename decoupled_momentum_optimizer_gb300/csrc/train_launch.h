@@ -63,23 +63,24 @@ cudaError_t launch_quantize(const QuantParams& p, int dtype, int fmt, cudaStream
 struct MatmulParams {
   CUtensorMap a, b;    // codes, unused without blocks
   CUtensorMap sa, sb;  // scales
-  long long m, n;
-  int kb;  // blocks of 128 along k, may be 0
-  long long ldo;
+  CUtensorMap o;       // the result, where bulk_out
+  long long m, n, ldo;
   void* out;
-  int out_dtype, add;
-  int a_fmt, b_fmt;
+  int kb;         // blocks of 128 along k, may be 0
+  int bn, split;  // see MatmulPlan
+  int out_dtype, add, a_fmt, b_fmt;
+  int bulk_out;  // the result's start, rows and row stride are multiples of 16 bytes
   unsigned int* fault;
 };
 
-// How a product runs: CTAs that share a tile (1 or 2), the tensor maps' boxes (rows of codes; rows and
-// blocks of scales), tiles.
+// How a product runs: CTAs that share a tile's rows (1 or 2), the tile's width, the parts k is cut
+// into, the grid; and the tensor maps' boxes (rows of codes, blocks of scales).
 struct MatmulPlan {
-  int group, box_a, box_b, box_sb, box_blocks;
-  long long tiles;
+  int group, bn, split, rows_a, rows_b, chain;
+  unsigned int grid;
 };
-MatmulPlan plan_matmul(long long m, long long n, int sms);
-cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, int sms, cudaStream_t st);
+MatmulPlan plan_matmul(long long m, long long n, int kb, int sms);
+cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st);
 cudaError_t prepare_matmul_kernels();
 
 }  // namespace demo

@@ -3,7 +3,7 @@
 //
 //   out[m][n] (+)= sum over blocks b of sa[b][m] sb[b][n] * (sum over k in block b of a[m][k] b[n][k])
 //
-// A CTA computes a 128 x 224 tile.  TMA brings 128 codes of k of both operands into a ring of
+// A pair of CTAs computes a 256 x bn tile (bn up to 224), or one CTA 128 x bn.  TMA brings 128 codes of k of both operands into a ring of
 // shared-memory stages; four warps pack the scales of four blocks into a 32-bit word per row (UE8M0
 // bytes), which the tensor core copies to tensor memory; one thread issues four K = 32 block-scaled
 // tensor-core instructions per block.  Four blocks run into one of two halves of tensor memory, and eight warps meanwhile add the other half to float32 sums in
@@ -19,7 +19,7 @@ namespace demo {
 
 namespace {
 
-constexpr int kBM = 128, kBN = 224;
+constexpr int kBM = 128, kBN = 224;  // rows of a CTA's tile, most columns
 constexpr int kChain = 4;  // blocks of 128 that one half of tensor memory sums
 constexpr int kSumWarps = 8, kScaleWarps = 4;
 constexpr int kLoadWarp = kSumWarps + kScaleWarps, kMmaWarp = kLoadWarp + 1, kScaleLoadWarp = kLoadWarp + 2;
@@ -34,23 +34,25 @@ constexpr uint32_t kScaleCol = 2 * kBN, kScaleCols = 12;
 static_assert(kScaleCol + 2 * kScaleCols <= kTmemCols, "tensor memory");
 constexpr int kScaleSlots = kScaleWarps;  // chains whose words are ready in shared memory
 static_assert(kChain == 4, "a word holds the scales of a chain");
-constexpr int kCols = kBN / 2;  // columns of a summing warp
+constexpr int kCols = kBN / 2;  // most columns of a summing warp
+constexpr int kOutBytes = 32 * kBN;  // a warp's rows on their way out, bn bytes each
+constexpr int kMaxSplit = 8;  // portable cluster size
 
-// G CTAs (1, or a cluster of 2) share a tile of G * 128 x 224: each loads its 128 rows of a and
-// 224 / G of b, and the rest of the shared memory is stages.
+// G CTAs (1, or a cluster of 2) share a tile: each loads its 128 rows of a and bn / G of b, and the
+// rest of the shared memory is stages.
 template <int G>
 struct Shared {
-  static constexpr int kStages = G == 1 ? 4 : 6;
+  static constexpr int kStages = G == 1 ? 3 : 4;
   static constexpr uint32_t kABytes = kBM * kBlock, kBBytes = kBN / G * kBlock;
   uint8_t a[kStages][kABytes];  // 1024-byte aligned (swizzle atoms)
   uint8_t b[kStages][kBBytes];
-  uint4 out[kSumWarps][128];  // a warp's 32 rows x 64 bytes on their way out
+  uint8_t out[kSumWarps][kOutBytes];
   // Scale words: row 32 c + l of an operand at [l][c] of its 512-byte unit of 128 rows (a's, then
   // b's two), as the tensor core's copy wants them.
   uint32_t words[kScaleSlots][3][32][4];
-  // a chain's scales as they arrive
-  float sa[kScaleSlots][kChain][kBM];
-  float sb[kScaleSlots][kChain][kBN];
+  // a chain's scales as they arrive: rows of kBM, and of bn
+  float sa[kScaleSlots][kChain * kBM];
+  float sb[kScaleSlots][kChain * kBN];
   uint64_t full[kStages], empty[kStages];
   uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // scales
   uint64_t scaled[kScaleSlots], sfree[kScaleSlots];  // words
@@ -62,6 +64,8 @@ struct Shared {
 template <int G>
 constexpr size_t kSmem = sizeof(Shared<G>) + 1024;
 static_assert(kSmem<1> <= 227 * 1024 && kSmem<2> <= 227 * 1024, "shared memory");
+// A split tile's float32 sums go where the stages were.
+static_assert(kBM * kBN * 4 <= Shared<1>::kStages * (Shared<1>::kABytes + Shared<1>::kBBytes), "a tile of sums");
 
 // Phase `parity` of `bar`, or false once any wait of the CTA has given up.
 template <int G>
@@ -113,112 +117,170 @@ struct Tile {
   int m0, n0;
 };
 
-// Tiles in bands of 2048 rows of m, along n within a band: the tiles that run at one time then cover
-// about as many rows of a as of b, and share both in the L2 cache.  m0 is the CTA's own first row.
-template <int G>
-__device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n, int rank) {
-  constexpr int kBand = 16 / G;
-  const int per = kBand * tiles_n;
-  const int band = t / per, i = t - band * per;
-  const int height = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
-  const int col = i / height;
-  return Tile{((band * kBand + i - col * height) * G + rank) * kBM, col * kBN};
+// The tiles and blocks of a CTA (or pair).  Tiles go in bands of 2048 rows of m, along n within a
+// band: those that run at one time then cover about as many rows of a as of b, and share both in
+// the L2 cache.
+struct Work {
+  int tiles_m, tiles_n, tiles, bn;
+  int first, stride;  // tiles first, first + stride, ...
+  int kb0, blocks;    // blocks of k, from kb0
+  int group, rank;    // CTAs of a tile's rows, and this one's number
+
+  // m0 is the CTA's own first row.
+  __device__ __forceinline__ Tile tile(int t) const {
+    const int band_tiles = 16 / group;
+    const int per = band_tiles * tiles_n;
+    const int band = t / per, i = t - band * per;
+    const int height = tiles_m - band * band_tiles < band_tiles ? tiles_m - band * band_tiles : band_tiles;
+    const int col = i / height;
+    return Tile{((band * band_tiles + i - col * height) * group + rank) * kBM, col * bn};
+  }
+};
+
+// A CTA's chains (up to kChain blocks of a tile) in order, tile after tile.
+struct Chains {
+  const Work& w;
+  int t, c = 0, per_tile;
+  __device__ __forceinline__ explicit Chains(const Work& work)
+      : w(work), t(work.blocks > 0 ? work.first : work.tiles), per_tile((work.blocks + kChain - 1) / kChain) {}
+  __device__ __forceinline__ bool more() const { return t < w.tiles; }
+  __device__ __forceinline__ void next(int by = 1) {
+    for (c += by; c >= per_tile && t < w.tiles; c -= per_tile) t += w.stride;
+  }
+};
+
+// The scales of 128 rows and a chain's blocks (`ld` floats from block to block) as exponent bytes:
+// word i is row 32 i + lane's.  Rows past `rows` have scale 1.
+__device__ __forceinline__ uint4 scale_words(const float* v, int ld, int rows, int lane) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = 0x7f7f7f7fu;
+    if (32 * i < rows) {
+      w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < kChain; ++j) w[i] |= ((__float_as_uint(v[j * ld + 32 * i + lane]) >> 23) & 0xffu) << (8 * j);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Units of 16 bytes of a result row: E elements, converted from float32.
 template <typename T>
-__device__ __forceinline__ uint4 to_unit(const float* v) {
+__device__ __forceinline__ void store_elem(const MatmulParams& p, long long i, T v) {
+  T* o = static_cast<T*>(p.out) + i;
   if constexpr (sizeof(T) == 4) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    *o = p.add ? *o + v : v;
   } else {
-    Vec<T, 8> o;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o.e[e] = from_f32<T>(v[e]);
-    return *reinterpret_cast<uint4*>(&o);
+    *o = v;
   }
 }
 
-__device__ __forceinline__ float4 add4(float4 a, float4 b) {
-  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+// Results that no bulk store can write (rows or addresses off 16 bytes): a warp's `cols` columns,
+// staged as below, one row after another.
+template <typename T>
+__device__ __noinline__ void store_plain(const MatmulParams& p, const uint8_t* buf, int cols, int lane, long long m0,
+                                         long long n0) {
+  for (int r = 0; r < 32 && m0 + r < p.m; ++r)
+    for (int c = lane; c < cols && n0 + c < p.n; c += 32)
+      store_elem<T>(p, (m0 + r) * p.ldo + n0 + c, reinterpret_cast<const T*>(buf + r * p.bn)[c]);
 }
 
-// A warp's 32 rows (lane l holds row l) x kCols columns to out[m0 ..][n0 ..], 64 bytes of every row at
-// a time through 2 KB of shared memory: written a row per lane, read back as 8 rows x 4 units, so
-// that every store covers whole 32-byte sectors.  Unit u of row r is stored at u ^ ((r >> 1) & 3):
-// two rows span the banks once, so eight lanes of either access reach different ones.
-template <typename T, bool ADD>
-__device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint64_t (&sum)[kCols / 2],
-                                           const MatmulParams& p, long long m0, long long n0) {
-  constexpr int E = 16 / static_cast<int>(sizeof(T));
-  const bool vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % E == 0;
-#pragma unroll
-  for (int c = 0; c < kCols; c += 4 * E) {
-    if (n0 + c >= p.n) break;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (c + u * E >= kCols) break;
-      float v[E];
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 q = unpack2(sum[(c + u * E + e) / 2]);
-        v[e] = q.x;
-        v[e + 1] = q.y;
-      }
-      buf[lane * 4 + (u ^ ((lane >> 1) & 3))] = to_unit<T>(v);
-    }
+// What a warp has staged (32 rows of bn bytes, `cols` columns) to out[m0 ..][n0 ..]: one bulk store,
+// which cuts off what is past the matrix, adds where asked, and runs on behind the warp's next work.
+template <typename T>
+__device__ __forceinline__ void store_staged(const MatmulParams& p, const uint8_t* buf, int cols, int lane,
+                                             long long m0, long long n0) {
+  if (p.bulk_out) {
+    fence_proxy_async_smem();
     __syncwarp();
+    if (lane == 0 && m0 < p.m && n0 < p.n) {
+      if (p.add)
+        tma_add_2d(&p.o, buf, static_cast<int>(n0), static_cast<int>(m0));
+      else
+        tma_store_2d(&p.o, buf, static_cast<int>(n0), static_cast<int>(m0));
+      bulk_commit();
+    }
+  } else {
+    __syncwarp();
+    store_plain<T>(p, buf, cols, lane, m0, n0);
+  }
+}
+
+// The staging buffer may be written again: its last bulk store has read it.
+__device__ __forceinline__ void staging_free(int lane) {
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
+}
+
+// A warp's 32 rows (lane l holds row l) x bn / 2 columns to out[m0 ..][n0 ..], through rows of bn bytes
+// in shared memory: all columns at once in 16 bits, half of them at a time in 32.
+template <typename T>
+__device__ __forceinline__ void store_sums(const MatmulParams& p, uint8_t* buf, int lane,
+                                           const uint64_t (&sum)[kCols / 2], long long m0, long long n0) {
+  if constexpr (sizeof(T) == 2) {
+    staging_free(lane);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = 8 * q + (lane >> 2), u = lane & 3;
-      uint4 w = buf[r * 4 + (u ^ ((r >> 1) & 3))];
-      const long long m = m0 + r, n = n0 + c + u * E;
-      if (m < p.m && n < p.n && c + u * E < kCols) {
-        T* o = static_cast<T*>(p.out) + m * p.ldo + n;
-        if (vec && n + E <= p.n) {
-          if constexpr (ADD) {
-            const float4 s = add4(*reinterpret_cast<const float4*>(o), *reinterpret_cast<const float4*>(&w));
-            w = *reinterpret_cast<const uint4*>(&s);
-          }
-          *reinterpret_cast<uint4*>(o) = w;
-        } else {
-          const T* x = reinterpret_cast<const T*>(&w);
+    for (int u = 0; u < kCols / 8; ++u) {
+      if (16 * u < p.bn) {
+        Vec<T, 8> o;
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (n + e < p.n) o[e] = ADD ? from_f32<T>(to_f32(o[e]) + to_f32(x[e])) : x[e];
+        for (int e = 0; e < 4; ++e) {
+          const float2 q = unpack2(sum[4 * u + e]);
+          o.e[2 * e] = from_f32<T>(q.x);
+          o.e[2 * e + 1] = from_f32<T>(q.y);
+        }
+        *reinterpret_cast<Vec<T, 8>*>(buf + lane * p.bn + 16 * u) = o;
+      }
+    }
+    store_staged<T>(p, buf, p.bn / 2, lane, m0, n0);
+  } else {
+    const int units = p.bn / 16;  // of four columns, a half
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      staging_free(lane);
+#pragma unroll
+      for (int u = 0; u < kCols / 4; ++u) {
+        if (u >= h * units && u < (h + 1) * units) {
+          const float2 x = unpack2(sum[2 * u]), y = unpack2(sum[2 * u + 1]);
+          *reinterpret_cast<float4*>(buf + lane * p.bn + 16 * (u - h * units)) = make_float4(x.x, x.y, y.x, y.y);
         }
       }
+      store_staged<T>(p, buf, p.bn / 4, lane, m0, n0 + h * (p.bn / 4));
     }
-    __syncwarp();
+  }
+}
+
+// Four columns of a row from a split tile's joined sums.
+template <typename T>
+__device__ __forceinline__ void store_four(const MatmulParams& p, long long m, long long n, float4 v) {
+  if (m >= p.m || n >= p.n) return;
+  const long long i = m * p.ldo + n;
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  if (p.bulk_out && n + 4 <= p.n) {  // rows are multiples of 16 bytes from an aligned start
+    if constexpr (sizeof(T) == 4) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + i);
+      if (p.add) {
+        const float4 w = *o;
+        v = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
+      }
+      *o = v;
+    } else {
+      Vec<T, 4> o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.e[e] = from_f32<T>(x[e]);
+      *reinterpret_cast<Vec<T, 4>*>(static_cast<T*>(p.out) + i) = o;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.n) store_elem<T>(p, i + e, from_f32<T>(x[e]));
   }
 }
 
 }  // namespace
 
-// A CTA's chains (up to kChain blocks of a tile) in order, tile after tile.
-struct Chains {
-  int t, tiles, stride;
-  int c = 0, per_tile;
-  __device__ __forceinline__ Chains(int first, int n, int step, int kb)
-      : t(kb > 0 ? first : n), tiles(n), stride(step), per_tile((kb + kChain - 1) / kChain) {}
-  __device__ __forceinline__ bool more() const { return t < tiles; }
-  __device__ __forceinline__ void next(int by = 1) {
-    for (c += by; c >= per_tile && t < tiles; c -= per_tile) t += stride;
-  }
-};
-
-// Up to 128 rows' scales of a chain (LD floats from block to block) as exponent bytes: word i is row
-// 32 i + lane's.
-template <int ROWS, int LD>
-__device__ __forceinline__ uint4 scale_words(const float* v, int lane) {
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < ROWS / 32; ++i)
-#pragma unroll
-    for (int j = 0; j < kChain; ++j)
-      w[i] |= ((__float_as_uint(v[j * LD + 32 * i + lane]) >> 23) & 0xffu) << (8 * j);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
+// G = 2: pairs of CTAs, each pair walks its tiles.  G = 1: a cluster of p.split CTAs for a tile, each
+// sums its share of k; the shares are joined in the order of k through distributed shared memory.
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ MatmulParams p) {
   extern __shared__ uint8_t raw[];
@@ -227,10 +289,27 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   // the warp's number from one lane: the roles below are branches of whole warps
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = G == 1 ? 0 : static_cast<int>(cluster_rank());
-  const int tiles_m = static_cast<int>((p.m + G * kBM - 1) / (G * kBM));
-  const int tiles_n = static_cast<int>((p.n + kBN - 1) / kBN);
-  const int tiles = tiles_m * tiles_n;
+  const int rank = G == 1 ? 0 : static_cast<int>(cluster_rank());  // in the pair
+  const int part = G == 1 ? static_cast<int>(cluster_rank()) : 0;  // of k
+  Work work;
+  work.tiles_m = static_cast<int>((p.m + G * kBM - 1) / (G * kBM));
+  work.tiles_n = static_cast<int>((p.n + p.bn - 1) / p.bn);
+  work.tiles = work.tiles_m * work.tiles_n;
+  work.bn = p.bn;
+  work.group = G;
+  work.rank = rank;
+  if constexpr (G == 1) {
+    const int q = p.kb / p.split, r = p.kb - q * p.split;
+    work.first = blockIdx.x / p.split;
+    work.stride = work.tiles;
+    work.kb0 = part * q + (part < r ? part : r);
+    work.blocks = q + (part < r ? 1 : 0);
+  } else {
+    work.first = blockIdx.x / G;
+    work.stride = gridDim.x / G;
+    work.kb0 = 0;
+    work.blocks = p.kb;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -256,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   __syncthreads();
   if constexpr (G > 1) cluster_sync();  // the other CTA's barriers are there
   tensor_fence_after();
+  griddep_launch_dependents();
+  griddep_wait();  // the operands, and the result that was there, are complete from here on
   const uint32_t tmem = s.tmem;
 
   if (warp >= kSumWarps) {
@@ -263,12 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     if (warp < kLoadWarp) {
       // ---- scale words: warp w makes those of every fourth chain, in slot w ----
       const int w = warp - kSumWarps;
-      Chains in(blockIdx.x / G, tiles, gridDim.x / G, p.kb);
+      Chains in(work);
       uint32_t phase = 0;
       for (in.next(w); in.more(); in.next(kScaleWarps)) {
         if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.sfull[w], phase, p.fault))) break;
-        const uint4 wa = scale_words<128, kBM>(s.sa[w][0], lane), wb = scale_words<128, kBN>(s.sb[w][0], lane),
-                    wc = scale_words<kBN - 128, kBN>(s.sb[w][0] + 128, lane);
+        const uint4 wa = scale_words(s.sa[w], kBM, kBM, lane), wb = scale_words(s.sb[w], p.bn, p.bn, lane),
+                    wc = scale_words(s.sb[w] + 128, p.bn, p.bn - 128, lane);
         __syncwarp();
         if (lane == 0) arrive_here(&s.sempty[w]);
         if (!__all_sync(0xffffffffu, wait_or_dead(s, &s.sfree[w], phase ^ 1u, p.fault))) break;
@@ -285,18 +366,19 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       Ring<kStages> st;
       uint32_t used = 0;  // stages that have been loaded at least once
       bool ok = true;
-      for (int t = blockIdx.x / G; ok && t < tiles; t += gridDim.x / G) {
-        const Tile tl = tile_at<G>(t, tiles_m, tiles_n, rank);
-        for (int kb = 0; kb < p.kb; ++kb) {
+      const uint32_t bytes = G * S::kABytes + p.bn * kBlock;  // of a stage, of the pair together
+      for (int t = work.first; ok && t < work.tiles; t += work.stride) {
+        const Tile tl = work.tile(t);
+        for (int kb = work.kb0; kb < work.kb0 + work.blocks; ++kb) {
           if (!(ok = wait_or_dead(s, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
           // a pair's loads all complete on the even CTA's barrier
-          if (rank == 0) mbar_expect_tx(&s.full[st.slot], G * (S::kABytes + S::kBBytes));
+          if (rank == 0) mbar_expect_tx(&s.full[st.slot], bytes);
           if constexpr (G == 1) {
             tma_load_2d(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
             tma_load_2d(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0);
           } else {
             tma_load_2d_pair(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
-            tma_load_2d_pair(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0 + rank * (kBN / G));
+            tma_load_2d_pair(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0 + rank * (p.bn / G));
           }
           used |= 1u << st.slot;
           st.next();
@@ -313,16 +395,17 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     } else if (warp == kScaleLoadWarp && elect_one()) {
       // ---- loads of scales, in the same queue as the codes': a plain load would wait behind every
       // stage that is under way.  (From the codes' thread they cost it half of its time.) ----
-      Chains in(blockIdx.x / G, tiles, gridDim.x / G, p.kb);
+      Chains in(work);
       Ring<kScaleSlots> sc;
       uint32_t used = 0;
       bool ok = true;
       for (; in.more(); in.next()) {
         if (!(ok = wait_or_dead(s, &s.sempty[sc.slot], sc.phase ^ 1u, p.fault))) break;
-        const Tile tl = tile_at<G>(in.t, tiles_m, tiles_n, rank);
-        mbar_expect_tx(&s.sfull[sc.slot], kChain * (kBM + kBN) * 4);
-        tma_load_2d(s.sa[sc.slot], &p.sa, &s.sfull[sc.slot], tl.m0, kChain * in.c);
-        tma_load_2d(s.sb[sc.slot], &p.sb, &s.sfull[sc.slot], tl.n0, kChain * in.c);
+        const Tile tl = work.tile(in.t);
+        const int kb = work.kb0 + kChain * in.c;  // rows past the last block are filled, or not used
+        mbar_expect_tx(&s.sfull[sc.slot], kChain * (kBM + p.bn) * 4);
+        tma_load_2d(s.sa[sc.slot], &p.sa, &s.sfull[sc.slot], tl.m0, kb);
+        tma_load_2d(s.sb[sc.slot], &p.sb, &s.sfull[sc.slot], tl.n0, kb);
         used |= 1u << sc.slot;
         sc.next();
       }
@@ -332,13 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       }
     } else if (warp == kMmaWarp && rank == 0 && elect_one()) {
       // ---- tensor-core instructions ----
-      const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, G * kBM, kBN);
+      const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, G * kBM, p.bn);
       Ring<kStages> st;
       Ring<kScaleSlots> sc;
       Ring<2> acc;
       bool ok = true;
-      for (int t = blockIdx.x / G; ok && t < tiles; t += gridDim.x / G) {
-        for (int kb = 0; ok && kb < p.kb; kb += kChain) {
+      for (int t = work.first; ok && t < work.tiles; t += work.stride) {
+        for (int kb = 0; ok && kb < work.blocks; kb += kChain) {
           if (!(ok = wait_or_dead(s, &s.tempty[acc.slot], acc.phase ^ 1u, p.fault))) break;
           if (!(ok = wait_or_dead(s, &s.scaled[sc.slot], sc.phase, p.fault))) break;
           tensor_fence_after();
@@ -347,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           for (int i = 0; i < 3; ++i) tensor_copy_scales<G>(sf + 4 * i, smem_addr(s.words[sc.slot][i]));
 #pragma unroll
           for (int j = 0; j < kChain; ++j) {
-            if (kb + j >= p.kb) break;
+            if (kb + j >= work.blocks) break;
             if (!(ok = wait_or_dead(s, &s.full[st.slot], st.phase, p.fault))) break;
             tensor_fence_after();
             const uint64_t da = operand_desc(smem_addr(s.a[st.slot])), db = operand_desc(smem_addr(s.b[st.slot]));
@@ -368,17 +451,17 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     }
   } else {
     registers_up<kSumRegs>();
-    // ---- float32 sums: warp w holds rows 32 (w & 3) .., columns kCols (w >> 2) .. ----
-    const int col0 = kCols * (warp >> 2);
+    // ---- float32 sums: warp w holds rows 32 (w & 3) .., columns bn / 2 (w >> 2) .. ----
+    const int cols = p.bn / 2, col0 = cols * (warp >> 2);
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + col0;
     Ring<2> acc;
     bool ok = true;
-    for (int t = blockIdx.x / G; ok && t < tiles; t += gridDim.x / G) {
-      const Tile tl = tile_at<G>(t, tiles_m, tiles_n, rank);
+    for (int t = work.first; ok && t < work.tiles; t += work.stride) {
+      const Tile tl = work.tile(t);
       uint64_t sum[kCols / 2];  // pairs of columns
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) sum[i] = 0;
-      for (int kb = 0; kb < p.kb; kb += kChain) {
+      for (int kb = 0; kb < work.blocks; kb += kChain) {
         // every lane waits (each reads what the barrier guards); the warp goes on or stops as one
         ok = __all_sync(0xffffffffu, wait_or_dead(s, &s.tfull[acc.slot], acc.phase, p.fault));
         if (!ok) break;
@@ -388,34 +471,44 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         tmem_load16(taddr + acc.slot * kBN, v[0]);
 #pragma unroll
         for (int c = 0; c < kCols / 16; ++c) {
-          tensor_wait_load(v[c & 1]);
-          if (c + 1 < kCols / 16) {
-            tmem_load16(taddr + acc.slot * kBN + 16 * (c + 1), v[(c + 1) & 1]);
-          } else {
-            tensor_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at_issuer<G, false>(&s.tempty[acc.slot]);
-          }
+          if (16 * c < cols) {
+            tensor_wait_load(v[c & 1]);
+            if (16 * (c + 1) < cols) {
+              tmem_load16(taddr + acc.slot * kBN + 16 * (c + 1), v[(c + 1) & 1]);
+            } else {
+              tensor_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_at_issuer<G, false>(&s.tempty[acc.slot]);
+            }
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            sum[8 * c + j] = add2(sum[8 * c + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]));
+            for (int j = 0; j < 8; ++j)
+              sum[8 * c + j] = add2(sum[8 * c + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]));
+          }
         }
         acc.next();
       }
       if (!ok) break;
-      const long long m0 = tl.m0 + 32 * (warp & 3), n0 = tl.n0 + col0;
-      if (m0 < p.m && n0 < p.n) {
-        uint4* buf = s.out[warp];
+      if (G == 1 && p.split > 1) {
+        // to shared memory, unit u (four columns) of row r at [u][r]
+        float4* red = reinterpret_cast<float4*>(s.a);
+#pragma unroll
+        for (int u = 0; u < kCols / 4; ++u) {
+          if (4 * u < cols) {
+            const float2 x = unpack2(sum[2 * u]), y = unpack2(sum[2 * u + 1]);
+            red[(col0 / 4 + u) * kBM + 32 * (warp & 3) + lane] = make_float4(x.x, x.y, y.x, y.y);
+          }
+        }
+      } else {
+        const long long m0 = tl.m0 + 32 * (warp & 3), n0 = tl.n0 + col0;
         if (p.out_dtype == kBF16)
-          store_rows<__nv_bfloat16, false>(buf, lane, sum, p, m0, n0);
+          store_sums<__nv_bfloat16>(p, s.out[warp], lane, sum, m0, n0);
         else if (p.out_dtype == kF16)
-          store_rows<__half, false>(buf, lane, sum, p, m0, n0);
-        else if (p.add)
-          store_rows<float, true>(buf, lane, sum, p, m0, n0);
+          store_sums<__half>(p, s.out[warp], lane, sum, m0, n0);
         else
-          store_rows<float, false>(buf, lane, sum, p, m0, n0);
+          store_sums<float>(p, s.out[warp], lane, sum, m0, n0);
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
   tensor_fence_before();
   __syncthreads();
@@ -425,7 +518,34 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     mbar_wait_bounded(&s.drain, 0);
   }
   __syncthreads();
-  if constexpr (G > 1) cluster_sync();  // neither CTA leaves while the other may still reach its memory
+  if (G > 1 || p.split > 1) cluster_sync();  // a pair: neither CTA leaves while the other may reach its memory
+  if (G == 1 && p.split > 1) {
+    // each CTA joins its share of the columns, always from the first part of k to the last
+    if (warp < kSumWarps) {
+      const Tile tl = work.tile(work.first);
+      const int units = p.bn / 4, row = threadIdx.x & (kBM - 1);
+      const int hi = units * (part + 1) / p.split;
+      const uint32_t red = smem_addr(s.a);
+      for (int u = units * part / p.split + (threadIdx.x >> 7); u < hi; u += 2) {
+        float4 v[kMaxSplit];
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+          if (q < p.split) v[q] = load_cluster(red + (u * kBM + row) * 16, q);
+#pragma unroll
+        for (int q = 1; q < kMaxSplit; ++q)
+          if (q < p.split)
+            v[0] = make_float4(v[0].x + v[q].x, v[0].y + v[q].y, v[0].z + v[q].z, v[0].w + v[q].w);
+        if (p.out_dtype == kBF16)
+          store_four<__nv_bfloat16>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
+        else if (p.out_dtype == kF16)
+          store_four<__half>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
+        else
+          store_four<float>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
   if (warp == kMmaWarp) {
     tensor_fence_after();
     tmem_free<G>(tmem, kTmemCols);
@@ -433,29 +553,63 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
 }
 
 template <int G>
-static cudaError_t launch_matmul_t(const MatmulParams& p, long long tiles, int sms, cudaStream_t st) {
+static cudaError_t launch_matmul_t(const MatmulParams& p, unsigned grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  const long long groups = tiles < sms / G ? tiles : sms / G;
-  cfg.gridDim = dim3(static_cast<unsigned>(groups * G));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem<G>;
   cfg.stream = st;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = G;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = G > 1 ? 1 : 0;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = G == 1 ? p.split : G;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, matmul_kernel<G>, p);
 }
 
-MatmulPlan plan_matmul(long long m, long long n, int sms) {
-  const int group = m > kBM ? 2 : 1;
-  return MatmulPlan{group, kBM, kBN / group, kBN, kChain, ((m + group * kBM - 1) / (group * kBM)) * ((n + kBN - 1) / kBN)};
+// Few tiles (128 x 224 ones that would leave half of the SMs idle, or m that fills no pair): one CTA
+// per tile, with k cut into as many parts as there are SMs for, at least a chain each.  Otherwise
+// pairs, with the width whose last round is fullest: a block takes about max(2 bn, 256 + bn) cycles
+// (the tensor cores, or what the CTA reads) and a tile about 2500 more.
+MatmulPlan plan_matmul(long long m, long long n, int kb, int sms) {
+  const auto tiles = [&](int rows, int bn) { return ((m + rows - 1) / rows) * ((n + bn - 1) / bn); };
+  MatmulPlan plan;
+  plan.split = 1;
+  if (m <= kBM || 2 * tiles(kBM, kBN) <= sms) {
+    plan.group = 1;
+    plan.bn = n >= kBN ? kBN : static_cast<int>(n + 31) / 32 * 32;
+    if (plan.bn < 64) plan.bn = 64;
+    const long long t = tiles(kBM, plan.bn);
+    long long s = sms / t;
+    if (s > (kb + kChain - 1) / kChain) s = (kb + kChain - 1) / kChain;
+    if (s > kMaxSplit) s = kMaxSplit;
+    if (s > 1) plan.split = static_cast<int>(s);
+    plan.grid = static_cast<unsigned>(t * plan.split);
+  } else {
+    plan.group = 2;
+    const long long pairs = sms / 2;
+    double best = 0;
+    for (int bn = kBN; bn >= 96; bn -= 32) {
+      const long long t = tiles(2 * kBM, bn), rounds = (t + pairs - 1) / pairs;
+      const double cost = static_cast<double>(rounds) * (2500.0 + static_cast<double>(kb) * (256 + bn));
+      if (best == 0 || cost < best) {
+        best = cost;
+        plan.bn = bn;
+        plan.grid = static_cast<unsigned>(2 * (t < pairs ? t : pairs));
+      }
+    }
+  }
+  plan.rows_a = kBM;
+  plan.rows_b = plan.bn / plan.group;
+  plan.chain = kChain;
+  return plan;
 }
 
-cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, int sms, cudaStream_t st) {
-  return plan.group == 1 ? launch_matmul_t<1>(p, plan.tiles, sms, st) : launch_matmul_t<2>(p, plan.tiles, sms, st);
+cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st) {
+  return plan.group == 1 ? launch_matmul_t<1>(p, plan.grid, st) : launch_matmul_t<2>(p, plan.grid, st);
 }
 
 cudaError_t prepare_matmul_kernels() {

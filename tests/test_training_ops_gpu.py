@@ -259,7 +259,8 @@ def check_product(m, n, k, a_fmt="e4m3", b_fmt="e4m3", tiles=False, out="f32", p
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 1, 128), (2, 3, 129), (128, 256, 128), (128, 256, 1024), (129, 257, 300),
-                                   (5, 300, 515), (300, 5, 515), (256, 512, 2048), (260, 1000, 768), (513, 100, 4100)])
+                                   (5, 300, 515), (300, 5, 515), (256, 512, 2048), (260, 1000, 768), (513, 100, 4100), (700, 33, 9000),
+                                   (2100, 1300, 700), (3000, 2000, 129), (5000, 450, 1024)])
 @pytest.mark.parametrize("tiles", [False, True])
 def test_matmul(m, n, k, tiles):
     check_product(m, n, k, tiles=tiles)
@@ -272,9 +273,10 @@ def test_matmul_types(a_fmt, b_fmt, out):
     check_product(150, 300, 700, a_fmt, b_fmt, out=out)
 
 
-@pytest.mark.parametrize("out,pad,offset", [("f32", 1, 0), ("f32", 4, 0), ("f32", 0, 1), ("bf16", 3, 0), ("bf16", 8, 0), ("f16", 0, 2)])
+@pytest.mark.parametrize("out,pad,offset", [("f32", 1, 0), ("f32", 4, 0), ("f32", 3, 0), ("f32", 0, 1), ("bf16", 3, 0), ("bf16", 7, 0),
+                                            ("bf16", 8, 0), ("f16", 0, 2)])
 @pytest.mark.parametrize("add", [False, True])
-@pytest.mark.parametrize("m,n", [(150, 300), (140, 64), (3, 33)])
+@pytest.mark.parametrize("m,n", [(150, 300), (140, 64), (3, 33), (2500, 1377)])
 def test_matmul_strides(out, pad, offset, add, m, n):
     if add and out != "f32":
         pytest.skip("add is float32's")
@@ -320,9 +322,10 @@ def test_matmul_non_finite():
     assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
 
 
-def test_matmul_repeats_to_the_bit_and_on_another_stream():
-    a, _ = quantized(300, 1500, seed=37)
-    b, _ = quantized(500, 1500, seed=38)
+@pytest.mark.parametrize("m,n,k", [(300, 500, 1500), (3000, 1500, 700)])
+def test_matmul_repeats_to_the_bit_and_on_another_stream(m, n, k):
+    a, _ = quantized(m, k, seed=37)
+    b, _ = quantized(n, k, seed=38)
     first = dm.fp8_matmul(a, b, dtype=torch.float32)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
