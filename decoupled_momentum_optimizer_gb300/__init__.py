@@ -404,5 +404,5 @@ def __getattr__(name):
     if name in _TRAINING_OPS:
         from . import training_ops
 
-        return getattr(training_ops, name)
+        return globals().setdefault(name, getattr(training_ops, name))
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -254,7 +254,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
 }
 
 size_t demo_fp8_linear_workspace(int64_t m, int64_t n, int64_t k) {
-  if (m <= 0 || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+  if (m <= kLinearRows || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
   return static_cast<size_t>(code_bytes(m, k) + scale_bytes(m, k));
 }
 
@@ -281,6 +281,24 @@ int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, 
       const Region rw = flat(workspace, static_cast<int64_t>(need));
       if (overlap(rw, ro) || overlap(rw, rx) || overlap(rw, rc) || overlap(rw, rs)) return DEMO_EINVAL;
     }
+  }
+  if (m <= kLinearRows) {
+    DeviceInfo dev;
+    if ((s = device_info(&dev)) != DEMO_OK) return s;
+    LinearParams q;
+    std::memset(&q, 0, sizeof(q));
+    q.x = x;
+    q.w = w_codes;
+    q.w_scales = w_scales;
+    q.out = out;
+    q.ldx = ldx;
+    q.ldo = ldo;
+    q.n = n;
+    q.k = k;
+    q.m = static_cast<int>(m);
+    q.kb = static_cast<int>(up(k, kBlock) / kBlock);
+    q.out_dtype = out_dtype;
+    return to_status(launch_linear(q, dtype, w_fmt, dev.sms, static_cast<cudaStream_t>(stream)));
   }
   void* codes = workspace;
   float* scales = reinterpret_cast<float*>(static_cast<char*>(workspace) + code_bytes(m, k));

@@ -42,6 +42,29 @@ struct alignas(N * sizeof(T)) Vec {
   T e[N];
 };
 
+// Launch with programmatic stream serialisation: the kernel's blocks may be placed while the stream's
+// previous kernel ends, and wait for it (kernel_begin) before they touch memory.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+__device__ __forceinline__ void kernel_begin() {
+  griddep_launch_dependents();
+  griddep_wait();
+}
+
 // ----------------------------------------------------------------------------
 // The dropout mask: 16 bits per element of a counter-based hash
 // ----------------------------------------------------------------------------

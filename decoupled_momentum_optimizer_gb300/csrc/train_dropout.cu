@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_flat(const __grid_consta
   constexpr int N = kPer16<T>;
   using V = Vec<T, N>;
   const DropMask d = drop_mask(p.drop);
+  kernel_begin();
   const long long units = n / N;
   const V* x = static_cast<const V*>(p.x);
   const V* res = static_cast<const V*>(p.residual);
@@ -83,6 +84,7 @@ template <typename T, bool RES, bool VEC>
 __global__ void __launch_bounds__(kDropThreads) dropout_groups(const __grid_constant__ DropoutParams p, long long G) {
   using V = Vec<T, 4>;
   const DropMask d = drop_mask(p.drop);
+  kernel_begin();
   const long long g = static_cast<long long>(blockIdx.x) * kDropThreads + threadIdx.x;
   if (g >= p.rows * G) return;
   // 64-bit division only where the group count needs it
@@ -114,6 +116,7 @@ template <typename T, bool RES>
 __global__ void __launch_bounds__(kDropThreads)
     dropout_segments(const __grid_constant__ DropoutParams p, long long G, long long per_row) {
   const DropMask d = drop_mask(p.drop);
+  kernel_begin();
   const int lane = threadIdx.x & 31;
   const long long s = static_cast<long long>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5);
   if (s >= p.rows * per_row) return;  // whole warps
@@ -155,18 +158,16 @@ static cudaError_t launch_dropout_t(const DropoutParams& p, cudaStream_t st) {
   if (flat) {
     const long long n = p.rows * p.cols;
     const long long units = n / kPer16<T> + 1;  // at least one block, for the last group
-    dropout_flat<T, RES><<<blocks(units, kDropThreads * kFlatUnroll), kDropThreads, 0, st>>>(p, n);
+    return launch_overlapped(dropout_flat<T, RES>, blocks(units, kDropThreads * kFlatUnroll), kDropThreads, 0, st, p, n);
   } else if (vec) {
-    dropout_groups<T, RES, true><<<blocks(p.rows * G, kDropThreads), kDropThreads, 0, st>>>(p, G);
+    return launch_overlapped(dropout_groups<T, RES, true>, blocks(p.rows * G, kDropThreads), kDropThreads, 0, st, p, G);
   } else if (p.cols < 64) {
     // A warp per segment would leave most of its lanes idle on rows this short.
-    dropout_groups<T, RES, false><<<blocks(p.rows * G, kDropThreads), kDropThreads, 0, st>>>(p, G);
+    return launch_overlapped(dropout_groups<T, RES, false>, blocks(p.rows * G, kDropThreads), kDropThreads, 0, st, p, G);
   } else {
     const long long per_row = (p.cols + 127) / 128;
-    dropout_segments<T, RES>
-        <<<blocks(p.rows * per_row, kDropThreads / 32), kDropThreads, 0, st>>>(p, G, per_row);
+    return launch_overlapped(dropout_segments<T, RES>, blocks(p.rows * per_row, kDropThreads / 32), kDropThreads, 0, st, p, G, per_row);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_dropout(const DropoutParams& p, int dtype, cudaStream_t st) {

@@ -83,4 +83,16 @@ MatmulPlan plan_matmul(long long m, long long n, int kb, int sms);
 cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st);
 cudaError_t prepare_matmul_kernels();
 
+// out = Q(x) w^T for few rows of x: see train_linear.cu.
+constexpr int kLinearRows = 32;  // most rows of x
+struct LinearParams {
+  const void* x;
+  const void* w;
+  const float* w_scales;
+  void* out;
+  long long ldx, ldo, n, k;
+  int m, kb, out_dtype;
+};
+cudaError_t launch_linear(const LinearParams& p, int dtype, int w_fmt, int sms, cudaStream_t st);
+
 }  // namespace demo

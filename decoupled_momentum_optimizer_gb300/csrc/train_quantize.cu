@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
   const long long c0 = static_cast<long long>(tile_c) * kBlock + 4 * lane;
   const int live_rows = p.rows - r0 >= 16 ? 16 : p.rows > r0 ? static_cast<int>(p.rows - r0) : 0;
   const int live_cols = p.cols - c0 >= 4 ? 4 : p.cols > c0 ? static_cast<int>(p.cols - c0) : 0;
+  kernel_begin();
   float v[16][4];
   {
     const T* x = static_cast<const T*>(p.x) + r0 * p.ldx + c0;
@@ -203,17 +204,9 @@ static cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
   // Accesses of four elements where every row's groups of four are aligned and whole.
   const bool vec = p.cols % 4 == 0 && p.ldx % 4 == 0 && at(p.x) &&
                    (p.gate == nullptr || (p.ldg % 4 == 0 && at(p.gate)));
-  if (p.gate != nullptr) {
-    if (vec)
-      quantize_kernel<T, FMT, true, true><<<grid, kQuantThreads, 0, st>>>(p);
-    else
-      quantize_kernel<T, FMT, false, true><<<grid, kQuantThreads, 0, st>>>(p);
-  } else if (vec) {
-    quantize_kernel<T, FMT, true, false><<<grid, kQuantThreads, 0, st>>>(p);
-  } else {
-    quantize_kernel<T, FMT, false, false><<<grid, kQuantThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  auto* kernel = p.gate != nullptr ? (vec ? quantize_kernel<T, FMT, true, true> : quantize_kernel<T, FMT, false, true>)
+                                   : (vec ? quantize_kernel<T, FMT, true, false> : quantize_kernel<T, FMT, false, false>);
+  return launch_overlapped(kernel, grid, kQuantThreads, 0, st, p);
 }
 
 cudaError_t launch_quantize(const QuantParams& p, int dtype, int fmt, cudaStream_t st) {

@@ -16,50 +16,73 @@ _FMT_OF = {dt: code for code, dt in FP8_FORMATS.values()}
 BLOCK = 128
 
 
-def _pkg():
-    import decoupled_momentum_optimizer_gb300 as dm
+class _Library:
+    """The library's entry points, bound on first use (these calls are made per layer and step: the
+    binding costs as much as a small kernel, so it looks nothing up twice)."""
 
-    return dm
+    def __getattr__(self, name):
+        import decoupled_momentum_optimizer_gb300 as dm
+
+        setattr(self, name, getattr(dm, name[3:]) if name.startswith("dm_") else getattr(dm.lib(), name))
+        return getattr(self, name)
 
 
-def _dtype(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32, bfloat16 or float16")
-    return _DTYPES[t.dtype]
+_lib = _Library()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(name, args, index, stream):
+    """Entry point ``name`` on ``args`` and the stream's pointer, with device ``index`` current and
+    initialised; raises on a negative status."""
+    if index in _lib.dm__inited and _current_device() == index:
+        raw = _raw_stream(index) if stream is None and _raw_stream is not None else _lib.dm__stream(stream, index)
+        status = getattr(_lib, name)(*args, raw)
+    else:
+        with _lib.dm__OnDevice(torch.device("cuda", index)):
+            status = getattr(_lib, name)(*args, _lib.dm__stream(stream, index))
+    if status:
+        _lib.dm__check(status, name)
 
 
 def _matrix(t, name, like=None, shape=None):
     """(pointer, row stride, rows, columns) of a tensor seen as rows of its last dimension."""
-    dt = _dtype(t, name)
+    try:
+        ptr, size, dt = t.data_ptr(), t.shape, t.dtype
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
     if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
-        if t.device != like.device:
+        if dt != like.dtype:
+            raise TypeError(f"{name} has dtype {dt}, expected {like.dtype}")
+        if t.get_device() != like.get_device():
             raise ValueError(f"{name} is on {t.device}, the call's other tensors on {like.device}")
         shape = like.shape
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dim() == 0:
+    elif dt not in _DTYPES:
+        raise TypeError(f"{name} has dtype {dt}, expected float32, bfloat16 or float16")
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
+    if len(size) == 2:
+        rows, cols = size
+        ld, inner = t.stride()
+        if inner != 1 and cols > 1 and rows > 0:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+        return ptr, ld, rows, cols
+    if not size:
         raise ValueError(f"{name} must have at least one dimension")
-    cols = t.shape[-1]
+    cols = size[-1]
     rows = t.numel() // cols if cols else 0
     if cols > 1 and rows > 0 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     ld = cols
-    if rows > 1:
-        if t.dim() == 2:
-            ld = t.stride(0)
-        elif not t.is_contiguous():  # leading dimensions that make one sequence of rows
-            lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
-            for (_, s), (n2, s2) in zip(lead, lead[1:]):
-                if s != n2 * s2:
-                    raise ValueError(f"{name}'s leading dimensions must have one stride between rows")
-            ld = lead[-1][1]
-    return t.data_ptr(), ld, rows, cols, dt
+    if rows > 1 and not t.is_contiguous():  # leading dimensions that make one sequence of rows
+        lead = [(n, s) for n, s in zip(size[:-1], t.stride()[:-1]) if n != 1]
+        for (_, s), (n2, s2) in zip(lead, lead[1:]):
+            if s != n2 * s2:
+                raise ValueError(f"{name}'s leading dimensions must have one stride between rows")
+        ld = lead[-1][1]
+    return ptr, ld, rows, cols
 
 
 def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
@@ -69,15 +92,15 @@ def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
     The gradient of ``x`` is ``dropout(dy, p, seed=..., step=..., site=...)`` with the same
     arguments; the residual's is ``dy``.  ``out`` may be ``x`` or ``residual`` themselves.
     """
-    dm = _pkg()
-    xp, ldx, rows, cols, dt = _matrix(x, "x")
-    with dm._OnDevice(x.device) as d:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        op, ldo = _matrix(out, "out", like=x)[:2]
-        rp, ldr = _matrix(residual, "residual", like=x)[:2] if residual is not None else (None, 0)
-        dm._check(dm.lib().demo_dropout(xp, ldx, rp, ldr, op, ldo, dt, rows, cols, p, seed, step, site,
-                                        dm._stream(stream, d.index)), "demo_dropout")
+    xp, ldx, rows, cols = _matrix(x, "x")
+    rp, ldr = _matrix(residual, "residual", x)[:2] if residual is not None else (None, 0)
+    if out is None:
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        op, ldo = out.data_ptr(), cols
+    else:
+        op, ldo = _matrix(out, "out", x)[:2]
+    _run("demo_dropout", (xp, ldx, rp, ldr, op, ldo, _DTYPES[x.dtype], rows, cols, p, seed, step, site),
+         x.get_device(), stream)
     return out
 
 
@@ -93,25 +116,29 @@ class Fp8Matrix:
     __slots__ = ("codes", "scales", "shape", "tiles")
 
     def __init__(self, codes, scales, k, *, tiles=False):
-        if codes.dim() != 2 or codes.dtype not in _FMT_OF:
+        if codes.dtype not in _FMT_OF or codes.dim() != 2:
             raise TypeError("codes must be a 2-D float8_e4m3fn or float8_e5m2 tensor")
-        rows, blocks = codes.shape[0], (k + BLOCK - 1) // BLOCK
-        if codes.shape[1] != blocks * BLOCK:
-            raise ValueError(f"codes have {codes.shape[1]} columns, expected {blocks * BLOCK} for k = {k}")
-        if scales.dtype != torch.float32 or tuple(scales.shape) != (blocks, (rows + 3) // 4 * 4):
+        rows, width = codes.shape
+        blocks = (k + BLOCK - 1) // BLOCK
+        if width != blocks * BLOCK:
+            raise ValueError(f"codes have {width} columns, expected {blocks * BLOCK} for k = {k}")
+        if scales.dtype != torch.float32 or scales.shape != (blocks, (rows + 3) // 4 * 4):
             raise ValueError(f"scales must be float32 [{blocks}, {(rows + 3) // 4 * 4}]")
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("codes and scales must be contiguous")
-        if not codes.is_cuda or scales.device != codes.device:
+        if not codes.is_cuda or scales.get_device() != codes.get_device():
             raise ValueError("codes and scales must be on one CUDA device (there is no CPU path)")
-        self.codes, self.scales, self.shape, self.tiles = codes, scales, (rows, k), bool(tiles)
+        self.codes, self.scales, self.shape, self.tiles = codes, scales, (rows, k), tiles
 
     @classmethod
     def empty(cls, rows, k, fmt="e4m3", *, tiles=False, device="cuda"):
         """Uninitialised buffers of the right sizes, for fp8_quantize's ``out``."""
-        kp = (k + BLOCK - 1) // BLOCK * BLOCK
-        codes = torch.empty(rows, kp, dtype=FP8_FORMATS[fmt][1], device=device)
-        return cls(codes, torch.empty(kp // BLOCK, (rows + 3) // 4 * 4, device=device), k, tiles=tiles)
+        q = cls.__new__(cls)
+        blocks = (k + BLOCK - 1) // BLOCK
+        q.codes = torch.empty((rows, blocks * BLOCK), dtype=FP8_FORMATS[fmt][1], device=device)
+        q.scales = torch.empty((blocks, (rows + 3) // 4 * 4), dtype=torch.float32, device=device)
+        q.shape, q.tiles = (rows, k), tiles
+        return q
 
     def dequantize(self):
         """The float32 values (torch operations: for tests and inspection)."""
@@ -130,68 +157,82 @@ def fp8_quantize(x, *, fmt="e4m3", form="rows", scales="rows", relu=False, gate=
     applied on the way in, in this order; ``gate`` zeroes the elements where it is not positive.
     ``out``    the Fp8Matrix, or the pair, to write into
     """
-    dm = _pkg()
-    if form not in ("rows", "cols", "both"):
-        raise ValueError(f"form is {form!r}, expected rows, cols or both")
-    if scales not in ("rows", "tiles"):
-        raise ValueError(f"scales is {scales!r}, expected rows or tiles")
     if fmt not in FP8_FORMATS:
         raise ValueError(f"fmt is {fmt!r}, expected one of {tuple(FP8_FORMATS)}")
-    xp, ldx, _, _, dt = _matrix(x, "x")
+    if scales != "rows" and scales != "tiles":
+        raise ValueError(f"scales is {scales!r}, expected rows or tiles")
+    tiles = scales == "tiles"
+    xp, ldx, rows, cols = _matrix(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x has {x.dim()} dimensions, expected 2")
-    rows, cols = x.shape
-    tiles = scales == "tiles"
-    with dm._OnDevice(x.device) as d:
-        gp, ldg = _matrix(gate, "gate", like=x)[:2] if gate is not None else (None, 0)
-        shapes = [s for f, s in (("rows", (rows, cols)), ("cols", (cols, rows))) if form in (f, "both")]
-        if out is None:
-            qs = [Fp8Matrix.empty(*s, fmt, tiles=tiles, device=x.device) for s in shapes]
-        else:
-            qs = list(out) if form == "both" else [out]
-            for q, s in zip(qs, shapes):
-                if q.shape != s or q.codes.dtype != FP8_FORMATS[fmt][1] or q.tiles != tiles or \
-                        q.codes.device != x.device:
-                    raise ValueError(f"out must be a {fmt} Fp8Matrix of shape {s} with {scales} scales on {x.device}")
-            if len(qs) != len(shapes):
-                raise ValueError("out must be a pair for form='both'")
-        ptrs = [None] * 4
-        for i, q in enumerate(qs):
-            at = 2 if form == "cols" else 2 * i
-            ptrs[at], ptrs[at + 1] = q.codes.data_ptr(), q.scales.data_ptr()
-        dm._check(dm.lib().demo_fp8_quantize(xp, ldx, dt, rows, cols, int(bool(relu)), gp, ldg, p, seed, step, site,
-                                             FP8_FORMATS[fmt][0], int(tiles), *ptrs, dm._stream(stream, d.index)),
-                  "demo_fp8_quantize")
-    return tuple(qs) if form == "both" else qs[0]
+    gp, ldg = _matrix(gate, "gate", x)[:2] if gate is not None else (None, 0)
+    by_rows = by_cols = None
+    if form == "both":
+        by_rows, by_cols = out if out is not None else (None, None)
+    elif form == "rows":
+        by_rows = out
+    elif form == "cols":
+        by_cols = out
+    else:
+        raise ValueError(f"form is {form!r}, expected rows, cols or both")
+    cr = sr = cc = sc = None
+    if form != "cols":
+        by_rows = _form(by_rows, rows, cols, fmt, tiles, x)
+        cr, sr = by_rows.codes.data_ptr(), by_rows.scales.data_ptr()
+    if form != "rows":
+        by_cols = _form(by_cols, cols, rows, fmt, tiles, x)
+        cc, sc = by_cols.codes.data_ptr(), by_cols.scales.data_ptr()
+    _run("demo_fp8_quantize", (xp, ldx, _DTYPES[x.dtype], rows, cols, bool(relu), gp, ldg, p, seed, step, site,
+                               FP8_FORMATS[fmt][0], tiles, cr, sr, cc, sc), x.get_device(), stream)
+    return (by_rows, by_cols) if form == "both" else by_rows if by_cols is None else by_cols
 
 
-def _out(out, shape, dtype, device):
+def _form(q, rows, k, fmt, tiles, x):
+    """A new Fp8Matrix [rows, k] beside x, or the given one if it is one."""
+    if q is None:
+        return Fp8Matrix.empty(rows, k, fmt, tiles=tiles, device=x.device)
+    if q.shape != (rows, k) or q.codes.dtype != FP8_FORMATS[fmt][1] or q.tiles != tiles or \
+            q.codes.get_device() != x.get_device():
+        raise ValueError(f"out must be a {fmt} Fp8Matrix of shape {(rows, k)} with "
+                         f"{'tiles' if tiles else 'rows'} scales on {x.device}")
+    return q
+
+
+def _out(out, shape, dtype, beside):
+    """(out or a new tensor, pointer, row stride, dtype's code)."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=beside.device)
+        return out, out.data_ptr(), shape[-1], _DTYPES[dtype]
     if dtype is not None and out.dtype != dtype:
         raise TypeError(f"out has dtype {out.dtype}, expected {dtype}")
-    if out.device != device:
-        raise ValueError(f"out is on {out.device}, the call's other tensors on {device}")
-    return out
+    if out.get_device() != beside.get_device():
+        raise ValueError(f"out is on {out.device}, the call's other tensors on {beside.device}")
+    ptr, ld = _matrix(out, "out", None, shape)[:2]
+    return out, ptr, ld, _DTYPES[out.dtype]
+
+
+def _result_dtype(out, dtype, default):
+    dtype = dtype if dtype is not None or out is not None else default
+    if dtype is not None and dtype not in _DTYPES:
+        raise TypeError(f"dtype is {dtype}, expected float32, bfloat16 or float16")
+    return dtype
 
 
 def fp8_matmul(a, b, *, out=None, dtype=None, add=False, stream=None):
     """``a b^T`` of two Fp8Matrix ([m, k] and [n, k]) into ``out`` or a new tensor of ``dtype``
     (bfloat16 by default), or added to the float32 ``out`` (demo_fp8_matmul)."""
-    dm = _pkg()
-    if a.shape[1] != b.shape[1]:
-        raise ValueError(f"a has k = {a.shape[1]}, b has k = {b.shape[1]}")
-    if a.codes.device != b.codes.device:
-        raise ValueError(f"a is on {a.codes.device}, b on {b.codes.device}")
+    (m, k), (n, kb) = a.shape, b.shape
+    if k != kb:
+        raise ValueError(f"a has k = {k}, b has k = {kb}")
+    ac, bc = a.codes, b.codes
+    index = ac.get_device()
+    if bc.get_device() != index:
+        raise ValueError(f"a is on {ac.device}, b on {bc.device}")
     if add and out is None:
         raise ValueError("add needs an out to add to")
-    (m, k), n = a.shape, b.shape[0]
-    with dm._OnDevice(a.codes.device) as d:
-        out = _out(out, (m, n), dtype or (None if out is not None else torch.bfloat16), a.codes.device)
-        op, ldo, _, _, dt = _matrix(out, "out", shape=(m, n))
-        dm._check(dm.lib().demo_fp8_matmul(a.codes.data_ptr(), a.scales.data_ptr(), _FMT_OF[a.codes.dtype],
-                                           b.codes.data_ptr(), b.scales.data_ptr(), _FMT_OF[b.codes.dtype],
-                                           m, n, k, op, ldo, dt, int(bool(add)), dm._stream(stream, d.index)), "demo_fp8_matmul")
+    out, op, ldo, dt = _out(out, (m, n), _result_dtype(out, dtype, torch.bfloat16), ac)
+    _run("demo_fp8_matmul", (ac.data_ptr(), a.scales.data_ptr(), _FMT_OF[ac.dtype], bc.data_ptr(),
+                             b.scales.data_ptr(), _FMT_OF[bc.dtype], m, n, k, op, ldo, dt, bool(add)), index, stream)
     return out
 
 
@@ -201,28 +242,27 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     or ``out`` says otherwise; ``workspace`` (uint8, only used beyond a few rows) is allocated
     through torch where it is not given.
     """
-    dm = _pkg()
-    xp, ldx, m, k, dt = _matrix(x, "x")
-    n = w.shape[0]
-    if k != w.shape[1]:
-        raise ValueError(f"x has k = {k}, w has k = {w.shape[1]}")
-    if w.codes.device != x.device:
-        raise ValueError(f"w is on {w.codes.device}, x on {x.device}")
+    xp, ldx, m, k = _matrix(x, "x")
+    n, kw = w.shape
+    if k != kw:
+        raise ValueError(f"x has k = {k}, w has k = {kw}")
+    wc, index = w.codes, x.get_device()
+    if wc.get_device() != index:
+        raise ValueError(f"w is on {wc.device}, x on {x.device}")
+    lead = x.shape[:-1]
     if k == 0:
-        m = x.shape[:-1].numel()
-    with dm._OnDevice(x.device) as d:
-        shape = (*x.shape[:-1], n)
-        out = _out(out, shape, dtype or (None if out is not None else x.dtype), x.device)
-        op, ldo, _, _, odt = _matrix(out, "out", shape=shape)
-        need = dm.lib().demo_fp8_linear_workspace(m, n, k)
-        if need and workspace is None:
+        m = lead.numel()
+    out, op, ldo, odt = _out(out, (*lead, n), _result_dtype(out, dtype, x.dtype), x)
+    need = _lib.demo_fp8_linear_workspace(m, n, k)
+    wp = None
+    if need:
+        if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        wp, wn = (workspace.data_ptr(), workspace.numel()) if need else (None, 0)
-        if need and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != x.device):
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
-        dm._check(dm.lib().demo_fp8_linear(xp, ldx, dt, w.codes.data_ptr(), w.scales.data_ptr(), _FMT_OF[w.codes.dtype],
-                                           m, n, k, op, ldo, odt, wp, wn,
-                                           dm._stream(stream, d.index)), "demo_fp8_linear")
+        wp, need = workspace.data_ptr(), workspace.numel()
+    _run("demo_fp8_linear", (xp, ldx, _DTYPES[x.dtype], wc.data_ptr(), w.scales.data_ptr(), _FMT_OF[wc.dtype], m, n, k,
+                             op, ldo, odt, wp, need), index, stream)
     return out
 
 

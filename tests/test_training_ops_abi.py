@@ -102,7 +102,7 @@ def matmul(L, **kw):
              out=p(0x5000000), ldo=200, dtype=0, add=0)
     a.update(kw)
     return L.demo_fp8_matmul(a["ac"], a["asc"], a["af"], a["bc"], a["bsc"], a["bf"], a["m"], a["n"], a["k"], a["out"],
-                            , a["ldo"], a["dtype"], a["add"], None)
+                             a["ldo"], a["dtype"], a["add"], None)
 
 
 def test_matmul_refusals(L):

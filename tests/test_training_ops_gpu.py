@@ -402,3 +402,27 @@ def test_linear_non_finite_and_empty(m):
     assert y.shape == (2, m // 2, 100) and y.dtype == torch.bfloat16
     with pytest.raises(dm.DemoError):  # too small a workspace (or, for few rows, none is needed)
         dm.fp8_linear(draw(600, 260, "f32", 47), w, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_operators_in_a_graph():
+    """The calls captured once and replayed on new contents give what they give outside."""
+    x, w = draw(200, 300, "bf16", 50), draw(260, 300, "f32", 51)
+    res = draw(200, 260, "bf16", 52)
+    qw = dm.fp8_quantize(w, scales="tiles")
+
+    def forward():
+        q = dm.fp8_quantize(x, relu=True, p=0.2, seed=1, step=2)
+        y = dm.fp8_matmul(q, qw)
+        return dm.dropout(y, 0.1, seed=1, step=2, site=1, residual=res), dm.fp8_linear(x[:3], qw)
+
+    forward()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = forward()
+    for seed in (53, 54):
+        x.copy_(draw(200, 300, "bf16", seed))
+        graph.replay()
+        want = forward()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
