@@ -79,9 +79,9 @@ struct MatmulPlan {
   int group, bn, split, rows_a, rows_b, chain;
   unsigned int grid;
 };
-MatmulPlan plan_matmul(long long m, long long n, int kb, int sms);
+MatmulPlan plan_matmul(long long m, long long n, int kb);
 cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st);
-cudaError_t prepare_matmul_kernels();
+cudaError_t prepare_matmul_kernels(int sms);
 
 // out = Q(x) w^T for few rows of x: see train_linear.cu.
 constexpr int kLinearRows = 32;  // most rows of x

@@ -311,6 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     work.blocks = p.kb;
   }
 
+  if (threadIdx.x == 32 * kLoadWarp && p.kb > 0) {
+    prefetch_tmap(&p.a);
+    prefetch_tmap(&p.b);
+    prefetch_tmap(&p.sa);
+    prefetch_tmap(&p.sb);
+    if (p.bulk_out) prefetch_tmap(&p.o);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
@@ -521,27 +528,24 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   if (G > 1 || p.split > 1) cluster_sync();  // a pair: neither CTA leaves while the other may reach its memory
   if (G == 1 && p.split > 1) {
     // each CTA joins its share of the columns, always from the first part of k to the last
-    if (warp < kSumWarps) {
-      const Tile tl = work.tile(work.first);
-      const int units = p.bn / 4, row = threadIdx.x & (kBM - 1);
-      const int hi = units * (part + 1) / p.split;
-      const uint32_t red = smem_addr(s.a);
-      for (int u = units * part / p.split + (threadIdx.x >> 7); u < hi; u += 2) {
-        float4 v[kMaxSplit];
+    const Tile tl = work.tile(work.first);
+    const int units = p.bn / 4, row = threadIdx.x & (kBM - 1);
+    const int hi = units * (part + 1) / p.split;
+    const uint32_t red = smem_addr(s.a);
+    for (int u = units * part / p.split + (threadIdx.x >> 7); u < hi && tl.m0 + row < p.m; u += kThreads / kBM) {
+      float4 v[kMaxSplit];
 #pragma unroll
-        for (int q = 0; q < kMaxSplit; ++q)
-          if (q < p.split) v[q] = load_cluster(red + (u * kBM + row) * 16, q);
+      for (int q = 0; q < kMaxSplit; ++q)
+        if (q < p.split) v[q] = load_cluster(red + (u * kBM + row) * 16, q);
 #pragma unroll
-        for (int q = 1; q < kMaxSplit; ++q)
-          if (q < p.split)
-            v[0] = make_float4(v[0].x + v[q].x, v[0].y + v[q].y, v[0].z + v[q].z, v[0].w + v[q].w);
-        if (p.out_dtype == kBF16)
-          store_four<__nv_bfloat16>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
-        else if (p.out_dtype == kF16)
-          store_four<__half>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
-        else
-          store_four<float>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
-      }
+      for (int q = 1; q < kMaxSplit; ++q)
+        if (q < p.split) v[0] = make_float4(v[0].x + v[q].x, v[0].y + v[q].y, v[0].z + v[q].z, v[0].w + v[q].w);
+      if (p.out_dtype == kBF16)
+        store_four<__nv_bfloat16>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
+      else if (p.out_dtype == kF16)
+        store_four<__half>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
+      else
+        store_four<float>(p, tl.m0 + row, tl.n0 + 4 * u, v[0]);
     }
     __syncwarp();
     cluster_sync();  // no CTA leaves while another reads its sums
@@ -553,53 +557,67 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
 }
 
 template <int G>
-static cudaError_t launch_matmul_t(const MatmulParams& p, unsigned grid, cudaStream_t st) {
+struct MatmulLaunch {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem<G>;
-  cfg.stream = st;
   cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = G == 1 ? p.split : G;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<G>, p);
-}
+  MatmulLaunch(unsigned grid, int cluster, cudaStream_t st) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem<G>;
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+  }
+};
+
+// Clusters of 1 .. kMaxSplit single CTAs, and pairs (entry 0), that the device runs at one time: a
+// cluster stays within a group of SMs, so these are fewer than the SMs divided by the size.  Filled
+// once, by the first device that is initialised (every device the library runs on is the same GPU).
+static int g_clusters[kMaxSplit + 1];
 
 // Few tiles (128 x 224 ones that would leave half of the SMs idle, or m that fills no pair): one CTA
-// per tile, with k cut into as many parts as there are SMs for, at least a chain each.  Otherwise
-// pairs, with the width whose last round is fullest: a block takes about max(2 bn, 256 + bn) cycles
-// (the tensor cores, or what the CTA reads) and a tile about 2500 more.
-MatmulPlan plan_matmul(long long m, long long n, int kb, int sms) {
+// per tile, with k cut into parts where that pays.  Otherwise pairs.  Either way the cheapest width
+// (and number of parts) in cycles: a block costs a pair max(2 bn, 256 + bn) (the tensor cores, or
+// what a CTA reads at 64 bytes a cycle) and a single CTA 256 + 2 bn; a pair's tile about 2500 more;
+// joining parts about 6000 and the reading of a tile of sums (measured at 64 x 8192 x 2048 and
+// 768 x 768 x 8192: 6000 to 9000).
+MatmulPlan plan_matmul(long long m, long long n, int kb) {
+  const int sms = g_clusters[1];
   const auto tiles = [&](int rows, int bn) { return ((m + rows - 1) / rows) * ((n + bn - 1) / bn); };
   MatmulPlan plan;
   plan.split = 1;
-  if (m <= kBM || 2 * tiles(kBM, kBN) <= sms) {
-    plan.group = 1;
-    plan.bn = n >= kBN ? kBN : static_cast<int>(n + 31) / 32 * 32;
-    if (plan.bn < 64) plan.bn = 64;
-    const long long t = tiles(kBM, plan.bn);
-    long long s = sms / t;
-    if (s > (kb + kChain - 1) / kChain) s = (kb + kChain - 1) / kChain;
-    if (s > kMaxSplit) s = kMaxSplit;
-    if (s > 1) plan.split = static_cast<int>(s);
-    plan.grid = static_cast<unsigned>(t * plan.split);
+  plan.group = m <= kBM || 2 * tiles(kBM, kBN) <= sms ? 1 : 2;
+  double best = 0;
+  const auto offer = [&](int bn, int split, double cost, long long grid) {
+    if (best == 0 || cost < best) {
+      best = cost;
+      plan.bn = bn;
+      plan.split = split;
+      plan.grid = static_cast<unsigned>(grid);
+    }
+  };
+  if (plan.group == 1) {
+    const int chains = (kb + kChain - 1) / kChain;
+    const double rows = m < kBM ? m : kBM;
+    for (int bn = kBN; bn >= 64; bn -= 32) {
+      const long long t = tiles(kBM, bn);
+      for (int split = 1; split <= kMaxSplit && (split == 1 || (split <= chains && t <= g_clusters[split])); ++split) {
+        const double rounds = static_cast<double>((t + g_clusters[split] - 1) / g_clusters[split]);
+        const double join = split > 1 ? 6000 + rows * bn / 8 : 0;
+        offer(bn, split, rounds * (((kb + split - 1) / split) * (256.0 + 2 * bn) + join + 1000), t * split);
+      }
+    }
   } else {
-    plan.group = 2;
-    const long long pairs = sms / 2;
-    double best = 0;
+    const long long pairs = g_clusters[0];
     for (int bn = kBN; bn >= 96; bn -= 32) {
       const long long t = tiles(2 * kBM, bn), rounds = (t + pairs - 1) / pairs;
-      const double cost = static_cast<double>(rounds) * (2500.0 + static_cast<double>(kb) * (256 + bn));
-      if (best == 0 || cost < best) {
-        best = cost;
-        plan.bn = bn;
-        plan.grid = static_cast<unsigned>(2 * (t < pairs ? t : pairs));
-      }
+      offer(bn, 1, static_cast<double>(rounds) * (2500.0 + static_cast<double>(kb) * (256 + bn)),
+            2 * (t < pairs ? t : pairs));
     }
   }
   plan.rows_a = kBM;
@@ -609,15 +627,33 @@ MatmulPlan plan_matmul(long long m, long long n, int kb, int sms) {
 }
 
 cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st) {
-  return plan.group == 1 ? launch_matmul_t<1>(p, plan.grid, st) : launch_matmul_t<2>(p, plan.grid, st);
+  if (plan.group == 1) {
+    MatmulLaunch<1> l(plan.grid, plan.split, st);
+    return cudaLaunchKernelEx(&l.cfg, matmul_kernel<1>, p);
+  }
+  MatmulLaunch<2> l(plan.grid, 2, st);
+  return cudaLaunchKernelEx(&l.cfg, matmul_kernel<2>, p);
 }
 
-cudaError_t prepare_matmul_kernels() {
-  const cudaError_t e = cudaFuncSetAttribute(matmul_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kSmem<1>));
+cudaError_t prepare_matmul_kernels(int sms) {
+  cudaError_t e = cudaFuncSetAttribute(matmul_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSmem<1>));
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(matmul_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kSmem<2>));
+  e = cudaFuncSetAttribute(matmul_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem<2>));
+  if (e != cudaSuccess || g_clusters[0] != 0) return e;
+  for (int size = kMaxSplit; size >= 1; --size) {
+    MatmulLaunch<1> l(static_cast<unsigned>(sms / size * size), size, nullptr);
+    l.cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&g_clusters[size], matmul_kernel<1>, &l.cfg)) != cudaSuccess) return e;
+    if (g_clusters[size] < 1) return cudaErrorInvalidConfiguration;
+  }
+  MatmulLaunch<2> l(static_cast<unsigned>(sms / 2 * 2), 2, nullptr);
+  l.cfg.numAttrs = 1;
+  int pairs = 0;
+  if ((e = cudaOccupancyMaxActiveClusters(&pairs, matmul_kernel<2>, &l.cfg)) != cudaSuccess) return e;
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  g_clusters[0] = pairs;
+  return cudaSuccess;
 }
 
 }  // namespace demo
