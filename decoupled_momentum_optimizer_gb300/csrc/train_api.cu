@@ -83,6 +83,17 @@ bool code_map(EncodeTiledFn encode, CUtensorMap* map, const void* codes, int64_t
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Codes as [block][row][128]: boxes of 4 blocks x 16 rows.
+bool block_map(EncodeTiledFn encode, CUtensorMap* map, const void* codes, int64_t rows, int64_t blocks) {
+  const cuuint64_t dims[3] = {kBlock, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(blocks) * kBlock, kBlock};
+  const cuuint32_t box[3] = {kBlock, 16, 4};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Scales: [blocks][ld] float32, boxes of `box_rows` columns and `box_blocks` rows.
 bool scale_map(EncodeTiledFn encode, CUtensorMap* map, const float* scales, int64_t rows, int64_t blocks, int box_rows,
                int box_blocks) {
@@ -254,7 +265,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
 }
 
 size_t demo_fp8_linear_workspace(int64_t m, int64_t n, int64_t k) {
-  if (m <= kLinearRows || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+  if (m <= 0 || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim || few_rows(m, k)) return 0;
   return static_cast<size_t>(code_bytes(m, k) + scale_bytes(m, k));
 }
 
@@ -282,21 +293,22 @@ int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, 
       if (overlap(rw, ro) || overlap(rw, rx) || overlap(rw, rc) || overlap(rw, rs)) return DEMO_EINVAL;
     }
   }
-  if (m <= kLinearRows) {
+  if (few_rows(m, k)) {
     DeviceInfo dev;
     if ((s = device_info(&dev)) != DEMO_OK) return s;
     LinearParams q;
     std::memset(&q, 0, sizeof(q));
+    q.kb = static_cast<int>(up(k, kBlock) / kBlock);
+    if (q.kb > 0 && (!block_map(dev.encode, &q.w, w_codes, n, q.kb) || !scale_map(dev.encode, &q.ws, w_scales, n, q.kb, 16, 4)))
+      return DEMO_ECUDA;
+    q.fault = dev.fault;
     q.x = x;
-    q.w = w_codes;
-    q.w_scales = w_scales;
     q.out = out;
     q.ldx = ldx;
     q.ldo = ldo;
     q.n = n;
     q.k = k;
     q.m = static_cast<int>(m);
-    q.kb = static_cast<int>(up(k, kBlock) / kBlock);
     q.out_dtype = out_dtype;
     return to_status(launch_linear(q, dtype, w_fmt, dev.sms, static_cast<cudaStream_t>(stream)));
   }

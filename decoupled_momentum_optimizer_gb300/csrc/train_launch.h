@@ -83,16 +83,21 @@ MatmulPlan plan_matmul(long long m, long long n, int kb);
 cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st);
 cudaError_t prepare_matmul_kernels(int sms);
 
-// out = Q(x) w^T for few rows of x: see train_linear.cu.
-constexpr int kLinearRows = 32;  // most rows of x
+// out = Q(x) w^T for few rows of x, whose codes and scales fit in shared memory: see train_linear.cu.
+constexpr int kLinearRows = 16, kLinearSmem = 68 * 1024;
+constexpr bool few_rows(long long m, long long k) {
+  return m <= kLinearRows && m * ((k + kBlock - 1) / kBlock) * (kBlock + 4) <= kLinearSmem;
+}
 struct LinearParams {
+  CUtensorMap w;   // codes as [block][row][128], boxes of 4 x 16 x 128; unused without blocks
+  CUtensorMap ws;  // scales, boxes of 4 blocks x 16 rows
   const void* x;
-  const void* w;
-  const float* w_scales;
   void* out;
   long long ldx, ldo, n, k;
   int m, kb, out_dtype;
+  unsigned int* fault;
 };
+cudaError_t prepare_linear_kernels();
 cudaError_t launch_linear(const LinearParams& p, int dtype, int w_fmt, int sms, cudaStream_t st);
 
 }  // namespace demo

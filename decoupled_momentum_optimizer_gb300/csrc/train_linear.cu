@@ -1,23 +1,38 @@
 // x w^T for a few rows of x (tokens being generated) and w in 8-bit floating point, block-scaled: one
 // kernel that quantizes x, multiplies and scales, bound by reading w once.
 //
-// A warp multiplies 16 rows of w at a time (the instruction's 16 x 32 operand) by up to 8 T tokens,
-// one block of 128 along k after another; the warps of a CTA share its rows and take the blocks in
-// turn, so that a short k still fills the machine with reads, and join their sums in order through
-// shared memory.  w goes straight from global memory to the registers the instruction reads: its k
-// order is free as long as both operands agree, so lane (g, c) takes 16 consecutive codes of row g at
-// 16 c and at 64 + 16 c, whole 16-byte loads, a block ahead of the arithmetic.  Lane (g, c) likewise
-// quantizes 32 elements of token g, the four lanes of a token sharing the block's maximum.  Every CTA
-// repeats that (at most 32 tokens), which is cheaper than a kernel of its own before this one.
+// One CTA per SM streams its rows of w through a ring of shared-memory stages: one thread keeps
+// TMA loads of 16 rows x 4 blocks (8 KB, with their scales) under way, up to 128 KB of them, while
+// sixteen warps first quantize all of x into shared memory (four lanes a block, 32 elements each;
+// every SM repeats that, behind the first stages' arrival) and then multiply.  A
+// group of four warps owns 16 rows at a time, the instruction's 16 x 32 operand, each warp one of a
+// stage's four blocks; the four join their sums in order.  The instruction's k order is free as long
+// as both operands agree, so lane (g, c) takes 16 consecutive codes of row g at 16 c and at 64 + 16 c
+// of a block, whole 16-byte reads of either operand.
 //
 // The block's 128 products accumulate in the instruction's float32, blocks in IEEE float32.
 #include "train_common.cuh"
+#include "train_tensor.cuh"
 
 namespace demo {
 
 namespace {
 
-constexpr int kLinearMaxWarps = 16;
+constexpr int kWarps = 16, kGroups = 4;
+constexpr int kThreads = 32 * (kWarps + 1);  // + one that loads
+constexpr int kQuad = 4;                     // blocks of a stage, one for each warp of a group
+constexpr int kRows = 16;
+constexpr int kStages = 16;
+
+struct LinearShared {
+  uint8_t w[kStages][kQuad][kRows][kBlock];  // 1024-byte aligned (swizzle atoms)
+  float ws[kStages][kQuad][kRows];
+  float part[kWarps][kLinearRows][kRows];
+  uint64_t full[kStages], empty[kStages];
+  volatile uint32_t dead;
+  uint32_t pad[3];  // x's codes and scales follow, 16-byte aligned
+};
+static_assert(sizeof(LinearShared) + 1024 + kLinearSmem <= 227 * 1024, "shared memory");
 
 // D += A B, 16 x 8, K = 32 codes, float32 accumulators.
 template <int WFMT>
@@ -37,160 +52,257 @@ __device__ __forceinline__ void mma_f8(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 consecutive elements of a token as float32, zero from `live` on.
+// 32 elements of a block of a token, every fourth unit of 16 bytes from unit c on; zero from `live` on.
+template <typename T>
+constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+constexpr int kUnits = 32 / kUnit<T>;
+
 template <typename T, bool VEC>
-__device__ __forceinline__ void load16(const T* p, long long live, float* v) {
-  constexpr int N = 16 / static_cast<int>(sizeof(T));
-  if (VEC && live >= 16) {
+__device__ __forceinline__ void load32(const T* block, int c, long long live, Vec<T, kUnit<T>> (&v)[kUnits<T>]) {
+  constexpr int N = kUnit<T>;
 #pragma unroll
-    for (int i = 0; i < 16 / N; ++i) {
-      const Vec<T, N> q = reinterpret_cast<const Vec<T, N>*>(p)[i];
+  for (int j = 0; j < kUnits<T>; ++j) {
+    const int at = (4 * j + c) * N;
+    if (VEC && at + N <= live) {
+      v[j] = *reinterpret_cast<const Vec<T, N>*>(block + at);
+    } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[N * i + e] = to_f32(q.e[e]);
+      for (int e = 0; e < N; ++e) v[j].e[e] = at + e < live ? block[at + e] : from_f32<T>(0.0f);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = e < live ? to_f32(p[e]) : 0.0f;
   }
 }
 
+// The larger magnitude; a NaN stays.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// Shared memory behind LinearShared: x's codes [m][128 kb] (tokens of odd number have the halves of
+// every block swapped, so that eight lanes of a 16-byte read reach different banks), scales [m][kb].
 template <typename T, bool VEC, int WFMT, int TILES>
-__global__ void __launch_bounds__(32 * kLinearMaxWarps) linear_kernel(const __grid_constant__ LinearParams p) {
-  extern __shared__ float part[];  // [warps][8 TILES tokens][16 rows]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  const long long n0 = static_cast<long long>(blockIdx.x) * 16;
-  // rows past the end repeat the last one (their results are not written)
-  const long long r0 = n0 + g < p.n ? n0 + g : p.n - 1, r1 = n0 + g + 8 < p.n ? n0 + g + 8 : p.n - 1;
-  const long long kp = static_cast<long long>(p.kb) * kBlock, ldw = (p.n + 3) / 4 * 4;
-  const uint8_t* w0 = static_cast<const uint8_t*>(p.w) + r0 * kp + 16 * c;
-  const uint8_t* w1 = static_cast<const uint8_t*>(p.w) + r1 * kp + 16 * c;
+__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
+  extern __shared__ uint8_t raw[];
+  LinearShared& s = *reinterpret_cast<LinearShared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* codes = reinterpret_cast<uint8_t*>(&s + 1);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int kp = p.kb * kBlock;
+  float* scales = reinterpret_cast<float*>(codes + p.m * kp);
+  // This CTA's rows of w, 16 at a time: row blocks blockIdx.x, + gridDim.x, ..; group j takes the j-th,
+  // j + 4-th ..  Stages come in rounds of up to four row blocks, `quads` stages each, in turn.
+  const int row_blocks = static_cast<int>((p.n + kRows - 1) / kRows);
+  const int own = (row_blocks - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int quads = (p.kb + kQuad - 1) / kQuad;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kQuad);
+    }
+    s.dead = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32 * kWarps && p.kb > 0) {
+    prefetch_tmap(&p.w);
+    prefetch_tmap(&p.ws);
+  }
+  __syncthreads();
   kernel_begin();
 
-  float sum[TILES][4];
-#pragma unroll
-  for (int t = 0; t < TILES; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[t][e] = 0.0f;
-  uint4 a[2][2];  // [row][half] of the block to come
-  float s0 = 0.0f, s1 = 0.0f;
-  const auto fetch = [&](int kb) {
-    const long long at = static_cast<long long>(kb) * kBlock;
-    a[0][0] = *reinterpret_cast<const uint4*>(w0 + at);
-    a[0][1] = *reinterpret_cast<const uint4*>(w0 + at + 64);
-    a[1][0] = *reinterpret_cast<const uint4*>(w1 + at);
-    a[1][1] = *reinterpret_cast<const uint4*>(w1 + at + 64);
-    s0 = p.w_scales[kb * ldw + r0];
-    s1 = p.w_scales[kb * ldw + r1];
-  };
-  if (warp < p.kb) fetch(warp);
-  for (int kb = warp; kb < p.kb; kb += warps) {
-    uint32_t b[TILES][2][4];
-    float sx[TILES];
-    const long long k0 = static_cast<long long>(kb) * kBlock + 16 * c;
-#pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      const int m = 8 * t + g;
-      float v[32];
-      const T* x = static_cast<const T*>(p.x) + m * p.ldx + k0;
-      load16<T, VEC>(x, m < p.m ? p.k - k0 : 0, v);
-      load16<T, VEC>(x + 64, m < p.m ? p.k - k0 - 64 : 0, v + 16);
+  if (warp == kWarps) {
+    named_sync(6, kThreads);
+    if (elect_one()) {
+      Ring<kStages> st;
+      bool ok = true;
+      uint32_t used = 0;
+      for (int first = 0; ok && first < own; first += kGroups) {
+        const int live = own - first < kGroups ? own - first : kGroups;
+        for (int q = 0; ok && q < quads; ++q) {
+          for (int j = 0; j < live; ++j) {
+            if (!(ok = wait_bounded<false>(&s.dead, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
+            const int row = static_cast<int>(blockIdx.x + (first + j) * gridDim.x) * kRows;
+            mbar_expect_tx(&s.full[st.slot], kQuad * kRows * (kBlock + 4));
+            tma_load_3d(s.w[st.slot], &p.w, &s.full[st.slot], 0, row, kQuad * q);
+            tma_load_2d(s.ws[st.slot], &p.ws, &s.full[st.slot], row, kQuad * q);
+            used |= 1u << st.slot;
+            st.next();
+          }
+        }
+      }
+      if (!ok)  // stopped early: wait (bounded) for the copies that are under way
+        for (int i = 0; i < kStages; ++i)
+          if (used >> i & 1u) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
+    }
+  } else {
+    // ---- x: a warp quantizes eight blocks of 128 at a time, four lanes each, 32 elements a lane ----
+    const int blocks = p.m * p.kb, c4 = lane & 3;
+    for (int first = 8 * warp; first < blocks; first += 8 * kWarps) {
+      const int i = first + (lane >> 2) < blocks ? first + (lane >> 2) : blocks - 1;  // block kb of token m
+      const int m = i / p.kb, kb = i - m * p.kb;
+      Vec<T, kUnit<T>> v[kUnits<T>];
+      load32<T, VEC>(static_cast<const T*>(p.x) + m * p.ldx + static_cast<long long>(kb) * kBlock, c4,
+                     p.k - static_cast<long long>(kb) * kBlock, v);
+      if (first < 8 * kWarps) named_arrive(6, kThreads);  // w may be asked for: what follows waits behind it
       float top = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        v[e] = finite_or_nan(v[e]);
-        top = fmaxf(top, fabsf(v[e]));
+      for (int j = 0; j < kUnits<T>; ++j)
+#pragma unroll
+        for (int e = 0; e < kUnit<T>; ++e) top = max_magnitude(top, to_f32(v[j].e[e]));
+      if (!(top <= 3.402823466e38f)) {  // an infinity or a NaN: the others' maximum
+        top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kUnits<T>; ++j)
+#pragma unroll
+          for (int e = 0; e < kUnit<T>; ++e) {
+            const float f = finite_or_nan(to_f32(v[j].e[e]));
+            v[j].e[e] = from_f32<T>(f);
+            top = fmaxf(top, fabsf(f));
+          }
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = scale_exponent(__float_as_uint(top), fmt_top(kE4M3));
-      const float inv = pow2f(-e);
-      sx[t] = pow2f(e);
+      const int ex = scale_exponent(__float_as_uint(top), fmt_top(kE4M3));
+      const float inv = pow2f(-ex);
+      uint8_t* dst = codes + i * kBlock;
+      const int flip = (m & 1) << 6;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        b[t][q >> 2][q & 3] = codes4<kE4M3>(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+      for (int j = 0; j < kUnits<T>; ++j) {
+        const int at = ((4 * j + c4) * kUnit<T>) ^ flip;
+#pragma unroll
+        for (int e = 0; e < kUnit<T>; e += 4)
+          *reinterpret_cast<uint32_t*>(dst + at + e) =
+              codes4<kE4M3>(to_f32(v[j].e[e]) * inv, to_f32(v[j].e[e + 1]) * inv, to_f32(v[j].e[e + 2]) * inv,
+                            to_f32(v[j].e[e + 3]) * inv);
+      }
+      if (c4 == 0) scales[i] = pow2f(ex);
     }
-    const uint4 x00 = a[0][0], x01 = a[0][1], x10 = a[1][0], x11 = a[1][1];
-    const float t0 = s0, t1 = s1;
-    if (kb + warps < p.kb) fetch(kb + warps);
+    if (8 * warp >= blocks) named_arrive(6, kThreads);
+    named_sync(1, 32 * kWarps);
+
+    // ---- products ----
+    const int group = warp >> 2, w4 = warp & 3, g = lane >> 2, c = lane & 3;
+    bool ok = true;
+    int base = 0;  // the round's first stage, counted from the start
+    for (int first = 0; ok && first + group < own; first += kGroups) {
+      const int live = own - first < kGroups ? own - first : kGroups;
+      float sum[TILES][4];
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma_f8<WFMT>(d, x00.x, x10.x, x00.y, x10.y, b[t][0][0], b[t][0][1]);
-      mma_f8<WFMT>(d, x00.z, x10.z, x00.w, x10.w, b[t][0][2], b[t][0][3]);
-      mma_f8<WFMT>(d, x01.x, x11.x, x01.y, x11.y, b[t][1][0], b[t][1][1]);
-      mma_f8<WFMT>(d, x01.z, x11.z, x01.w, x11.w, b[t][1][2], b[t][1][3]);
-      // this lane's results are rows g, g + 8 and tokens 2 c, 2 c + 1, whose scales lanes 8 c, 8 c + 4 hold
-      const float u0 = __shfl_sync(0xffffffffu, sx[t], 8 * c), u1 = __shfl_sync(0xffffffffu, sx[t], 8 * c + 4);
-      sum[t][0] = fmaf(d[0] * t0, u0, sum[t][0]);
-      sum[t][1] = fmaf(d[1] * t0, u1, sum[t][1]);
-      sum[t][2] = fmaf(d[2] * t1, u0, sum[t][2]);
-      sum[t][3] = fmaf(d[3] * t1, u1, sum[t][3]);
+      for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[t][e] = 0.0f;
+      for (int q = 0; q < quads; ++q) {
+        const int i = base + q * live + group, slot = i % kStages, kb = kQuad * q + w4;
+        ok = __all_sync(0xffffffffu, wait_bounded<false>(&s.dead, &s.full[slot], i / kStages & 1, p.fault));
+        if (!ok) break;
+        // unit u of row r is at u ^ (r & 7)
+        const uint8_t* w0 = s.w[slot][w4][g];
+        const uint8_t* w1 = s.w[slot][w4][g + 8];
+        const uint4 x00 = *reinterpret_cast<const uint4*>(w0 + ((c ^ g) << 4));
+        const uint4 x01 = *reinterpret_cast<const uint4*>(w0 + (((c + 4) ^ g) << 4));
+        const uint4 x10 = *reinterpret_cast<const uint4*>(w1 + ((c ^ g) << 4));
+        const uint4 x11 = *reinterpret_cast<const uint4*>(w1 + (((c + 4) ^ g) << 4));
+        const float s0 = s.ws[slot][w4][g], s1 = s.ws[slot][w4][g + 8];
+        if (kb < p.kb) {
+#pragma unroll
+          for (int t = 0; t < TILES; ++t) {
+            const int m = 8 * t + g, m0 = 8 * t + 2 * c;
+            uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+            if (m < p.m) {
+              const uint8_t* x = codes + m * kp + kb * kBlock + 16 * c;
+              b0 = *reinterpret_cast<const uint4*>(x + ((g & 1) << 6));
+              b1 = *reinterpret_cast<const uint4*>(x + ((~g & 1) << 6));
+            }
+            // this lane's results are rows g, g + 8 and tokens 2 c, 2 c + 1
+            const float u0 = m0 < p.m ? scales[m0 * p.kb + kb] : 0.0f;
+            const float u1 = m0 + 1 < p.m ? scales[(m0 + 1) * p.kb + kb] : 0.0f;
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_f8<WFMT>(d, x00.x, x10.x, x00.y, x10.y, b0.x, b0.y);
+            mma_f8<WFMT>(d, x00.z, x10.z, x00.w, x10.w, b0.z, b0.w);
+            mma_f8<WFMT>(d, x01.x, x11.x, x01.y, x11.y, b1.x, b1.y);
+            mma_f8<WFMT>(d, x01.z, x11.z, x01.w, x11.w, b1.z, b1.w);
+            sum[t][0] = fmaf(d[0] * s0, u0, sum[t][0]);
+            sum[t][1] = fmaf(d[1] * s0, u1, sum[t][1]);
+            sum[t][2] = fmaf(d[2] * s1, u0, sum[t][2]);
+            sum[t][3] = fmaf(d[3] * s1, u1, sum[t][3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) arrive_here(&s.empty[slot]);
+      }
+      base += live * quads;
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        float* q = &s.part[warp][8 * t + 2 * c][g];
+        q[0] = sum[t][0];
+        q[kRows] = sum[t][1];
+        q[8] = sum[t][2];
+        q[kRows + 8] = sum[t][3];
+      }
+      named_sync(2 + group, 32 * kQuad);
+      const long long n0 = static_cast<long long>(blockIdx.x + static_cast<long long>(first + group) * gridDim.x) * kRows;
+      for (int i = 32 * w4 + lane; ok && i < p.m * kRows; i += 32 * kQuad) {
+        const int m = i / kRows, r = i % kRows;
+        const long long n = n0 + r;
+        if (n >= p.n) continue;
+        float v = s.part[4 * group][m][r];
+#pragma unroll
+        for (int j = 1; j < kQuad; ++j) v += s.part[4 * group + j][m][r];
+        const long long at = m * p.ldo + n;
+        if (p.out_dtype == kF32)
+          static_cast<float*>(p.out)[at] = v;
+        else if (p.out_dtype == kBF16)
+          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+        else
+          static_cast<__half*>(p.out)[at] = __float2half_rn(v);
+      }
+      named_sync(2 + group, 32 * kQuad);  // the sums are read before the next rows' are written
     }
-  }
-#pragma unroll
-  for (int t = 0; t < TILES; ++t) {
-    float* q = part + (warp * 8 * TILES + 8 * t + 2 * c) * 16 + g;
-    q[0] = sum[t][0];
-    q[16] = sum[t][1];
-    q[8] = sum[t][2];
-    q[24] = sum[t][3];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 8 * TILES * 16; i += blockDim.x) {
-    const int m = i >> 4;
-    const long long n = n0 + (i & 15);
-    if (m >= p.m || n >= p.n) continue;
-    float v = part[i];
-    for (int w = 1; w < warps; ++w) v += part[w * 8 * TILES * 16 + i];
-    const long long at = m * p.ldo + n;
-    if (p.out_dtype == kF32)
-      static_cast<float*>(p.out)[at] = v;
-    else if (p.out_dtype == kBF16)
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-    else
-      static_cast<__half*>(p.out)[at] = __float2half_rn(v);
   }
 }
-
-struct LinearShape {
-  unsigned grid, threads;
-  size_t smem;
-  int tiles;
-  cudaStream_t st;
-};
 
 template <typename T, bool VEC, int WFMT>
-cudaError_t launch_tiles(const LinearParams& p, const LinearShape& s) {
-  auto* kernel = s.tiles == 1   ? linear_kernel<T, VEC, WFMT, 1>
-                 : s.tiles == 2 ? linear_kernel<T, VEC, WFMT, 2>
-                                : linear_kernel<T, VEC, WFMT, 4>;
-  return launch_overlapped(kernel, s.grid, s.threads, s.smem, s.st, p);
+auto* pick_tiles(int m) {
+  return m <= 8 ? linear_kernel<T, VEC, WFMT, 1> : linear_kernel<T, VEC, WFMT, 2>;
 }
-
+template <typename T, bool VEC>
+auto* pick_format(int w_fmt, int m) {
+  return w_fmt == kE4M3 ? pick_tiles<T, VEC, kE4M3>(m) : pick_tiles<T, VEC, kE5M2>(m);
+}
 template <typename T>
-cudaError_t launch_linear_t(const LinearParams& p, int w_fmt, const LinearShape& s) {
-  const bool vec = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (p.m == 1 || p.ldx * sizeof(T) % 16 == 0);
-  if (w_fmt == kE4M3) return vec ? launch_tiles<T, true, kE4M3>(p, s) : launch_tiles<T, false, kE4M3>(p, s);
-  return vec ? launch_tiles<T, true, kE5M2>(p, s) : launch_tiles<T, false, kE5M2>(p, s);
+auto* pick_vec(bool vec, int w_fmt, int m) {
+  return vec ? pick_format<T, true>(w_fmt, m) : pick_format<T, false>(w_fmt, m);
+}
+auto* pick(int dtype, bool vec, int w_fmt, int m) {
+  return dtype == kF32    ? pick_vec<float>(vec, w_fmt, m)
+         : dtype == kBF16 ? pick_vec<__nv_bfloat16>(vec, w_fmt, m)
+                          : pick_vec<__half>(vec, w_fmt, m);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearParams& p, int dtype, int w_fmt, int sms, cudaStream_t st) {
-  const long long ctas = (p.n + 15) / 16;
-  // Eight warps a CTA fill the machine's reads when there are CTAs for every SM, sixteen when not.
-  int warps = ctas > sms ? 8 : kLinearMaxWarps;
-  if (warps > p.kb) warps = p.kb > 0 ? p.kb : 1;
-  LinearShape s;
-  s.tiles = p.m <= 8 ? 1 : p.m <= 16 ? 2 : 4;
-  s.grid = static_cast<unsigned>(ctas);
-  s.threads = 32 * warps;
-  s.smem = static_cast<size_t>(warps) * 8 * s.tiles * 16 * sizeof(float);
-  s.st = st;
-  if (dtype == kF32) return launch_linear_t<float>(p, w_fmt, s);
-  if (dtype == kBF16) return launch_linear_t<__nv_bfloat16>(p, w_fmt, s);
-  return launch_linear_t<__half>(p, w_fmt, s);
+  const size_t size = dtype == kF32 ? 4 : 2;
+  // 16-byte units of x: every row starts on one
+  const bool vec = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 &&
+                   (p.m == 1 || static_cast<size_t>(p.ldx) * size % 16 == 0);
+  const long long row_blocks = (p.n + kRows - 1) / kRows;
+  const size_t smem = sizeof(LinearShared) + 1024 + static_cast<size_t>(p.m) * p.kb * (kBlock + 4);
+  return launch_overlapped(pick(dtype, vec, w_fmt, p.m), static_cast<unsigned>(row_blocks < sms ? row_blocks : sms),
+                           kThreads, smem, st, p);
+}
+
+cudaError_t prepare_linear_kernels() {
+  for (int dtype : {kF32, kBF16, kF16})
+    for (int i = 0; i < 8; ++i) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(pick(dtype, i & 1, i & 2 ? kE5M2 : kE4M3, i & 4 ? 16 : 8),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(sizeof(LinearShared) + 1024 + kLinearSmem));
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
 }
 
 }  // namespace demo

@@ -67,28 +67,11 @@ static_assert(kSmem<1> <= 227 * 1024 && kSmem<2> <= 227 * 1024, "shared memory")
 // A split tile's float32 sums go where the stages were.
 static_assert(kBM * kBN * 4 <= Shared<1>::kStages * (Shared<1>::kABytes + Shared<1>::kBBytes), "a tile of sums");
 
-// Phase `parity` of `bar`, or false once any wait of the CTA has given up.
 template <int G>
 __device__ __forceinline__ bool wait_or_dead(Shared<G>& s, uint64_t* bar, uint32_t parity, unsigned int* fault) {
-  uint64_t t0 = 0;  // read late: the timer itself is slow to read, and most waits are short
-  for (uint32_t it = 1;; ++it) {
-    if (G == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 255u) == 0u) {
-      if (s.dead) return false;
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitLimitNs) {
-        s.dead = 1;
-        atomicOr(fault, kFaultLoadTimeout);
-        return false;
-      }
-    }
-  }
+  return wait_bounded<G != 1>(&s.dead, bar, parity, fault);
 }
 
-__device__ __forceinline__ void arrive_here(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
 // An arrival on the barrier of the CTA whose thread issues the matrix instructions.  RELEASE: it
 // publishes writes to shared memory; reads of tensor memory are ordered by the tensor-core fences
 // alone, and a release to the cluster would hold the warp up.
@@ -99,19 +82,6 @@ __device__ __forceinline__ void arrive_at_issuer(uint64_t* bar) {
   else
     mbar_arrive_at<RELEASE>(bar, 0);
 }
-
-// A position in a ring of N slots: the slot, and the parity of its current phase.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
 
 struct Tile {
   int m0, n0;
@@ -584,8 +554,8 @@ static int g_clusters[kMaxSplit + 1];
 // per tile, with k cut into parts where that pays.  Otherwise pairs.  Either way the cheapest width
 // (and number of parts) in cycles: a block costs a pair max(2 bn, 256 + bn) (the tensor cores, or
 // what a CTA reads at 64 bytes a cycle) and a single CTA 256 + 2 bn; a pair's tile about 2500 more;
-// joining parts about 6000 and the reading of a tile of sums (measured at 64 x 8192 x 2048 and
-// 768 x 768 x 8192: 6000 to 9000).
+// joining parts about 9000 and the reading of a tile of sums (64 x 8192 x 2048 and 768 x 768 x 8192
+// spent 6000 to 9000 on it; at 6000 here, 32 x 8192 x 2048 was cut and took 15.0 us of 12.3).
 MatmulPlan plan_matmul(long long m, long long n, int kb) {
   const int sms = g_clusters[1];
   const auto tiles = [&](int rows, int bn) { return ((m + rows - 1) / rows) * ((n + bn - 1) / bn); };
@@ -608,7 +578,7 @@ MatmulPlan plan_matmul(long long m, long long n, int kb) {
       const long long t = tiles(kBM, bn);
       for (int split = 1; split <= kMaxSplit && (split == 1 || (split <= chains && t <= g_clusters[split])); ++split) {
         const double rounds = static_cast<double>((t + g_clusters[split] - 1) / g_clusters[split]);
-        const double join = split > 1 ? 6000 + rows * bn / 8 : 0;
+        const double join = split > 1 ? 9000 + rows * bn / 8 : 0;
         offer(bn, split, rounds * (((kb + split - 1) / split) * (256.0 + 2 * bn) + join + 1000), t * split);
       }
     }

@@ -136,6 +136,23 @@ __device__ __forceinline__ float4 load_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// A barrier of the CTA among `threads` threads (whole warps).
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // One lane of a converged warp (the same one every time).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -234,5 +251,43 @@ __host__ __device__ constexpr uint32_t mxf8_instruction(int a_fmt, int b_fmt, in
 __host__ __device__ constexpr uint32_t mxf8_scale_byte(int byte) {
   return (static_cast<uint32_t>(byte) << 4) | (static_cast<uint32_t>(byte) << 29);
 }
+
+// Phase `parity` of `bar` (of the cluster's arrivals, if CLUSTER), or false once any such wait of the
+// CTA has given up: the first to do so sets `dead` and the fault word.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_bounded(volatile uint32_t* dead, uint64_t* bar, uint32_t parity,
+                                             unsigned int* fault) {
+  uint64_t t0 = 0;  // read late: the timer itself is slow to read, and most waits are short
+  for (uint32_t it = 1;; ++it) {
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0u) {
+      if (*dead) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        *dead = 1;
+        atomicOr(fault, kFaultLoadTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void arrive_here(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A position in a ring of N slots: the slot, and the parity of its current phase.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 }  // namespace demo
