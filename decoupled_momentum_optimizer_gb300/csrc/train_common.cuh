@@ -83,6 +83,16 @@ struct DropMask {
   __device__ __forceinline__ bool keep(uint64_t h, int lane) const {
     return ((static_cast<uint32_t>(h >> (16 * lane))) & 0xffffu) >= threshold;
   }
+  // All four elements of a group, with one comparison of 32 bits each: a half's high 16 bits compare as
+  // they are, its low ones after a shift (a threshold of 65536 has no such form).
+  __device__ __forceinline__ void keep4(uint64_t h, bool (&keep)[4]) const {
+    const uint32_t lo = static_cast<uint32_t>(h), hi = static_cast<uint32_t>(h >> 32), t = threshold << 16;
+    const bool any = threshold < 65536u;
+    keep[0] = any && (lo << 16) >= t;
+    keep[1] = any && lo >= t;
+    keep[2] = any && (hi << 16) >= t;
+    keep[3] = any && hi >= t;
+  }
   // A dropped element is 0 whatever it held, an infinity or a NaN included.
   __device__ __forceinline__ float apply(float v, uint64_t h, int lane) const {
     return keep(h, lane) ? v * scale : 0.0f;
@@ -101,7 +111,8 @@ inline __device__ DropMask drop_mask(const DropParams& d) { return DropMask{d.ke
 // significand is above 1.75.
 __device__ __forceinline__ int scale_exponent(uint32_t bits, int top) {
   if (bits == 0) return 0;
-  const int e = static_cast<int>(bits >> 23) - 127 - top + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  // 0x1fffff carries into the exponent where the significand's bits are above 0x600000 (1.75)
+  const int e = static_cast<int>((bits + 0x1fffffu) >> 23) - 127 - top;
   return e < -126 ? -126 : e;
 }
 

@@ -12,8 +12,10 @@
 //
 // A CTA owns a 128 x 128 tile and keeps it in registers: warp w holds rows 16 w .. 16 w + 15, lane
 // l their columns 4 l .. 4 l + 3, all 16 row loads in flight at once.  A row's block is one warp's
-// 128 elements (one warp-wide maximum each), a column's block is 16 registers of a lane and the 8
-// warps' maxima in shared memory.  Row codes leave as 128 contiguous bytes per row; column codes
+// 128 elements (one warp-wide maximum each; lane i then works out row i's scale for all), a column's
+// block is 16 registers of a lane and the 8 warps' maxima in shared memory.  Infinities and NaN are
+// found by a multiply-add with 0 per element and mended only where there are any: the integer and
+// compare pipe, not HBM, limits 16-bit inputs, so it does as little as it can per element.  Row codes leave as 128 contiguous bytes per row; column codes
 // are packed 16 rows at a time from the same registers, and leave through a swizzled 16 KB tile in
 // shared memory as 128 contiguous bytes per column.  Bound by HBM: the matrix is read once and each
 // form written once.
@@ -28,6 +30,12 @@ struct QuantShared {
   uint32_t warpmax[8];
   uint4 codes[kBlock * 8];  // column codes, 8 units of 16 rows per column, swizzled
 };
+
+__device__ __forceinline__ float relu_nan(float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void load4(const T* p, int live, float (&v)[4]) {
@@ -76,7 +84,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] = v[i][e] < 0.0f ? 0.0f : v[i][e];
+      for (int e = 0; e < 4; ++e) v[i][e] = relu_nan(v[i][e]);
   }
   if (p.drop.threshold != 0) {
     const DropMask d = drop_mask(p.drop);
@@ -84,18 +92,28 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
     unsigned long long g = static_cast<unsigned long long>(r0) * G + static_cast<unsigned long long>(c0 / 4);
 #pragma unroll
     for (int i = 0; i < 16; ++i, g += G) {
-      const uint64_t h = d.group(g);
+      bool keep[4];
+      d.keep4(d.group(g), keep);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] = d.apply(v[i][e], h, e);
+      for (int e = 0; e < 4; ++e) v[i][e] = keep[e] ? v[i][e] * d.scale : 0.0f;
     }
   }
+  {
+    float odd = 0.0f;  // NaN once an element is infinite or NaN
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 16; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[i][e] = finite_or_nan(v[i][e]);
+      for (int e = 0; e < 4; ++e) odd = fmaf(v[i][e], 0.0f, odd);
+    if (__any_sync(0xffffffffu, odd != odd)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = finite_or_nan(v[i][e]);
+    }
+  }
 
   constexpr int top = fmt_top(FMT);
-  // Float bits of non-negative values order as unsigned integers.
+  // Float bits of non-negative values order as unsigned integers.  (fmaxf passes over a NaN.)
   uint32_t rowbits[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i)
@@ -117,20 +135,27 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
   if (p.codes_rows != nullptr) {
     const long long kp = static_cast<long long>(p.col_blocks) * kBlock;
     uint8_t* dst = static_cast<uint8_t*>(p.codes_rows) + r0 * kp + c0;
-    float mine = 1.0f;  // lane i: the scale of row i
+    int mine = tile_e;  // lane i: the exponent of row i
+    if (!p.tiles) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t r = __reduce_max_sync(0xffffffffu, rowbits[i]);
+        if (lane == i) m = r;
+      }
+      mine = scale_exponent(m, top);
+    }
+    const float inverse = pow2f(-mine);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int e = p.tiles ? tile_e : scale_exponent(__reduce_max_sync(0xffffffffu, rowbits[i]), top);
-      const float inv = pow2f(-e);
-      if (lane == i) mine = pow2f(e);
-      if (i < live_rows)
-        *reinterpret_cast<uint32_t*>(dst + i * kp) =
-            codes4<FMT>(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+      const float inv = __shfl_sync(0xffffffffu, inverse, i);
+      if (i < live_rows) *reinterpret_cast<uint32_t*>(dst) = codes4<FMT>(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+      dst += kp;
     }
     // rows past the matrix up to the scales' stride hold 1
     const long long lds = (p.rows + 3) / 4 * 4;
     if (lane < 16 && r0 + lane < lds)
-      p.scales_rows[static_cast<long long>(tile_c) * lds + r0 + lane] = r0 + lane < p.rows ? mine : 1.0f;
+      p.scales_rows[static_cast<long long>(tile_c) * lds + r0 + lane] = r0 + lane < p.rows ? pow2f(mine) : 1.0f;
   }
   if (p.codes_cols != nullptr) {
     float inv[4];

@@ -191,7 +191,25 @@ def test_quantize_non_finite(form, tiles):
     check_quantized(x, "e5m2", tiles, form)
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("p", [0.3, 0.999])
+def test_quantize_dropout_at_the_ends_of_the_range(p, tiles):
+    """Blocks next to float32's smallest and largest values, whose products with dropout's factor
+    underflow or overflow: v is what float32 makes of x * factor, not finite values are NaN codes."""
+    x = draw(260, 256, "f32", 27)
+    x[:20] *= 1e-44
+    x[20:40] *= 1e-38
+    x[40:60] *= 1e-33
+    x[128:140] = x[128:140].clamp(-3, 3) * 1e38
+    x[140, 5] = 3.3e38
+    keep = ref.keep_mask(260, 256, p, 1, 2, 3)
+    with np.errstate(over="ignore"):
+        v = np.where(keep, x.cpu().numpy() * np.float32(ref.drop_scale(p)), np.float32(0))
+    check_quantized(x, "e4m3", tiles, "both", values=v.astype(np.float64), p=p, seed=1, step=2, site=3)
+    check_quantized(x, "e5m2", tiles, "both", values=v.astype(np.float64), p=p, seed=1, step=2, site=3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("act", ["relu", "gate", "both"])
 @pytest.mark.parametrize("p", [0.0, 0.25])
 @pytest.mark.parametrize("cols,pad", [(260, 0), (131, 2)])
