@@ -10,10 +10,10 @@
 // the same dropout mask), run in registers on the way, so the activation between them and the
 // quantized product is never stored in 16 or 32 bits.
 //
-// A CTA owns a 128 x 128 tile and keeps it in registers: warp w holds rows 16 w .. 16 w + 15, lane
-// l their columns 4 l .. 4 l + 3, all 16 row loads in flight at once.  A row's block is one warp's
+// A CTA owns a 128 x 128 tile and keeps it in registers: warp w holds rows 8 w .. 8 w + 7, lane
+// l their columns 4 l .. 4 l + 3, all row loads in flight at once.  A row's block is one warp's
 // 128 elements (one warp-wide maximum each; lane i then works out row i's scale for all), a column's
-// block is 16 registers of a lane and the 8 warps' maxima in shared memory.  Infinities and NaN are
+// block is 8 registers of a lane and the 16 warps' maxima in shared memory.  Infinities and NaN are
 // found by a multiply-add with 0 per element and mended only where there are any: the integer and
 // compare pipe, not HBM, limits 16-bit inputs, so it does as little as it can per element.  Row codes leave as 128 contiguous bytes per row; column codes
 // are packed 16 rows at a time from the same registers, and leave through a swizzled 16 KB tile in
@@ -23,12 +23,14 @@
 
 namespace demo {
 
-constexpr int kQuantThreads = 256;
+constexpr int kQuantWarps = 16, kQuantThreads = 32 * kQuantWarps;
+constexpr int kPer = kBlock / kQuantWarps;  // rows of a warp
 
 struct QuantShared {
-  float colmax[8][kBlock];  // each warp's column maxima (the tile's maximum uses the first column)
-  uint32_t warpmax[8];
-  uint4 codes[kBlock * 8];  // column codes, 8 units of 16 rows per column, swizzled
+  float colmax[kQuantWarps][kBlock];  // each warp's column maxima
+  float colinv[kBlock];               // 1 / each column's scale
+  uint32_t warpmax[kQuantWarps];
+  uint2 codes[kBlock * kQuantWarps];  // column codes, 16 units of 8 rows per column, swizzled
 };
 
 __device__ __forceinline__ float relu_nan(float v) {
@@ -55,25 +57,25 @@ __device__ __forceinline__ void load4(const T* p, int live, float (&v)[4]) {
 }
 
 template <typename T, int FMT, bool VEC, bool GATE>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid_constant__ QuantParams p) {
   __shared__ QuantShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned tile_r = blockIdx.x / p.col_blocks, tile_c = blockIdx.x - tile_r * p.col_blocks;
-  const long long r0 = static_cast<long long>(tile_r) * kBlock + 16 * warp;
+  const long long r0 = static_cast<long long>(tile_r) * kBlock + kPer * warp;
   const long long c0 = static_cast<long long>(tile_c) * kBlock + 4 * lane;
-  const int live_rows = p.rows - r0 >= 16 ? 16 : p.rows > r0 ? static_cast<int>(p.rows - r0) : 0;
+  const int live_rows = p.rows - r0 >= kPer ? kPer : p.rows > r0 ? static_cast<int>(p.rows - r0) : 0;
   const int live_cols = p.cols - c0 >= 4 ? 4 : p.cols > c0 ? static_cast<int>(p.cols - c0) : 0;
   kernel_begin();
-  float v[16][4];
+  float v[kPer][4];
   {
     const T* x = static_cast<const T*>(p.x) + r0 * p.ldx + c0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) load4<T, VEC>(x + i * p.ldx, i < live_rows ? live_cols : 0, v[i]);
+    for (int i = 0; i < kPer; ++i) load4<T, VEC>(x + i * p.ldx, i < live_rows ? live_cols : 0, v[i]);
   }
   if constexpr (GATE) {
     const T* g = static_cast<const T*>(p.gate) + r0 * p.ldg + c0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kPer; ++i) {
       float h[4];
       load4<T, VEC>(g + i * p.ldg, i < live_rows ? live_cols : 0, h);
 #pragma unroll
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
   }
   if (p.relu) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < kPer; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[i][e] = relu_nan(v[i][e]);
   }
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
     const unsigned long long G = static_cast<unsigned long long>((p.cols + 3) / 4);
     unsigned long long g = static_cast<unsigned long long>(r0) * G + static_cast<unsigned long long>(c0 / 4);
 #pragma unroll
-    for (int i = 0; i < 16; ++i, g += G) {
+    for (int i = 0; i < kPer; ++i, g += G) {
       bool keep[4];
       d.keep4(d.group(g), keep);
 #pragma unroll
@@ -101,12 +103,12 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
   {
     float odd = 0.0f;  // NaN once an element is infinite or NaN
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < kPer; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) odd = fmaf(v[i][e], 0.0f, odd);
     if (__any_sync(0xffffffffu, odd != odd)) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < kPer; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[i][e] = finite_or_nan(v[i][e]);
     }
@@ -114,22 +116,22 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
 
   constexpr int top = fmt_top(FMT);
   // Float bits of non-negative values order as unsigned integers.  (fmaxf passes over a NaN.)
-  uint32_t rowbits[16];
+  uint32_t rowbits[kPer];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < kPer; ++i)
     rowbits[i] = __float_as_uint(
         fmaxf(fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3]))), 0.0f));
   int tile_e = 0;
   if (p.tiles) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = umax32(m, rowbits[i]);
+    for (int i = 0; i < kPer; ++i) m = umax32(m, rowbits[i]);
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) sh.warpmax[warp] = m;
     __syncthreads();
     m = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = umax32(m, sh.warpmax[w]);
+    for (int w = 0; w < kQuantWarps; ++w) m = umax32(m, sh.warpmax[w]);
     tile_e = scale_exponent(m, top);
   }
   if (p.codes_rows != nullptr) {
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
     if (!p.tiles) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kPer; ++i) {
         const uint32_t r = __reduce_max_sync(0xffffffffu, rowbits[i]);
         if (lane == i) m = r;
       }
@@ -147,77 +149,62 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_co
     }
     const float inverse = pow2f(-mine);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kPer; ++i) {
       const float inv = __shfl_sync(0xffffffffu, inverse, i);
       if (i < live_rows) *reinterpret_cast<uint32_t*>(dst) = codes4<FMT>(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
       dst += kp;
     }
     // rows past the matrix up to the scales' stride hold 1
     const long long lds = (p.rows + 3) / 4 * 4;
-    if (lane < 16 && r0 + lane < lds)
+    if (lane < kPer && r0 + lane < lds)
       p.scales_rows[static_cast<long long>(tile_c) * lds + r0 + lane] = r0 + lane < p.rows ? pow2f(mine) : 1.0f;
   }
   if (p.codes_cols != nullptr) {
-    float inv[4];
+    float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (!p.tiles) {
-      float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kPer; ++i) {
         m.x = fmaxf(m.x, fabsf(v[i][0]));
         m.y = fmaxf(m.y, fabsf(v[i][1]));
         m.z = fmaxf(m.z, fabsf(v[i][2]));
         m.w = fmaxf(m.w, fabsf(v[i][3]));
       }
-      *reinterpret_cast<float4*>(&sh.colmax[warp][4 * lane]) = m;
+    }
+    *reinterpret_cast<float4*>(&sh.colmax[warp][4 * lane]) = m;
+    __syncthreads();
+    if (threadIdx.x < kBlock) {  // a thread per column
+      float c = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kQuantWarps; ++w) c = fmaxf(c, sh.colmax[w][threadIdx.x]);
+      const int e = p.tiles ? tile_e : scale_exponent(__float_as_uint(c), top);
+      sh.colinv[threadIdx.x] = pow2f(-e);
+      const long long lds = (p.cols + 3) / 4 * 4, col = static_cast<long long>(tile_c) * kBlock + threadIdx.x;
+      if (col < lds)  // columns past the matrix up to the scales' stride hold 1
+        p.scales_cols[static_cast<long long>(tile_r) * lds + col] = col < p.cols ? pow2f(e) : 1.0f;
     }
     __syncthreads();
-    const long long lds = (p.cols + 3) / 4 * 4;
-    {
-      float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (!p.tiles) {
+    const float4 q4 = *reinterpret_cast<const float4*>(&sh.colinv[4 * lane]);
+    const float inv[4] = {q4.x, q4.y, q4.z, q4.w};
+    // Column 4 l + e, unit `warp` (its rows 8 w ..): stored at unit w ^ (l & 15), so that the sixteen
+    // lanes of an 8-byte store phase reach different banks.
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          const float4 q = *reinterpret_cast<const float4*>(&sh.colmax[w][4 * lane]);
-          m.x = fmaxf(m.x, q.x);
-          m.y = fmaxf(m.y, q.y);
-          m.z = fmaxf(m.z, q.z);
-          m.w = fmaxf(m.w, q.w);
-        }
-      }
-      const float ms[4] = {m.x, m.y, m.z, m.w};
-      float s[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = p.tiles ? tile_e : scale_exponent(__float_as_uint(ms[e]), top);
-        inv[e] = pow2f(-x);
-        s[e] = e < live_cols ? pow2f(x) : 1.0f;
-      }
-      if (warp == 0 && c0 < lds)
-        *reinterpret_cast<float4*>(p.scales_cols + static_cast<long long>(tile_r) * lds + c0) =
-            make_float4(s[0], s[1], s[2], s[3]);
-    }
-    // Column 4 l + e, unit `warp` (its rows 16 w ..): stored at unit w ^ (l & 7), so that the eight
-    // lanes of a 16-byte store phase reach different banks.
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t q[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q[i] = codes4<FMT>(v[4 * i][e] * inv[e], v[4 * i + 1][e] * inv[e], v[4 * i + 2][e] * inv[e],
-                           v[4 * i + 3][e] * inv[e]);
-      sh.codes[(4 * lane + e) * 8 + (warp ^ (lane & 7))] = make_uint4(q[0], q[1], q[2], q[3]);
-    }
+    for (int e = 0; e < 4; ++e)
+      sh.codes[(4 * lane + e) * kQuantWarps + (warp ^ (lane & 15))] =
+          make_uint2(codes4<FMT>(v[0][e] * inv[e], v[1][e] * inv[e], v[2][e] * inv[e], v[3][e] * inv[e]),
+                     codes4<FMT>(v[4][e] * inv[e], v[5][e] * inv[e], v[6][e] * inv[e], v[7][e] * inv[e]));
     __syncthreads();
     const long long rp = static_cast<long long>(p.row_blocks) * kBlock;
     const long long col0 = static_cast<long long>(tile_c) * kBlock;
     const int unit = threadIdx.x & 7;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = (threadIdx.x >> 3) + 32 * j;
-      if (col0 + c < p.cols)
+    for (int j = 0; j < 2; ++j) {
+      const int c = (threadIdx.x >> 3) + 64 * j, k = (c >> 2) & 15;
+      if (col0 + c < p.cols) {
+        const uint2 lo = sh.codes[c * kQuantWarps + ((2 * unit) ^ k)], hi = sh.codes[c * kQuantWarps + ((2 * unit + 1) ^ k)];
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.codes_cols) + (col0 + c) * rp +
                                   static_cast<long long>(tile_r) * kBlock + 16 * unit) =
-            sh.codes[c * 8 + (unit ^ ((c >> 2) & 7))];
+            make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
   }
 }
