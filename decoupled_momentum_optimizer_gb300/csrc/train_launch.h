@@ -84,9 +84,13 @@ cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStr
 cudaError_t prepare_matmul_kernels(int sms);
 
 // out = Q(x) w^T for few rows of x, whose codes and scales fit in shared memory: see train_linear.cu.
-constexpr int kLinearRows = 16, kLinearSmem = 68 * 1024;
+// (One launch and no workspace: 37 rows of 1000 x 768 take 14 us a call, 24 as quantize and product,
+// and 48 rows would take longer on the device, 8.7 us of 7.0.)
+constexpr int kLinearRows = 40, kLinearSmem = 90 * 1024;
+// Its sums (1024 bytes a row), codes and scales.
+constexpr long long linear_bytes(long long m, long long blocks) { return m * (1024 + blocks * (kBlock + 4)); }
 constexpr bool few_rows(long long m, long long k) {
-  return m <= kLinearRows && m * ((k + kBlock - 1) / kBlock) * (kBlock + 4) <= kLinearSmem;
+  return m <= kLinearRows && linear_bytes(m, (k + kBlock - 1) / kBlock) <= kLinearSmem;
 }
 struct LinearParams {
   CUtensorMap w;   // codes as [block][row][128], boxes of 4 x 16 x 128; unused without blocks

@@ -27,12 +27,11 @@ constexpr int kStages = 16;
 struct LinearShared {
   uint8_t w[kStages][kQuad][kRows][kBlock];  // 1024-byte aligned (swizzle atoms)
   float ws[kStages][kQuad][kRows];
-  float part[kWarps][kLinearRows][kRows];
   uint64_t full[kStages], empty[kStages];
   volatile uint32_t dead;
-  uint32_t pad[3];  // x's codes and scales follow, 16-byte aligned
+  uint32_t pad[3];  // the rest follows, 16-byte aligned
 };
-static_assert(sizeof(LinearShared) + 1024 + kLinearSmem <= 227 * 1024, "shared memory");
+static_assert(sizeof(LinearShared) % 16 == 0 && sizeof(LinearShared) + 1024 + kLinearSmem <= 227 * 1024, "shared memory");
 
 // D += A B, 16 x 8, K = 32 codes, float32 accumulators.
 template <int WFMT>
@@ -80,13 +79,15 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
   return r;
 }
 
-// Shared memory behind LinearShared: x's codes [m][128 kb] (tokens of odd number have the halves of
-// every block swapped, so that eight lanes of a 16-byte read reach different banks), scales [m][kb].
+// Shared memory behind LinearShared: the warps' sums [warp][m][16 rows], x's codes [m][128 kb] (tokens
+// of odd number have the halves of every block swapped, so that eight lanes of a 16-byte read reach
+// different banks) and scales [m][kb].
 template <typename T, bool VEC, int WFMT, int TILES>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t raw[];
   LinearShared& s = *reinterpret_cast<LinearShared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* codes = reinterpret_cast<uint8_t*>(&s + 1);
+  float* part = reinterpret_cast<float*>(&s + 1);
+  uint8_t* codes = reinterpret_cast<uint8_t*>(part + kWarps * kRows * p.m);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int kp = p.kb * kBlock;
   float* scales = reinterpret_cast<float*>(codes + p.m * kp);
@@ -234,11 +235,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       base += live * quads;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
-        float* q = &s.part[warp][8 * t + 2 * c][g];
-        q[0] = sum[t][0];
-        q[kRows] = sum[t][1];
-        q[8] = sum[t][2];
-        q[kRows + 8] = sum[t][3];
+        const int m = 8 * t + 2 * c;
+        float* q = part + (warp * p.m + m) * kRows + g;
+        if (m < p.m) {
+          q[0] = sum[t][0];
+          q[8] = sum[t][2];
+        }
+        if (m + 1 < p.m) {
+          q[kRows] = sum[t][1];
+          q[kRows + 8] = sum[t][3];
+        }
       }
       named_sync(2 + group, 32 * kQuad);
       const long long n0 = static_cast<long long>(blockIdx.x + static_cast<long long>(first + group) * gridDim.x) * kRows;
@@ -246,9 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const int m = i / kRows, r = i % kRows;
         const long long n = n0 + r;
         if (n >= p.n) continue;
-        float v = s.part[4 * group][m][r];
+        const float* q = part + 4 * group * kRows * p.m + i;
+        float v = q[0];
 #pragma unroll
-        for (int j = 1; j < kQuad; ++j) v += s.part[4 * group + j][m][r];
+        for (int j = 1; j < kQuad; ++j) v += q[j * kRows * p.m];
         const long long at = m * p.ldo + n;
         if (p.out_dtype == kF32)
           static_cast<float*>(p.out)[at] = v;
@@ -264,7 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 
 template <typename T, bool VEC, int WFMT>
 auto* pick_tiles(int m) {
-  return m <= 8 ? linear_kernel<T, VEC, WFMT, 1> : linear_kernel<T, VEC, WFMT, 2>;
+  return m <= 8    ? linear_kernel<T, VEC, WFMT, 1>
+         : m <= 16 ? linear_kernel<T, VEC, WFMT, 2>
+         : m <= 32 ? linear_kernel<T, VEC, WFMT, 4>
+                   : linear_kernel<T, VEC, WFMT, 5>;
 }
 template <typename T, bool VEC>
 auto* pick_format(int w_fmt, int m) {
@@ -288,16 +298,16 @@ cudaError_t launch_linear(const LinearParams& p, int dtype, int w_fmt, int sms, 
   const bool vec = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 &&
                    (p.m == 1 || static_cast<size_t>(p.ldx) * size % 16 == 0);
   const long long row_blocks = (p.n + kRows - 1) / kRows;
-  const size_t smem = sizeof(LinearShared) + 1024 + static_cast<size_t>(p.m) * p.kb * (kBlock + 4);
+  const size_t smem = sizeof(LinearShared) + 1024 + static_cast<size_t>(linear_bytes(p.m, p.kb));
   return launch_overlapped(pick(dtype, vec, w_fmt, p.m), static_cast<unsigned>(row_blocks < sms ? row_blocks : sms),
                            kThreads, smem, st, p);
 }
 
 cudaError_t prepare_linear_kernels() {
   for (int dtype : {kF32, kBF16, kF16})
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const cudaError_t e =
-          cudaFuncSetAttribute(pick(dtype, i & 1, i & 2 ? kE5M2 : kE4M3, i & 4 ? 16 : 8),
+          cudaFuncSetAttribute(pick(dtype, i & 1, i & 2 ? kE5M2 : kE4M3, 8 << (i >> 2)),
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(sizeof(LinearShared) + 1024 + kLinearSmem));
       if (e != cudaSuccess) return e;

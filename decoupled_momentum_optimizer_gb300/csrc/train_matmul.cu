@@ -4,7 +4,7 @@
 //   out[m][n] (+)= sum over blocks b of sa[b][m] sb[b][n] * (sum over k in block b of a[m][k] b[n][k])
 //
 // A pair of CTAs computes a 256 x bn tile (bn up to 224), or one CTA 128 x bn.  TMA brings 128 codes of k of both operands into a ring of
-// shared-memory stages; four warps pack the scales of four blocks into a 32-bit word per row (UE8M0
+// shared-memory stages; two warps pack the scales of four blocks into a 32-bit word per row (UE8M0
 // bytes), which the tensor core copies to tensor memory; one thread issues four K = 32 block-scaled
 // tensor-core instructions per block.  Four blocks run into one of two halves of tensor memory, and eight warps meanwhile add the other half to float32 sums in
 // registers, so the tensor core's accumulator holds 512 products at most and every longer sum is an
@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kBM = 128, kBN = 224;  // rows of a CTA's tile, most columns
 constexpr int kChain = 4;  // blocks of 128 that one half of tensor memory sums
-constexpr int kSumWarps = 8, kScaleWarps = 4;
+constexpr int kSumWarps = 8, kScaleWarps = 2;
 constexpr int kLoadWarp = kSumWarps + kScaleWarps, kMmaWarp = kLoadWarp + 1, kScaleLoadWarp = kLoadWarp + 2;
 // Whole groups of four warps, launched with 128 registers a thread: the summing ones take 192, the
 // others keep 64.
@@ -42,7 +42,7 @@ constexpr int kMaxSplit = 8;  // portable cluster size
 // rest of the shared memory is stages.
 template <int G>
 struct Shared {
-  static constexpr int kStages = G == 1 ? 3 : 4;
+  static constexpr int kStages = G == 1 ? 3 : 5;
   static constexpr uint32_t kABytes = kBM * kBlock, kBBytes = kBN / G * kBlock;
   uint8_t a[kStages][kABytes];  // 1024-byte aligned (swizzle atoms)
   uint8_t b[kStages][kBBytes];
@@ -98,7 +98,7 @@ struct Work {
 
   // m0 is the CTA's own first row.
   __device__ __forceinline__ Tile tile(int t) const {
-    const int band_tiles = 16 / group;
+    const int band_tiles = 8 / group;
     const int per = band_tiles * tiles_n;
     const int band = t / per, i = t - band * per;
     const int height = tiles_m - band * band_tiles < band_tiles ? tiles_m - band * band_tiles : band_tiles;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   if (warp >= kSumWarps) {
     registers_down<kFeedRegs>();
     if (warp < kLoadWarp) {
-      // ---- scale words: warp w makes those of every fourth chain, in slot w ----
+      // ---- scale words: warp w makes those of every second chain, in slot w ----
       const int w = warp - kSumWarps;
       Chains in(work);
       uint32_t phase = 0;
