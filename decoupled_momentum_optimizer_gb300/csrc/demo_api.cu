@@ -524,6 +524,11 @@ int device_info(DeviceInfo* out) {
   return s;
 }
 
+long long take_stall() {
+  DeviceState* st = nullptr;
+  return current_state(&st) == DEMO_OK ? st->stall_at.exchange(0) : 0;
+}
+
 }  // namespace demo
 
 extern "C" {

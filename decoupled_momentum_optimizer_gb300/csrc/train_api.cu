@@ -261,6 +261,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   q.a_fmt = a_fmt;
   q.b_fmt = b_fmt;
   q.fault = dev.fault;
+  q.stall_at = take_stall();
   return to_status(launch_matmul(q, plan, static_cast<cudaStream_t>(stream)));
 }
 
@@ -302,6 +303,7 @@ int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, 
     if (q.kb > 0 && (!block_map(dev.encode, &q.w, w_codes, n, q.kb) || !scale_map(dev.encode, &q.ws, w_scales, n, q.kb, 16, 4)))
       return DEMO_ECUDA;
     q.fault = dev.fault;
+    q.stall_at = take_stall();
     q.x = x;
     q.out = out;
     q.ldx = ldx;

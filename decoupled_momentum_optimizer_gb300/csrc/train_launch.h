@@ -27,6 +27,9 @@ struct DeviceInfo {
   EncodeTiledFn encode;
 };
 int device_info(DeviceInfo* out);
+// Test hook of the bounded waits (demo_test_stall_next_launch): 1 + the load of the next launch's first
+// CTA that shall never complete, 0 for none; taken (and cleared) by the launch.
+long long take_stall();
 
 struct DropParams {
   unsigned long long key;  // sm(sm(sm(seed) ^ step) ^ site)
@@ -69,6 +72,7 @@ struct MatmulParams {
   int kb;         // blocks of 128 along k, may be 0
   int bn, split;  // see MatmulPlan
   int out_dtype, add, a_fmt, b_fmt;
+  long long stall_at;  // see take_stall
   int bulk_out;  // the result's start, rows and row stride are multiples of 16 bytes
   unsigned int* fault;
 };
@@ -99,6 +103,7 @@ struct LinearParams {
   void* out;
   long long ldx, ldo, n, k;
   int m, kb, out_dtype;
+  long long stall_at;  // see take_stall
   unsigned int* fault;
 };
 cudaError_t prepare_linear_kernels();

@@ -3,15 +3,21 @@
 //
 //   out[m][n] (+)= sum over blocks b of sa[b][m] sb[b][n] * (sum over k in block b of a[m][k] b[n][k])
 //
-// A pair of CTAs computes a 256 x bn tile (bn up to 224), or one CTA 128 x bn.  TMA brings 128 codes of k of both operands into a ring of
-// shared-memory stages; two warps pack the scales of four blocks into a 32-bit word per row (UE8M0
-// bytes), which the tensor core copies to tensor memory; one thread issues four K = 32 block-scaled
-// tensor-core instructions per block.  Four blocks run into one of two halves of tensor memory, and eight warps meanwhile add the other half to float32 sums in
-// registers, so the tensor core's accumulator holds 512 products at most and every longer sum is an
-// IEEE float32 addition: its own additions drop low bits, and over a whole k of thousands that
-// showed.  (Scales in the instruction instead of in the sums: with a multiply-add per element and
-// block in the eight warps, 8192 x 2048 x 8192 took 170 us, and 250 us with a scale per row of b.)
-// 224 columns leave room in tensor memory for two halves and their scales.
+// A pair of CTAs computes a 256 x bn tile (bn up to 224), or one CTA 128 x bn.  TMA brings 128 codes of
+// k of both operands into a ring of shared-memory stages, and the scales by a thread and a ring of
+// their own; two warps pack the scales of four blocks into a 32-bit word per row (UE8M0 bytes), which
+// the tensor core copies to tensor memory; one thread issues four K = 32 block-scaled tensor-core
+// instructions per block.  Four blocks run into one of two halves of tensor memory, and eight warps
+// meanwhile add the other half to float32 sums in registers: the tensor core's accumulator holds 512
+// products at most, and every longer sum is an IEEE float32 addition.  (The scales in the instruction
+// instead of in the sums: with a multiply-add per element and block in the eight warps, 8192 x 2048 x
+// 8192 took 170 us, and 250 us with a scale per row of b.)  224 columns leave room in tensor memory for
+// two halves and their scales.
+//
+// What bounds it: 8192 x 8192 x 2048 takes 91 us, 3.0 PFLOP/s, at 1.8 to 1.87 GHz (power).  A block of a
+// 256 x 224 tile is 448 cycles of tensor core and 30 KB for either CTA; it takes about 600, most of the
+// difference waiting for the stages (47 to 57 bytes a cycle and SM arrive).  Half of b per CTA of a
+// pair is what keeps that near the tensor cores' pace (one CTA per 128 x 224 tile reads 44 KB a block).
 #include "train_common.cuh"
 #include "train_tensor.cuh"
 
@@ -344,12 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       uint32_t used = 0;  // stages that have been loaded at least once
       bool ok = true;
       const uint32_t bytes = G * S::kABytes + p.bn * kBlock;  // of a stage, of the pair together
+      long long loads = 0;
       for (int t = work.first; ok && t < work.tiles; t += work.stride) {
         const Tile tl = work.tile(t);
         for (int kb = work.kb0; kb < work.kb0 + work.blocks; ++kb) {
           if (!(ok = wait_or_dead(s, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
           // a pair's loads all complete on the even CTA's barrier
-          if (rank == 0) mbar_expect_tx(&s.full[st.slot], bytes);
+          if (rank == 0) mbar_expect_tx(&s.full[st.slot], bytes + stall_extra(p.stall_at, blockIdx.x, loads++));
           if constexpr (G == 1) {
             tma_load_2d(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
             tma_load_2d(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0);
@@ -553,7 +560,7 @@ static int g_clusters[kMaxSplit + 1];
 // Few tiles (128 x 224 ones that would leave half of the SMs idle, or m that fills no pair): one CTA
 // per tile, with k cut into parts where that pays.  Otherwise pairs.  Either way the cheapest width
 // (and number of parts) in cycles: a block costs a pair max(2 bn, 256 + bn) (the tensor cores, or
-// what a CTA reads at 64 bytes a cycle) and a single CTA 256 + 2 bn; a pair's tile about 2500 more;
+// what a CTA reads at 64 bytes a cycle), and a single CTA 256 + 2 bn; a pair's tile about 2500 more;
 // joining parts about 9000 and the reading of a tile of sums (64 x 8192 x 2048 and 768 x 768 x 8192
 // spent 6000 to 9000 on it; at 6000 here, 32 x 8192 x 2048 was cut and took 15.0 us of 12.3).
 MatmulPlan plan_matmul(long long m, long long n, int kb) {

@@ -10,15 +10,19 @@
 // the same dropout mask), run in registers on the way, so the activation between them and the
 // quantized product is never stored in 16 or 32 bits.
 //
-// A CTA owns a 128 x 128 tile and keeps it in registers: warp w holds rows 8 w .. 8 w + 7, lane
-// l their columns 4 l .. 4 l + 3, all row loads in flight at once.  A row's block is one warp's
-// 128 elements (one warp-wide maximum each; lane i then works out row i's scale for all), a column's
-// block is 8 registers of a lane and the 16 warps' maxima in shared memory.  Infinities and NaN are
-// found by a multiply-add with 0 per element and mended only where there are any: the integer and
-// compare pipe, not HBM, limits 16-bit inputs, so it does as little as it can per element.  Row codes leave as 128 contiguous bytes per row; column codes
-// are packed 16 rows at a time from the same registers, and leave through a swizzled 16 KB tile in
-// shared memory as 128 contiguous bytes per column.  Bound by HBM: the matrix is read once and each
-// form written once.
+// A CTA owns a 128 x 128 tile and keeps it in registers: warp w holds rows 8 w .. 8 w + 7, lane l
+// their columns 4 l .. 4 l + 3, all row loads in flight at once; 64 registers a thread let two tiles of
+// sixteen warps share an SM (8 warps of 16 rows with 120 registers: 72 us where this takes 62).
+// A row's block is one warp's 128 elements (one warp-wide maximum each; lane i then works out row i's
+// scale for all), a column's block is 8 registers of a lane and the 16 warps' maxima in shared memory,
+// a thread per column.  Infinities and NaN are found by a multiply-add with 0 per element and mended
+// only where there are any.  Row codes leave as 128 contiguous bytes per row; column codes are packed 8
+// rows at a time from the same registers, and leave through a swizzled 16 KB tile in shared memory as
+// 128 contiguous bytes per column.
+//
+// Measured, both forms: 8192 x 2048 float32 tiles 16 us (6.2 TB/s, HBM's rate); 8192 x 8192 bfloat16 62 us
+// (4.3 TB/s), with relu and dropout 85 us: there the integer and compare pipe is 65% busy (17 of 32
+// instructions an element, the hash of dropout four of them) and sets the pace.
 #include "train_common.cuh"
 
 namespace demo {

@@ -7,6 +7,7 @@ torch unless an ``out`` is given, the call runs on torch's current stream (or ``
 """
 
 import ctypes
+import functools
 
 import torch
 
@@ -104,6 +105,11 @@ def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
     return out
 
 
+def _empty(rows, cols, dtype, device):
+    """torch.empty, by the form of it that parses its arguments fastest."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 class Fp8Matrix:
     """A [rows, k] matrix in 8-bit floating point, a scale for each block of 128 along a row.
 
@@ -135,8 +141,8 @@ class Fp8Matrix:
         """Uninitialised buffers of the right sizes, for fp8_quantize's ``out``."""
         q = cls.__new__(cls)
         blocks = (k + BLOCK - 1) // BLOCK
-        q.codes = torch.empty((rows, blocks * BLOCK), dtype=FP8_FORMATS[fmt][1], device=device)
-        q.scales = torch.empty((blocks, (rows + 3) // 4 * 4), dtype=torch.float32, device=device)
+        q.codes = _empty(rows, blocks * BLOCK, FP8_FORMATS[fmt][1], device)
+        q.scales = _empty(blocks, (rows + 3) // 4 * 4, torch.float32, device)
         q.shape, q.tiles = (rows, k), tiles
         return q
 
@@ -201,7 +207,7 @@ def _form(q, rows, k, fmt, tiles, x):
 def _out(out, shape, dtype, beside):
     """(out or a new tensor, pointer, row stride, dtype's code)."""
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=beside.device)
+        out = torch.empty(*shape, dtype=dtype, device=beside.device)
         return out, out.data_ptr(), shape[-1], _DTYPES[dtype]
     if dtype is not None and out.dtype != dtype:
         raise TypeError(f"out has dtype {out.dtype}, expected {dtype}")
@@ -236,6 +242,11 @@ def fp8_matmul(a, b, *, out=None, dtype=None, add=False, stream=None):
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _linear_workspace(m, n, k):
+    return _lib.demo_fp8_linear_workspace(m, n, k)
+
+
 def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     """``x w^T`` for ``x`` [..., k] in 16 or 32 bits and an Fp8Matrix ``w`` [n, k] (demo_fp8_linear):
     ``x`` is quantized by rows to e4m3 within the call.  The result has x's dtype unless ``dtype``
@@ -253,7 +264,7 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     if k == 0:
         m = lead.numel()
     out, op, ldo, odt = _out(out, (*lead, n), _result_dtype(out, dtype, x.dtype), x)
-    need = _lib.demo_fp8_linear_workspace(m, n, k)
+    need = _linear_workspace(m, n, k)
     wp = None
     if need:
         if workspace is None:

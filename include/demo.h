@@ -413,7 +413,8 @@ int demo_device_fault(unsigned int* code);
  * device-side waits (failure detection without a GPU fault); the pages have no
  * counterpart.  The next launch of a tile kernel on the current device (the one
  * demo_step, demo_encode or demo_decode_update runs, or their _wire / pipelined
- * variants; not the elementwise DiLoCo and AdamW kernels) makes its first warp
+ * variants, or demo_fp8_matmul or demo_fp8_linear for few rows, where the first CTA's loader
+ * thread stands for the warp below; not the elementwise kernels) makes its first warp
  * announce 16 bytes more than the load of that warp's item `item` (0-based)
  * delivers.  That load's barrier then never completes: the warp's bounded wait
  * gives up after its limit (2 s), the warp sets bit 1 of the fault word, waits

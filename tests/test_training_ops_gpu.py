@@ -444,3 +444,20 @@ def test_operators_in_a_graph():
         want = forward()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("call", ["pairs", "split", "linear"])
+def test_a_load_that_never_completes_ends_in_the_fault_word(call):
+    """The kernels' waits give up after their limit (2 s), every role stops, tensor memory is freed and
+    the context stays usable: the same call gives the right result right after."""
+    m, n, k = {"pairs": (2100, 1300, 700), "split": (200, 300, 2000), "linear": (3, 300, 2000)}[call]
+    w, wv = quantized(n, k, "e4m3", True, 60)
+    x = draw(m, k, "f32", 61)
+    a = dm.fp8_quantize(x)
+    run = (lambda: dm.fp8_linear(x, w)) if call == "linear" else (lambda: dm.fp8_matmul(a, w, dtype=torch.float32))
+    want = run()
+    assert dm.device_fault() == 0
+    dm.test_stall_next_launch(0)
+    run()
+    assert dm.device_fault() == 1
+    assert torch.equal(run(), want) and dm.device_fault() == 0
