@@ -461,3 +461,44 @@ def test_a_load_that_never_completes_ends_in_the_fault_word(call):
     run()
     assert dm.device_fault() == 1
     assert torch.equal(run(), want) and dm.device_fault() == 0
+
+
+# ---- offsets past 32 bits ------------------------------------------------------------------------
+
+def test_offsets_past_32_bits():
+    """Codes, inputs and results of more than 2^32 elements: what is at their far ends."""
+    rows, cols = (1 << 20) + 3, 4200  # 4.4e9 elements
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-130:] = draw(130, cols, "bf16", 70)
+    x[:, -1] = 0.0
+    x[-131:, -1] = torch.arange(1, 132).bfloat16().cuda()
+    by_rows, by_cols = dm.fp8_quantize(x, form="both")
+    want, scales = ref.quantize(f64(x[-2:]), "e4m3")
+    assert np.array_equal(f64(by_rows.codes[-2:]), want) and np.array_equal(f64(by_rows.scales[:, rows - 2:rows]), scales)
+    last = f64(x[rows // 128 * 128 - 256:, -1:])  # the last column, from a block's start
+    want, scales = ref.quantize(np.ascontiguousarray(last.T), "e4m3")
+    k0 = rows // 128 - 2
+    assert np.array_equal(f64(by_cols.codes[-1:, k0 * 128:]), want)
+    assert np.array_equal(f64(by_cols.scales[k0:, cols - 1]), scales[:, 0])
+    del by_cols
+    tokens = draw(3, cols, "bf16", 71)
+    got = f64(dm.fp8_linear(tokens, by_rows, dtype=torch.float32))
+    codes, sc = ref.quantize(f64(tokens), "e4m3")
+    tail = dm.Fp8Matrix(by_rows.codes[-131:].contiguous(), torch.nn.functional.pad(by_rows.scales[:, rows - 131:rows], (0, 1)).contiguous(), cols)
+    wv = f64(tail.dequantize())
+    want, total = ref.product(ref.values(codes, sc, cols), wv)
+    assert (np.abs(got[:, -131:] - want) <= ref.product_tolerance(total, cols)).all() and (got[:, :-131] == 0).all()
+    tq = dm.fp8_quantize(tokens)
+    want, total = ref.product(wv, f64(tq.dequantize()))
+    got = f64(dm.fp8_matmul(by_rows, tq, dtype=torch.float32)[-131:])  # the long matrix as a
+    assert (np.abs(got - want) <= ref.product_tolerance(total, cols)).all()
+    del x, by_rows
+    a, b = dm.fp8_quantize(draw(70001, 64, "f32", 72)), dm.fp8_quantize(draw(64000, 64, "f32", 73))
+    out = dm.fp8_matmul(a, b)  # 4.5e9 results
+    pick = [0, 33600, 70000]
+    want, total = ref.product(f64(a.dequantize()[pick]), f64(b.dequantize()))
+    tol = ref.product_tolerance(total, 64) + ref.round_tolerance(want, "bf16") * (1 + 2.0 ** -8)
+    assert (np.abs(f64(out[pick]) - want) <= tol).all()
+    odd = torch.empty(70001 * 64001, dtype=torch.bfloat16, device="cuda").view(70001, 64001)[:, :64000]
+    dm.fp8_matmul(a, b, out=odd)  # rows that no bulk store can write
+    assert torch.equal(odd[pick], out[pick]) and torch.equal(odd[-200:], out[-200:])
