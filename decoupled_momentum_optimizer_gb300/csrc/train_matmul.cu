@@ -14,10 +14,11 @@
 // 8192 took 170 us, and 250 us with a scale per row of b.)  224 columns leave room in tensor memory for
 // two halves and their scales.
 //
-// What bounds it: 8192 x 8192 x 2048 takes 91 us, 3.0 PFLOP/s, at 1.8 to 1.87 GHz (power).  A block of a
-// 256 x 224 tile is 448 cycles of tensor core and 30 KB for either CTA; it takes about 600, most of the
-// difference waiting for the stages (47 to 57 bytes a cycle and SM arrive).  Half of b per CTA of a
-// pair is what keeps that near the tensor cores' pace (one CTA per 128 x 224 tile reads 44 KB a block).
+// What bounds it: power.  8192 x 8192 x 2048 takes 91 us (3.0 PFLOP/s) in the first milliseconds and 103
+// over a second, at 1.37 kW with the SM clock down to 1.67 GHz.  At full clock the stages' arrival would
+// be next: a block of a 256 x 224 tile is 448 cycles of tensor core and 30 KB for either CTA, and takes
+// about 600; half of b per CTA of a pair is what keeps that near the tensor cores' pace (one CTA per
+// 128 x 224 tile reads 44 KB a block).
 #include "train_common.cuh"
 #include "train_tensor.cuh"
 

@@ -12,7 +12,7 @@
 //
 // A CTA owns a 128 x 128 tile and keeps it in registers: warp w holds rows 8 w .. 8 w + 7, lane l
 // their columns 4 l .. 4 l + 3, all row loads in flight at once; 64 registers a thread let two tiles of
-// sixteen warps share an SM (8 warps of 16 rows with 120 registers: 72 us where this takes 62).
+// sixteen warps share an SM (8 warps of 16 rows with 120 registers: 72 us where this took 62).
 // A row's block is one warp's 128 elements (one warp-wide maximum each; lane i then works out row i's
 // scale for all), a column's block is 8 registers of a lane and the 16 warps' maxima in shared memory,
 // a thread per column.  Infinities and NaN are found by a multiply-add with 0 per element and mended
@@ -20,9 +20,10 @@
 // rows at a time from the same registers, and leave through a swizzled 16 KB tile in shared memory as
 // 128 contiguous bytes per column.
 //
-// Measured, both forms: 8192 x 2048 float32 tiles 16 us (6.2 TB/s, HBM's rate); 8192 x 8192 bfloat16 62 us
-// (4.3 TB/s), with relu and dropout 85 us: there the integer and compare pipe is 65% busy (17 of 32
-// instructions an element, the hash of dropout four of them) and sets the pace.
+// Measured, both forms: 8192 x 2048 float32 tiles 16 us (6.2 TB/s, HBM's rate); 8192 x 8192 bfloat16 55 us
+// (4.8 TB/s; 62 with bounds checked in whole tiles too), with relu and dropout 82 us (68 without the
+// hash): there the integer and compare pipe, 65% busy with 17 of 32 instructions an element, sets the
+// pace.
 #include "train_common.cuh"
 
 namespace demo {
@@ -71,19 +72,32 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid
   const int live_cols = p.cols - c0 >= 4 ? 4 : p.cols > c0 ? static_cast<int>(p.cols - c0) : 0;
   kernel_begin();
   float v[kPer][4];
-  {
-    const T* x = static_cast<const T*>(p.x) + r0 * p.ldx + c0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) load4<T, VEC>(x + i * p.ldx, i < live_rows ? live_cols : 0, v[i]);
-  }
-  if constexpr (GATE) {
-    const T* g = static_cast<const T*>(p.gate) + r0 * p.ldg + c0;
+  const T* x = static_cast<const T*>(p.x) + r0 * p.ldx + c0;
+  const T* gate = GATE ? static_cast<const T*>(p.gate) + r0 * p.ldg + c0 : nullptr;
+  // a whole tile (for every thread of the CTA) needs no bounds
+  const bool whole = VEC && static_cast<long long>(tile_r + 1) * kBlock <= p.rows &&
+                     static_cast<long long>(tile_c + 1) * kBlock <= p.cols;
+  if (whole) {
+    Vec<T, 4> a[kPer], h[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      float h[4];
-      load4<T, VEC>(g + i * p.ldg, i < live_rows ? live_cols : 0, h);
+      a[i] = *reinterpret_cast<const Vec<T, 4>*>(x + i * p.ldx);
+      if constexpr (GATE) h[i] = *reinterpret_cast<const Vec<T, 4>*>(gate + i * p.ldg);
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] = h[e] > 0.0f ? v[i][e] : 0.0f;
+    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = !GATE || to_f32(h[i].e[e]) > 0.0f ? to_f32(a[i].e[e]) : 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      load4<T, VEC>(x + i * p.ldx, i < live_rows ? live_cols : 0, v[i]);
+      if constexpr (GATE) {
+        float h[4];
+        load4<T, VEC>(gate + i * p.ldg, i < live_rows ? live_cols : 0, h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = h[e] > 0.0f ? v[i][e] : 0.0f;
+      }
     }
   }
   if (p.relu) {

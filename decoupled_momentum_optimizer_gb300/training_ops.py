@@ -2,8 +2,8 @@
 
 Bindings of ``demo_dropout``, ``demo_fp8_quantize``, ``demo_fp8_matmul`` and ``demo_fp8_linear``
 (``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
-torch unless an ``out`` is given, the call runs on torch's current stream (or ``stream``) and raises
-:class:`DemoError` on a negative status.
+torch unless an ``out`` is given, the call runs on torch's current stream (or on ``stream``, as if it
+were the current one) and raises :class:`DemoError` on a negative status.
 """
 
 import ctypes
@@ -33,17 +33,27 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _run(name, args, index, stream):
-    """Entry point ``name`` on ``args`` and the stream's pointer, with device ``index`` current and
-    initialised; raises on a negative status."""
+def _run(name, args, index):
+    """Entry point ``name`` on ``args`` and device ``index``'s current stream, with the device current
+    and initialised; raises on a negative status."""
     if index in _lib.dm__inited and _current_device() == index:
-        raw = _raw_stream(index) if stream is None and _raw_stream is not None else _lib.dm__stream(stream, index)
+        raw = _raw_stream(index) if _raw_stream is not None else _lib.dm__stream(None, index)
         status = getattr(_lib, name)(*args, raw)
     else:
         with _lib.dm__OnDevice(torch.device("cuda", index)):
-            status = getattr(_lib, name)(*args, _lib.dm__stream(stream, index))
+            status = getattr(_lib, name)(*args, _lib.dm__stream(None, index))
     if status:
         _lib.dm__check(status, name)
+
+
+def _on_stream(stream, device, f, *args, **kw):
+    """``f`` with ``stream`` current, so that what it allocates belongs to the stream it is used on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
+    with torch.cuda.stream(stream):
+        return f(*args, **kw)
 
 
 def _matrix(t, name, like=None, shape=None):
@@ -93,6 +103,8 @@ def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
     The gradient of ``x`` is ``dropout(dy, p, seed=..., step=..., site=...)`` with the same
     arguments; the residual's is ``dy``.  ``out`` may be ``x`` or ``residual`` themselves.
     """
+    if stream is not None:
+        return _on_stream(stream, x.device, dropout, x, p, seed=seed, step=step, site=site, residual=residual, out=out)
     xp, ldx, rows, cols = _matrix(x, "x")
     rp, ldr = _matrix(residual, "residual", x)[:2] if residual is not None else (None, 0)
     if out is None:
@@ -101,7 +113,7 @@ def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
     else:
         op, ldo = _matrix(out, "out", x)[:2]
     _run("demo_dropout", (xp, ldx, rp, ldr, op, ldo, _DTYPES[x.dtype], rows, cols, p, seed, step, site),
-         x.get_device(), stream)
+         x.get_device())
     return out
 
 
@@ -163,6 +175,9 @@ def fp8_quantize(x, *, fmt="e4m3", form="rows", scales="rows", relu=False, gate=
     applied on the way in, in this order; ``gate`` zeroes the elements where it is not positive.
     ``out``    the Fp8Matrix, or the pair, to write into
     """
+    if stream is not None:
+        return _on_stream(stream, x.device, fp8_quantize, x, fmt=fmt, form=form, scales=scales, relu=relu, gate=gate, p=p,
+                          seed=seed, step=step, site=site, out=out)
     if fmt not in FP8_FORMATS:
         raise ValueError(f"fmt is {fmt!r}, expected one of {tuple(FP8_FORMATS)}")
     if scales != "rows" and scales != "tiles":
@@ -189,7 +204,7 @@ def fp8_quantize(x, *, fmt="e4m3", form="rows", scales="rows", relu=False, gate=
         by_cols = _form(by_cols, cols, rows, fmt, tiles, x)
         cc, sc = by_cols.codes.data_ptr(), by_cols.scales.data_ptr()
     _run("demo_fp8_quantize", (xp, ldx, _DTYPES[x.dtype], rows, cols, bool(relu), gp, ldg, p, seed, step, site,
-                               FP8_FORMATS[fmt][0], tiles, cr, sr, cc, sc), x.get_device(), stream)
+                               FP8_FORMATS[fmt][0], tiles, cr, sr, cc, sc), x.get_device())
     return (by_rows, by_cols) if form == "both" else by_rows if by_cols is None else by_cols
 
 
@@ -227,6 +242,8 @@ def _result_dtype(out, dtype, default):
 def fp8_matmul(a, b, *, out=None, dtype=None, add=False, stream=None):
     """``a b^T`` of two Fp8Matrix ([m, k] and [n, k]) into ``out`` or a new tensor of ``dtype``
     (bfloat16 by default), or added to the float32 ``out`` (demo_fp8_matmul)."""
+    if stream is not None:
+        return _on_stream(stream, a.codes.device, fp8_matmul, a, b, out=out, dtype=dtype, add=add)
     (m, k), (n, kb) = a.shape, b.shape
     if k != kb:
         raise ValueError(f"a has k = {k}, b has k = {kb}")
@@ -238,7 +255,7 @@ def fp8_matmul(a, b, *, out=None, dtype=None, add=False, stream=None):
         raise ValueError("add needs an out to add to")
     out, op, ldo, dt = _out(out, (m, n), _result_dtype(out, dtype, torch.bfloat16), ac)
     _run("demo_fp8_matmul", (ac.data_ptr(), a.scales.data_ptr(), _FMT_OF[ac.dtype], bc.data_ptr(),
-                             b.scales.data_ptr(), _FMT_OF[bc.dtype], m, n, k, op, ldo, dt, bool(add)), index, stream)
+                             b.scales.data_ptr(), _FMT_OF[bc.dtype], m, n, k, op, ldo, dt, bool(add)), index)
     return out
 
 
@@ -253,6 +270,8 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     or ``out`` says otherwise; ``workspace`` (uint8, only used beyond a few rows) is allocated
     through torch where it is not given.
     """
+    if stream is not None:
+        return _on_stream(stream, x.device, fp8_linear, x, w, out=out, dtype=dtype, workspace=workspace)
     xp, ldx, m, k = _matrix(x, "x")
     n, kw = w.shape
     if k != kw:
@@ -273,7 +292,7 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
         wp, need = workspace.data_ptr(), workspace.numel()
     _run("demo_fp8_linear", (xp, ldx, _DTYPES[x.dtype], wc.data_ptr(), w.scales.data_ptr(), _FMT_OF[wc.dtype], m, n, k,
-                             op, ldo, odt, wp, need), index, stream)
+                             op, ldo, odt, wp, need), index)
     return out
 
 

@@ -502,3 +502,29 @@ def test_offsets_past_32_bits():
     odd = torch.empty(70001 * 64001, dtype=torch.bfloat16, device="cuda").view(70001, 64001)[:, :64000]
     dm.fp8_matmul(a, b, out=odd)  # rows that no bulk store can write
     assert torch.equal(odd[pick], out[pick]) and torch.equal(odd[-200:], out[-200:])
+
+
+# ---- streams and shapes of the bindings ------------------------------------------------------------
+
+def test_results_and_workspaces_belong_to_the_stream_they_are_used_on():
+    """Calls queued behind a wait on another stream: what torch allocates meanwhile on this one may not
+    take their buffers (a workspace is given back as soon as the call returns)."""
+    w, _ = quantized(512, 1024, "e4m3", True, 80)
+    x = draw(100, 1024, "bf16", 81)
+    want = [dm.fp8_linear(x, w), dm.dropout(x, 0.5, seed=1, step=1), dm.fp8_matmul(dm.fp8_quantize(x), w)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)  # some tens of milliseconds
+    got = [dm.fp8_linear(x, w, stream=side), dm.dropout(x, 0.5, seed=1, step=1, stream=side.cuda_stream)]
+    got.append(dm.fp8_matmul(dm.fp8_quantize(x, stream=side), w, stream=side))
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in range(1024, 400 * 1024, 1024)]
+    side.synchronize()
+    assert len(junk) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_one_token_as_a_vector():
+    w, _ = quantized(100, 260, "e4m3", True, 82)
+    x = draw(2, 260, "f32", 83)
+    assert torch.equal(dm.fp8_linear(x[0], w), dm.fp8_linear(x[:1], w)[0])
+    assert dm.dropout(x[0], 0.1, seed=0, step=0).shape == (260,)
