@@ -94,7 +94,7 @@ struct Tile {
   int m0, n0;
 };
 
-// The tiles and blocks of a CTA (or pair).  Tiles go in bands of 2048 rows of m, along n within a
+// The tiles and blocks of a CTA (or pair).  Tiles go in bands of 1024 rows of m, along n within a
 // band: those that run at one time then cover about as many rows of a as of b, and share both in
 // the L2 cache.
 struct Work {
