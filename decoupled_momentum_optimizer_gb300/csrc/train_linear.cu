@@ -97,10 +97,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   const int kp = p.kb * kBlock;
   float* scales = reinterpret_cast<float*>(codes + p.m * kp);
   // This CTA's rows of w, 16 at a time: row blocks blockIdx.x, + gridDim.x, ..; group j takes the j-th,
-  // j + 4-th ..  Stages come in rounds of up to four row blocks, `quads` stages each, in turn.
+  // j + 4-th ..  The groups that have any share the stages evenly, each a ring of its own: whoever waits on
+  // a stage's barrier has then seen its every phase (a wait by parity passes at once for the phase after
+  // one that is still under way).  Stages are asked for in rounds of up to four row blocks, in turn.
   const int row_blocks = static_cast<int>((p.n + kRows - 1) / kRows);
   const int own = (row_blocks - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int quads = (p.kb + kQuad - 1) / kQuad;
+  const int ring = kStages / (own < kGroups ? own : kGroups);  // stages of a group
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -118,29 +121,34 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   kernel_begin();
 
   if (warp == kWarps) {
-    named_sync(6, kThreads);
     if (elect_one()) {
-      Ring<kStages> st;
       bool ok = true;
-      uint32_t used = 0;
+      int at = 0;          // in every group's ring
+      uint32_t phase = 0;
+      uint32_t used = 0, last = 0;  // stages that have been asked for, and the phases they were last
       long long loads = 0;
       for (int first = 0; ok && first < own; first += kGroups) {
         const int live = own - first < kGroups ? own - first : kGroups;
         for (int q = 0; ok && q < quads; ++q) {
           for (int j = 0; j < live; ++j) {
-            if (!(ok = wait_bounded<false>(&s.dead, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
+            const int slot = j * ring + at;
+            if (!(ok = wait_bounded<false>(&s.dead, &s.empty[slot], phase ^ 1u, p.fault))) break;
             const int row = static_cast<int>(blockIdx.x + (first + j) * gridDim.x) * kRows;
-            mbar_expect_tx(&s.full[st.slot], kQuad * kRows * (kBlock + 4) + stall_extra(p.stall_at, blockIdx.x, loads++));
-            tma_load_3d(s.w[st.slot], &p.w, &s.full[st.slot], 0, row, kQuad * q);
-            tma_load_2d(s.ws[st.slot], &p.ws, &s.full[st.slot], row, kQuad * q);
-            used |= 1u << st.slot;
-            st.next();
+            mbar_expect_tx(&s.full[slot], kQuad * kRows * (kBlock + 4) + stall_extra(p.stall_at, blockIdx.x, loads++));
+            tma_load_3d(s.w[slot], &p.w, &s.full[slot], 0, row, kQuad * q);
+            tma_load_2d(s.ws[slot], &p.ws, &s.full[slot], row, kQuad * q);
+            used |= 1u << slot;
+            last = (last & ~(1u << slot)) | phase << slot;
+          }
+          if (++at == ring) {
+            at = 0;
+            phase ^= 1u;
           }
         }
       }
       if (!ok)  // stopped early: wait (bounded) for the copies that are under way
         for (int i = 0; i < kStages; ++i)
-          if (used >> i & 1u) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
+          if (used >> i & 1u) mbar_wait_bounded(&s.full[i], last >> i & 1u);
     }
   } else {
     // ---- x: a warp quantizes eight blocks of 128 at a time, four lanes each, 32 elements a lane ----
@@ -151,7 +159,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       Vec<T, kUnit<T>> v[kUnits<T>];
       load32<T, VEC>(static_cast<const T*>(p.x) + m * p.ldx + static_cast<long long>(kb) * kBlock, c4,
                      p.k - static_cast<long long>(kb) * kBlock, v);
-      if (first < 8 * kWarps) named_arrive(6, kThreads);  // w may be asked for: what follows waits behind it
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < kUnits<T>; ++j)
@@ -185,23 +192,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       }
       if (c4 == 0) scales[i] = pow2f(ex);
     }
-    if (8 * warp >= blocks) named_arrive(6, kThreads);
     named_sync(1, 32 * kWarps);
 
     // ---- products ----
     const int group = warp >> 2, w4 = warp & 3, g = lane >> 2, c = lane & 3;
     bool ok = true;
-    int base = 0;  // the round's first stage, counted from the start
+    int at = 0;
+    uint32_t phase = 0;
     for (int first = 0; ok && first + group < own; first += kGroups) {
-      const int live = own - first < kGroups ? own - first : kGroups;
       float sum[TILES][4];
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[t][e] = 0.0f;
       for (int q = 0; q < quads; ++q) {
-        const int i = base + q * live + group, slot = i % kStages, kb = kQuad * q + w4;
-        ok = __all_sync(0xffffffffu, wait_bounded<false>(&s.dead, &s.full[slot], i / kStages & 1, p.fault));
+        const int slot = group * ring + at, kb = kQuad * q + w4;
+        ok = __all_sync(0xffffffffu, wait_bounded<false>(&s.dead, &s.full[slot], phase, p.fault));
         if (!ok) break;
         // unit u of row r is at u ^ (r & 7)
         const uint8_t* w0 = s.w[slot][w4][g];
@@ -237,8 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
         __syncwarp();
         if (lane == 0) arrive_here(&s.empty[slot]);
+        if (++at == ring) {
+          at = 0;
+          phase ^= 1u;
+        }
       }
-      base += live * quads;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         const int m = 8 * t + 2 * c;

@@ -144,13 +144,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// A barrier of the CTA among `threads` threads (whole warps).
+// A barrier of the CTA among `threads` threads (whole warps).  The warp is brought together first, and
+// the barrier takes threads, not warps: it may follow code whose lanes went different ways.
 __device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ void named_arrive(int id, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+  __syncwarp();
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // One lane of a converged warp (the same one every time).

@@ -528,3 +528,23 @@ def test_one_token_as_a_vector():
     x = draw(2, 260, "f32", 83)
     assert torch.equal(dm.fp8_linear(x[0], w), dm.fp8_linear(x[:1], w)[0])
     assert dm.dropout(x[0], 0.1, seed=0, step=0).shape == (260,)
+
+
+@pytest.mark.parametrize("row_blocks", [1, 2, 3, 4, 5, 6, 7, 9])
+def test_linear_repeats_with_any_share_of_the_rows(row_blocks):
+    """Every number of row blocks a CTA can own (the groups' rings of stages differ in length, and a last
+    round may be short), called back to back: every result is the same to the bit and within bounds."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n, k = 16 * (sms * row_blocks - sms // 2), 2048
+    w, wv = quantized(n, k, "e4m3", True, 90 + row_blocks)
+    x = draw(3, k, "bf16", 91)
+    codes, scales = ref.quantize(f64(x), "e4m3")
+    want, total = ref.product(ref.values(codes, scales, k), wv)
+    first = dm.fp8_linear(x, w, dtype=torch.float32)
+    assert (np.abs(f64(first) - want) <= ref.product_tolerance(total, k)).all()
+    outs = [torch.empty_like(first) for _ in range(50)]
+    for _ in range(10):
+        for out in outs:
+            dm.fp8_linear(x, w, out=out)
+        assert all(torch.equal(out, first) for out in outs)
+    assert dm.device_fault() == 0
