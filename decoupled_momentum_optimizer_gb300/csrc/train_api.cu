@@ -246,7 +246,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   q.bulk_out = at(out, 16) && n * size % 16 == 0 && (m == 1 || ldo * size % 16 == 0);
   if ((q.kb > 0 && (!code_map(dev.encode, &q.a, a_codes, m, up(k, kBlock), plan.rows_a) ||
                     !code_map(dev.encode, &q.b, b_codes, n, up(k, kBlock), plan.rows_b) ||
-                    !scale_map(dev.encode, &q.sa, a_scales, m, q.kb, plan.rows_a, plan.chain) ||
+                    !scale_map(dev.encode, &q.sa, a_scales, m, q.kb, kBlock, plan.chain) ||
                     !scale_map(dev.encode, &q.sb, b_scales, n, q.kb, plan.bn, plan.chain))) ||
       (q.bulk_out && !out_map(dev.encode, &q.o, out, m, n, ldo, out_dtype, plan.bn)))
     return DEMO_ECUDA;
@@ -256,6 +256,8 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   q.out = out;
   q.bn = plan.bn;
   q.split = plan.split;
+  q.rows_a = plan.rows_a;
+  q.stages = plan.stages;
   q.out_dtype = out_dtype;
   q.add = add;
   q.a_fmt = a_fmt;

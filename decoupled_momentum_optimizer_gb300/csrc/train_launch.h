@@ -70,7 +70,7 @@ struct MatmulParams {
   long long m, n, ldo;
   void* out;
   int kb;         // blocks of 128 along k, may be 0
-  int bn, split;  // see MatmulPlan
+  int bn, split, rows_a, stages;  // see MatmulPlan
   int out_dtype, add, a_fmt, b_fmt;
   long long stall_at;  // see take_stall
   int bulk_out;  // the result's start, rows and row stride are multiples of 16 bytes
@@ -78,9 +78,9 @@ struct MatmulParams {
 };
 
 // How a product runs: CTAs that share a tile's rows (1 or 2), the tile's width, the parts k is cut
-// into, the grid; and the tensor maps' boxes (rows of codes, blocks of scales).
+// into, the stages, the grid; and the tensor maps' boxes (rows of codes, blocks of scales).
 struct MatmulPlan {
-  int group, bn, split, rows_a, rows_b, chain;
+  int group, bn, split, stages, rows_a, rows_b, chain;
   unsigned int grid;
 };
 MatmulPlan plan_matmul(long long m, long long n, int kb);
@@ -88,8 +88,10 @@ cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStr
 cudaError_t prepare_matmul_kernels(int sms);
 
 // out = Q(x) w^T for few rows of x, whose codes and scales fit in shared memory: see train_linear.cu.
-// (One launch and no workspace: 37 rows of 1000 x 768 take 14 us a call, 24 as quantize and product,
-// and 48 rows would take longer on the device, 8.7 us of 7.0.)
+// One launch and no workspace: a call takes 10 to 13 us from Python, of 17 as quantize and product, at
+// every size measured up to 40 rows.  On the device alone it is the faster one up to 16 rows (1000 x 768
+// 3.4 us of 6.7, 8192 x 2048 9.5 of 9.1), and at 24 to 40 where w is small (1000 x 768 5.3 .. 6.3 of 6.8;
+// 24 x 8192 x 2048 12.7 of 9.1).
 constexpr int kLinearRows = 40, kLinearSmem = 90 * 1024;
 // Its sums (1024 bytes a row), codes and scales.
 constexpr long long linear_bytes(long long m, long long blocks) { return m * (1024 + blocks * (kBlock + 4)); }

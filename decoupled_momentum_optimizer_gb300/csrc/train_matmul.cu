@@ -19,6 +19,8 @@
 // be next: a block of a 256 x 224 tile is 448 cycles of tensor core and 30 KB for either CTA, and takes
 // about 600; half of b per CTA of a pair is what keeps that near the tensor cores' pace (one CTA per
 // 128 x 224 tile reads 44 KB a block).
+#include <algorithm>
+
 #include "train_common.cuh"
 #include "train_tensor.cuh"
 
@@ -44,15 +46,16 @@ static_assert(kChain == 4, "a word holds the scales of a chain");
 constexpr int kCols = kBN / 2;  // most columns of a summing warp
 constexpr int kOutBytes = 32 * kBN;  // a warp's rows on their way out, bn bytes each
 constexpr int kMaxSplit = 8;  // portable cluster size
+constexpr int kMaxStages = 8;
 
 // G CTAs (1, or a cluster of 2) share a tile: each loads its 128 rows of a and bn / G of b, and the
 // rest of the shared memory is stages.
 template <int G>
 struct Shared {
-  static constexpr int kStages = G == 1 ? 3 : 5;
-  static constexpr uint32_t kABytes = kBM * kBlock, kBBytes = kBN / G * kBlock;
-  uint8_t a[kStages][kABytes];  // 1024-byte aligned (swizzle atoms)
-  uint8_t b[kStages][kBBytes];
+  // Stages: a's rows, then b's, whole units of 1024 bytes (swizzle atoms).  A pair has five; single CTAs
+  // have as many as fit (at most kMaxStages), with only the rows of a that exist.
+  static constexpr int kRingBytes = G == 1 ? 3 * (kBM + kBN) * kBlock : 5 * (kBM + kBN / 2) * kBlock;
+  uint8_t ring[kRingBytes];  // 1024-byte aligned
   uint8_t out[kSumWarps][kOutBytes];
   // Scale words: row 32 c + l of an operand at [l][c] of its 512-byte unit of 128 rows (a's, then
   // b's two), as the tensor core's copy wants them.
@@ -60,7 +63,7 @@ struct Shared {
   // a chain's scales as they arrive: rows of kBM, and of bn
   float sa[kScaleSlots][kChain * kBM];
   float sb[kScaleSlots][kChain * kBN];
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // scales
   uint64_t scaled[kScaleSlots], sfree[kScaleSlots];  // words
   uint64_t tfull[2], tempty[2];
@@ -72,7 +75,7 @@ template <int G>
 constexpr size_t kSmem = sizeof(Shared<G>) + 1024;
 static_assert(kSmem<1> <= 227 * 1024 && kSmem<2> <= 227 * 1024, "shared memory");
 // A split tile's float32 sums go where the stages were.
-static_assert(kBM * kBN * 4 <= Shared<1>::kStages * (Shared<1>::kABytes + Shared<1>::kBBytes), "a tile of sums");
+static_assert(kBM * kBN * 4 <= Shared<1>::kRingBytes, "a tile of sums");
 
 template <int G>
 __device__ __forceinline__ bool wait_or_dead(Shared<G>& s, uint64_t* bar, uint32_t parity, unsigned int* fault) {
@@ -262,12 +265,16 @@ template <int G>
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ MatmulParams p) {
   extern __shared__ uint8_t raw[];
   using S = Shared<G>;
-  constexpr int kStages = S::kStages;
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   // the warp's number from one lane: the roles below are branches of whole warps
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = G == 1 ? 0 : static_cast<int>(cluster_rank());  // in the pair
   const int part = G == 1 ? static_cast<int>(cluster_rank()) : 0;  // of k
+  // A stage: the rows of a that are loaded (the tensor core reads 128, past fewer into what follows: those
+  // results are not used), and b's.
+  const int a_bytes = (G == 1 ? p.rows_a : kBM) * kBlock;
+  const int stage_bytes = a_bytes + (G == 1 ? p.bn : kBN / 2) * kBlock;
+  const int stages = G == 1 ? p.stages : 5;
   Work work;
   work.tiles_m = static_cast<int>((p.m + G * kBM - 1) / (G * kBM));
   work.tiles_n = static_cast<int>((p.n + p.bn - 1) / p.bn);
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     if (p.bulk_out) prefetch_tmap(&p.o);
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
     }
@@ -347,10 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       }
     } else if (warp == kLoadWarp && elect_one()) {
       // ---- loads of codes ----
-      Ring<kStages> st;
+      Ring st(stages);
       uint32_t used = 0;  // stages that have been loaded at least once
       bool ok = true;
-      const uint32_t bytes = G * S::kABytes + p.bn * kBlock;  // of a stage, of the pair together
+      const uint32_t bytes = G * a_bytes + p.bn * kBlock;  // of a stage, of the pair together
       long long loads = 0;
       for (int t = work.first; ok && t < work.tiles; t += work.stride) {
         const Tile tl = work.tile(t);
@@ -358,12 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           if (!(ok = wait_or_dead(s, &s.empty[st.slot], st.phase ^ 1u, p.fault))) break;
           // a pair's loads all complete on the even CTA's barrier
           if (rank == 0) mbar_expect_tx(&s.full[st.slot], bytes + stall_extra(p.stall_at, blockIdx.x, loads++));
+          uint8_t* a = s.ring + st.slot * stage_bytes;
           if constexpr (G == 1) {
-            tma_load_2d(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
-            tma_load_2d(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0);
+            tma_load_2d(a, &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
+            tma_load_2d(a + a_bytes, &p.b, &s.full[st.slot], kb * kBlock, tl.n0);
           } else {
-            tma_load_2d_pair(s.a[st.slot], &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
-            tma_load_2d_pair(s.b[st.slot], &p.b, &s.full[st.slot], kb * kBlock, tl.n0 + rank * (p.bn / G));
+            tma_load_2d_pair(a, &p.a, &s.full[st.slot], kb * kBlock, tl.m0);
+            tma_load_2d_pair(a + a_bytes, &p.b, &s.full[st.slot], kb * kBlock, tl.n0 + rank * (p.bn / G));
           }
           used |= 1u << st.slot;
           st.next();
@@ -374,14 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       // the others in the one before.  (A pair's stages complete on the even CTA's barriers; the odd
       // one waits for it at the end.)
       if (!ok) {
-        for (int i = 0; i < kStages; ++i)
+        for (int i = 0; i < stages; ++i)
           if (rank == 0 && (used >> i & 1u)) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
       }
     } else if (warp == kScaleLoadWarp && elect_one()) {
       // ---- loads of scales, in the same queue as the codes': a plain load would wait behind every
       // stage that is under way.  (From the codes' thread they cost it half of its time.) ----
       Chains in(work);
-      Ring<kScaleSlots> sc;
+      Ring sc(kScaleSlots);
       uint32_t used = 0;
       bool ok = true;
       for (; in.more(); in.next()) {
@@ -401,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     } else if (warp == kMmaWarp && rank == 0 && elect_one()) {
       // ---- tensor-core instructions ----
       const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, G * kBM, p.bn);
-      Ring<kStages> st;
-      Ring<kScaleSlots> sc;
-      Ring<2> acc;
+      Ring st(stages);
+      Ring sc(kScaleSlots);
+      Ring acc(2);
       bool ok = true;
       for (int t = work.first; ok && t < work.tiles; t += work.stride) {
         for (int kb = 0; ok && kb < work.blocks; kb += kChain) {
@@ -418,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
             if (kb + j >= work.blocks) break;
             if (!(ok = wait_or_dead(s, &s.full[st.slot], st.phase, p.fault))) break;
             tensor_fence_after();
-            const uint64_t da = operand_desc(smem_addr(s.a[st.slot])), db = operand_desc(smem_addr(s.b[st.slot]));
+            const uint32_t a = smem_addr(s.ring) + st.slot * stage_bytes;
+            const uint64_t da = operand_desc(a), db = operand_desc(a + a_bytes);
 #pragma unroll
             for (int k = 0; k < kBlock / 32; ++k)  // 32 bytes along the swizzled row: 2 units of 16
               tensor_mma_mxf8<G>(tmem + acc.slot * kBN, da + 2 * k, db + 2 * k, idesc | mxf8_scale_byte(j), sf, sf + 4,
@@ -439,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     // ---- float32 sums: warp w holds rows 32 (w & 3) .., columns bn / 2 (w >> 2) .. ----
     const int cols = p.bn / 2, col0 = cols * (warp >> 2);
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + col0;
-    Ring<2> acc;
+    Ring acc(2);
     bool ok = true;
     for (int t = work.first; ok && t < work.tiles; t += work.stride) {
       const Tile tl = work.tile(t);
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       if (!ok) break;
       if (G == 1 && p.split > 1) {
         // to shared memory, unit u (four columns) of row r at [u][r]
-        float4* red = reinterpret_cast<float4*>(s.a);
+        float4* red = reinterpret_cast<float4*>(s.ring);
 #pragma unroll
         for (int u = 0; u < kCols / 4; ++u) {
           if (4 * u < cols) {
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     const Tile tl = work.tile(work.first);
     const int units = p.bn / 4, row = threadIdx.x & (kBM - 1);
     const int hi = units * (part + 1) / p.split;
-    const uint32_t red = smem_addr(s.a);
+    const uint32_t red = smem_addr(s.ring);
     for (int u = units * part / p.split + (threadIdx.x >> 7); u < hi && tl.m0 + row < p.m; u += kThreads / kBM) {
       float4 v[kMaxSplit];
 #pragma unroll
@@ -560,16 +569,30 @@ static int g_clusters[kMaxSplit + 1];
 
 // Few tiles (128 x 224 ones that would leave half of the SMs idle, or m that fills no pair): one CTA
 // per tile, with k cut into parts where that pays.  Otherwise pairs.  Either way the cheapest width
-// (and number of parts) in cycles: a block costs a pair max(2 bn, 256 + bn) (the tensor cores, or
-// what a CTA reads at 64 bytes a cycle), and a single CTA 256 + 2 bn; a pair's tile about 2500 more;
-// joining parts about 9000 and the reading of a tile of sums (64 x 8192 x 2048 and 768 x 768 x 8192
-// spent 6000 to 9000 on it; at 6000 here, 32 x 8192 x 2048 was cut and took 15.0 us of 12.3).
+// (and number of parts) in cycles.
+//
+// A pair: a block costs max(2 bn, 256 + bn) (the tensor cores, or what a CTA reads at 64 bytes a
+// cycle), a tile about 2500 more.
+//
+// A single CTA: a block costs what the CTA reads, the tensor core, or a stage's round trip of about
+// 2200 shared by the stages, whichever is longest (at 1400, 8 x 2048 x 8192 was cut into too few parts
+// and took 13.8 us of 9.1; at 3200, 200 x 2048 x 8192 took 13.7 of 12.2).  Joining parts costs about
+// 9000 and the reading of a tile of sums.  A tile that is not cut is staged, where eight rows' 16-byte
+// stores of bn bytes apart meet in the same banks, 8 ways at widths of whole 128s, 4 of 64s, 2 of 32s:
+// 2 bn cycles for each way (32 x 1024 x 128 at widths 64, 96 .. 224: 3.75, 3.80, 4.76, 4.11, 4.65,
+// 4.45 us).  Stores in another order for each row have no conflicts, but the exchange of registers
+// before them cost every width 0.6 to 1 us: it is code that runs once.
 MatmulPlan plan_matmul(long long m, long long n, int kb) {
   const int sms = g_clusters[1];
   const auto tiles = [&](int rows, int bn) { return ((m + rows - 1) / rows) * ((n + bn - 1) / bn); };
   MatmulPlan plan;
   plan.split = 1;
   plan.group = m <= kBM || 2 * tiles(kBM, kBN) <= sms ? 1 : 2;
+  int rows_a = kBM;
+  const auto stages_of = [&](int bn) {
+    const int fit = Shared<1>::kRingBytes / ((rows_a + bn) * kBlock);
+    return fit < kMaxStages ? fit : kMaxStages;
+  };
   double best = 0;
   const auto offer = [&](int bn, int split, double cost, long long grid) {
     if (best == 0 || cost < best) {
@@ -582,12 +605,16 @@ MatmulPlan plan_matmul(long long m, long long n, int kb) {
   if (plan.group == 1) {
     const int chains = (kb + kChain - 1) / kChain;
     const double rows = m < kBM ? m : kBM;
+    rows_a = m < kBM ? static_cast<int>(m + 7) / 8 * 8 : kBM;
     for (int bn = kBN; bn >= 64; bn -= 32) {
       const long long t = tiles(kBM, bn);
       for (int split = 1; split <= kMaxSplit && (split == 1 || (split <= chains && t <= g_clusters[split])); ++split) {
         const double rounds = static_cast<double>((t + g_clusters[split] - 1) / g_clusters[split]);
-        const double join = split > 1 ? 9000 + rows * bn / 8 : 0;
-        offer(bn, split, rounds * (((kb + split - 1) / split) * (256.0 + 2 * bn) + join + 1000), t * split);
+        const double ways = bn % 128 == 0 ? 8 : bn % 64 == 0 ? 4 : 2;
+        const double end = split > 1 ? 10000 + rows * bn / 8 : 500 + 2 * bn * ways;
+        const int bytes = (rows_a + bn) * kBlock;
+        const double block = std::max({bytes / 64.0, 2.0 * bn, 2200.0 / stages_of(bn)});
+        offer(bn, split, rounds * (((kb + split - 1) / split) * block + end), t * split);
       }
     }
   } else {
@@ -598,7 +625,8 @@ MatmulPlan plan_matmul(long long m, long long n, int kb) {
             2 * (t < pairs ? t : pairs));
     }
   }
-  plan.rows_a = kBM;
+  plan.rows_a = rows_a;
+  plan.stages = plan.group == 1 ? stages_of(plan.bn) : 5;
   plan.rows_b = plan.bn / plan.group;
   plan.chain = kChain;
   return plan;

@@ -275,13 +275,14 @@ __device__ __forceinline__ void arrive_here(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// A position in a ring of N slots: the slot, and the parity of its current phase.
-template <int N>
+// A position in a ring of `size` slots: the slot, and the parity of its current phase.
 struct Ring {
+  int size;
   int slot = 0;
   uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int n) : size(n) {}
   __device__ __forceinline__ void next() {
-    if (++slot == N) {
+    if (++slot == size) {
       slot = 0;
       phase ^= 1u;
     }

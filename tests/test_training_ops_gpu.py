@@ -340,6 +340,22 @@ def test_matmul_non_finite():
     assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
 
 
+@pytest.mark.parametrize("m", [1, 7, 8, 9, 57, 64, 65, 104, 121, 127])
+@pytest.mark.parametrize("n,k", [(500, 4200), (5000, 300)])
+def test_matmul_of_few_rows(m, n, k):
+    """Fewer rows than the tensor core multiplies: stages hold only those, and there are more of them."""
+    check_product(m, n, k)
+
+
+@pytest.mark.parametrize("m", [1, 9, 121])
+def test_matmul_of_few_rows_next_to_non_finite_codes(m):
+    """What the tensor core reads past a's rows (b's codes, a NaN among them) reaches no result."""
+    xa, xb = draw(m, 1300, "f32", 43), draw(600, 1300, "f32", 44)
+    xb[::2] = float("nan")
+    got = f64(dm.fp8_matmul(dm.fp8_quantize(xa), dm.fp8_quantize(xb), dtype=torch.float32))
+    assert np.isnan(got[:, ::2]).all() and np.isfinite(got[:, 1::2]).all()
+
+
 @pytest.mark.parametrize("m,n,k", [(300, 500, 1500), (3000, 1500, 700)])
 def test_matmul_repeats_to_the_bit_and_on_another_stream(m, n, k):
     a, _ = quantized(m, k, seed=37)
@@ -548,3 +564,26 @@ def test_linear_repeats_with_any_share_of_the_rows(row_blocks):
             dm.fp8_linear(x, w, out=out)
         assert all(torch.equal(out, first) for out in outs)
     assert dm.device_fault() == 0
+
+
+@pytest.mark.parametrize("m,k", [(1024, 4096), (256, 8192)])
+def test_a_product_is_complete_when_the_next_encode_reads_it(m, k):
+    """A gradient that a product writes last, encoded at once: the later replicas' encodes start before
+    their predecessor's end, but not before the product's."""
+    n, R = 2048, 3
+    kw = dict(k=8, mode="demo", seed=4, step=2, wire="f32", beta=0.99, sign=True)
+    ops = [(quantized(m, k, "e5m2", seed=95 + r)[0], quantized(n, k, seed=98 + r)[0]) for r in range(R)]
+    runs = []
+    for wait in (True, False, False, False):
+        g = [torch.zeros(m * n, device="cuda") for _ in range(R)]
+        mom = [torch.zeros(m * n, device="cuda") for _ in range(R)]
+        pay = [dm.payload_buffers("demo", m * n, 8, step=2, wire="f32") for _ in range(R)]
+        torch.cuda.synchronize()
+        for r in range(R):
+            dm.fp8_matmul(*ops[r], out=g[r].view(m, n), add=True)
+        if wait:
+            torch.cuda.synchronize()
+        dm.encode_replicas(g, mom, [p[0] for p in pay], [p[1] for p in pay], **kw)
+        runs.append(mom + [t for p in pay for t in p])
+    for got in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got, runs[0]))
