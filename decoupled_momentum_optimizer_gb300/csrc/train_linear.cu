@@ -1,14 +1,14 @@
 // x w^T for a few rows of x (tokens being generated) and w in 8-bit floating point, block-scaled: one
 // kernel that quantizes x, multiplies and scales, bound by reading w once.
 //
-// One CTA per SM streams its rows of w through a ring of shared-memory stages: one thread keeps
-// TMA loads of 16 rows x 4 blocks (8 KB, with their scales) under way, up to 128 KB of them, while
-// sixteen warps first quantize all of x into shared memory (four lanes a block, 32 elements each;
-// every SM repeats that, behind the first stages' arrival) and then multiply.  A
-// group of four warps owns 16 rows at a time, the instruction's 16 x 32 operand, each warp one of a
-// stage's four blocks; the four join their sums in order.  The instruction's k order is free as long
-// as both operands agree, so lane (g, c) takes 16 consecutive codes of row g at 16 c and at 64 + 16 c
-// of a block, whole 16-byte reads of either operand.
+// One CTA per SM streams its rows of w through shared memory: one thread keeps TMA loads of 16 rows x
+// 4 blocks (8 KB, with their scales) under way, up to 128 KB of them, while sixteen warps first quantize
+// all of x into shared memory (four lanes a block, 32 elements each; every SM repeats that, behind the
+// first stages' arrival) and then multiply.  A group of four warps has a ring of stages of its own and
+// owns 16 rows at a time, the instruction's 16 x 32 operand, each warp one of a stage's four blocks;
+// the four join their sums in order.  The instruction's k order is free as long as both operands agree,
+// so lane (g, c) takes 16 consecutive codes of row g at 16 c and at 64 + 16 c of a block, whole 16-byte
+// reads of either operand.
 //
 // The block's 128 products accumulate in the instruction's float32, blocks in IEEE float32.
 //
