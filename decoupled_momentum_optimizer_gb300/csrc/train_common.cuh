@@ -118,6 +118,16 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits, int top) {
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// A scale as the tensor core takes it, an exponent byte (UE8M0).  A quantized matrix's scales are 0 or
+// powers of two from 2^-126 to 2^127; any other would lose its significand or sign without a word, so it
+// becomes the byte of NaN, in every product.  (Turned left by nine bits, a power of two is its exponent,
+// and whatever has a sign or a significand is above 255.)  0 is taken for 2^-127.
+constexpr uint32_t kScaleNaN = 255;
+__device__ __forceinline__ uint32_t scale_byte(float s) {
+  const uint32_t bits = __float_as_uint(s), r = __funnelshift_l(bits, bits, 9);
+  return r < kScaleNaN ? r : kScaleNaN;
+}
+
 // A non-finite element becomes a NaN code (neither format's codes saturate silently); it does not
 // take part in its block's scale (fmaxf passes over a NaN).
 __device__ __forceinline__ float finite_or_nan(float v) {

@@ -217,6 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint4 x10 = *reinterpret_cast<const uint4*>(w1 + ((c ^ g) << 4));
         const uint4 x11 = *reinterpret_cast<const uint4*>(w1 + (((c + 4) ^ g) << 4));
         const float s0 = s.ws[slot][w4][g], s1 = s.ws[slot][w4][g + 8];
+        // what the products' sums start from: NaN under a scale that is no power of two
+        const float nan = __uint_as_float(0x7fc00000u);
+        const float z0 = scale_byte(s0) == kScaleNaN ? nan : 0.0f, z1 = scale_byte(s1) == kScaleNaN ? nan : 0.0f;
         if (kb < p.kb) {
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             // this lane's results are rows g, g + 8 and tokens 2 c, 2 c + 1
             const float u0 = m0 < p.m ? scales[m0 * p.kb + kb] : 0.0f;
             const float u1 = m0 + 1 < p.m ? scales[(m0 + 1) * p.kb + kb] : 0.0f;
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float d[4] = {z0, z0, z1, z1};
             mma_f8<WFMT>(d, x00.x, x10.x, x00.y, x10.y, b0.x, b0.y);
             mma_f8<WFMT>(d, x00.z, x10.z, x00.w, x10.w, b0.z, b0.w);
             mma_f8<WFMT>(d, x01.x, x11.x, x01.y, x11.y, b1.x, b1.y);

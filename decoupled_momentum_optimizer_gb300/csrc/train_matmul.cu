@@ -139,7 +139,7 @@ __device__ __forceinline__ uint4 scale_words(const float* v, int ld, int rows, i
     if (32 * i < rows) {
       w[i] = 0;
 #pragma unroll
-      for (int j = 0; j < kChain; ++j) w[i] |= ((__float_as_uint(v[j * ld + 32 * i + lane]) >> 23) & 0xffu) << (8 * j);
+      for (int j = 0; j < kChain; ++j) w[i] |= scale_byte(v[j * ld + 32 * i + lane]) << (8 * j);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);

@@ -127,13 +127,16 @@ class Fp8Matrix:
 
     ``codes``  float8 [rows, ceil(k / 128) * 128], zero past k
     ``scales`` float32 [ceil(k / 128), rows rounded up to 4]: element (r, c) is
-               ``codes[r, c] * scales[c // 128, r]``
+               ``codes[r, c] * scales[c // 128, r]``.  Every scale is a power of two from 2^-126 to 2^127,
+               as :func:`fp8_quantize` writes them (0 only where its block's codes are 0); the products
+               make NaN of the results that any other scale takes part in.  ``check=True`` refuses
+               such scales here (it waits for the device).
     ``tiles``  whether the scales are equal within each 128 rows as well
     """
 
     __slots__ = ("codes", "scales", "shape", "tiles")
 
-    def __init__(self, codes, scales, k, *, tiles=False):
+    def __init__(self, codes, scales, k, *, tiles=False, check=False):
         if codes.dtype not in _FMT_OF or codes.dim() != 2:
             raise TypeError("codes must be a 2-D float8_e4m3fn or float8_e5m2 tensor")
         rows, width = codes.shape
@@ -146,6 +149,10 @@ class Fp8Matrix:
             raise ValueError("codes and scales must be contiguous")
         if not codes.is_cuda or scales.get_device() != codes.get_device():
             raise ValueError("codes and scales must be on one CUDA device (there is no CPU path)")
+        if check:
+            bits = scales[:, :rows].view(torch.int32)
+            if not bool((((bits & -0x7f800001) == 0) & (bits != 0x7f800000)).all()):
+                raise ValueError("scales must be powers of two from 2^-126 to 2^127 (or 0)")
         self.codes, self.scales, self.shape, self.tiles = codes, scales, (rows, k), tiles
 
     @classmethod

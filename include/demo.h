@@ -351,6 +351,10 @@ int demo_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, 
  *   codes   uint8 [rows][128 K], zero past k
  *   scales  float32 [K][rows rounded up to 4]
  *   X[r][c] = value(codes[r][c]) * scales[c / 128][r]
+ * Every scale is a power of two from 2^-126 to 2^127, as demo_fp8_quantize writes them (or 0, where
+ * the codes of its block are all 0): the tensor core applies an exponent.  The products make NaN of
+ * the results that any other scale takes part in, so codes whose scales have a significand, from
+ * elsewhere, have to be quantized anew.  What lies past the matrix's rows in either buffer is not used.
  * demo_fp8_bytes returns the codes' bytes and, through scale_bytes (if not NULL), the scales' (host
  * only; 0 for negative sizes).  Both buffers are 16-byte aligned.
  */
@@ -375,10 +379,11 @@ int demo_fp8_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64
 
 /*
  * demo_fp8_matmul -- out = A B^T (out += A B^T if add, float32 only): A [m, k] and B [n, k]
- * quantized by rows.  The scales are powers of two from 2^-126 to 2^127, as demo_fp8_quantize
- * writes them: the tensor core applies them (only a scale's exponent is read).
+ * quantized by rows.
  *   out       [m, n] of out_dtype, apart from every input
- * Sums over 512 of k run in the tensor core's float32 accumulator, longer ones in IEEE float32.  NaN codes give NaN results.  k = 0 gives zeros (or leaves out as it is, if add).
+ * Sums over 512 of k run in the tensor core's float32 accumulator, longer ones in IEEE float32.  NaN
+ * codes, and scales that are no power of two, give NaN results.  k = 0 gives zeros (or leaves out as it
+ * is, if add).
  */
 int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,
                     int b_fmt, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
@@ -388,6 +393,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
  * demo_fp8_linear -- out = Q(x) W^T: x [m, k] of dtype, quantized by rows to e4m3 within the call
  * (as demo_fp8_quantize does), W [n, k] quantized by rows; out [m, n] of out_dtype.  The serving
  * form of the product: few rows of x (one token's) are quantized by the kernel that multiplies.
+ * NaN codes, and scales that are no power of two, give NaN results here too, for any m.
  *   workspace   device, 16-byte aligned, at least demo_fp8_linear_workspace(m, n, k) bytes (host
  *               only; 0 for few rows, then workspace may be NULL), apart from the other buffers;
  *               fewer bytes give DEMO_ENOSPACE.  Its contents mean nothing between calls.
