@@ -84,6 +84,15 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
   return r;
 }
 
+// sum + d s u for two scales s and u.  Either one, or their product, can leave float32's range with d
+// where d s u does not; so the sum of the two exponents is applied in two halves.  d times the first is
+// exact unless d s u overflows or vanishes itself.
+__device__ __forceinline__ float add_scaled(float sum, float d, float s, float u) {
+  const uint32_t e = __float_as_uint(s) + __float_as_uint(u);  // exponents alone, 254 at most each
+  const uint32_t half = (e >> 1) & 0x7f800000u;
+  return fmaf(d * __uint_as_float(half), __uint_as_float(e - half), sum);
+}
+
 // Shared memory behind LinearShared: the warps' sums [warp][m][16 rows], x's codes [m][128 kb] (tokens
 // of odd number have the halves of every block swapped, so that eight lanes of a 16-byte read reach
 // different banks) and scales [m][kb].
@@ -238,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             mma_f8<WFMT>(d, x00.z, x10.z, x00.w, x10.w, b0.z, b0.w);
             mma_f8<WFMT>(d, x01.x, x11.x, x01.y, x11.y, b1.x, b1.y);
             mma_f8<WFMT>(d, x01.z, x11.z, x01.w, x11.w, b1.z, b1.w);
-            sum[t][0] = fmaf(d[0] * s0, u0, sum[t][0]);
-            sum[t][1] = fmaf(d[1] * s0, u1, sum[t][1]);
-            sum[t][2] = fmaf(d[2] * s1, u0, sum[t][2]);
-            sum[t][3] = fmaf(d[3] * s1, u1, sum[t][3]);
+            sum[t][0] = add_scaled(sum[t][0], d[0], s0, u0);
+            sum[t][1] = add_scaled(sum[t][1], d[1], s0, u1);
+            sum[t][2] = add_scaled(sum[t][2], d[2], s1, u0);
+            sum[t][3] = add_scaled(sum[t][3], d[3], s1, u1);
           }
         }
         __syncwarp();

@@ -74,3 +74,57 @@ def test_check_of_given_scales():
         dm.Fp8Matrix(q.codes, s, 300)
         with pytest.raises(ValueError, match="powers of two"):
             dm.Fp8Matrix(q.codes, s, 300, check=True)
+
+
+def check_linear_range(x, w, k):
+    """fp8_linear of x and w against 64 bits wherever no sum of magnitudes comes near float32's largest
+    value; infinite or NaN where the result is above it."""
+    m = x.shape[0]
+    q = dm.fp8_quantize(w.cuda())
+    xv = ref.values(*ref.quantize(x.double().numpy(), "e4m3"), k)
+    want, total = ref.product(xv, ref.values(f64(q.codes), f64(q.scales), k))
+    got = f64(dm.fp8_linear(x.cuda(), q))
+    largest = float(np.finfo(np.float32).max)
+    inside = total < largest / 4
+    # A block's term and the sum it joins lose half of the smallest step each; the tensor core's sums are
+    # not held to float32's subnormal steps.
+    tiny = (2 * ((k + 127) // 128) + 4) * 2.0 ** -149 if m <= 40 else 2.0 ** -126
+    tol = ref.product_tolerance(total, k) + ref.round_tolerance(want, "f32") + tiny
+    assert (np.abs(got - want) <= tol)[inside].all()
+    assert not np.isfinite(got[np.abs(want) > 1.01 * largest]).any()
+    return inside
+
+
+@pytest.mark.parametrize("m", [5, 9, 20, 40, 41, 200])
+@pytest.mark.parametrize("k", [515, 1700])
+def test_linear_between_the_ends_of_the_range(m, k):
+    """Tokens and rows of w of every size, and of one size in a block and another in the next: the scales'
+    product, or a sum times one of them, leaves float32's range where the result does not."""
+    sizes = [2.0 ** e for e in (-124, -70, 0, 70, 123)]
+    x, w = normal(m, k, 11), normal(130, k, 12)
+    for i, size in enumerate(sizes):
+        x[i::5] *= size / x[i::5].abs().max()
+        w[i::5] *= size / w[i::5].abs().max()
+    x[:, 128:256] *= 2.0 ** -40
+    w[:, 128:256] = (w[:, 128:256] * 2.0 ** 40).clamp(-2.0 ** 123, 2.0 ** 123)
+    inside = check_linear_range(x, w, k)
+    assert 0.5 < inside.mean() < 0.9
+
+
+@pytest.mark.parametrize("m", [3, 20, 100])
+def test_linear_of_small_codes_under_large_scales(m):
+    """The scales' product is 2^130 where the result is 2^112, or 0."""
+    x, w = torch.zeros(m, 300), torch.zeros(50, 300)
+    x[:, 7], x[:, 8] = 448 * 2.0 ** 65, 2.0 ** -9 * 2.0 ** 65
+    w[:, 9], w[:25, 8] = 448 * 2.0 ** 65, 2.0 ** -9 * 2.0 ** 65
+    got = f64(dm.fp8_linear(x.cuda(), dm.fp8_quantize(w.cuda())))
+    assert (got[:, :25] == 2.0 ** 112).all() and (got[:, 25:] == 0).all()
+
+
+@pytest.mark.parametrize("m", [3, 20, 100])
+def test_linear_of_large_values_that_do_not_meet(m):
+    """Blocks with float32's largest powers of two in both, opposite zeros: no infinity times zero."""
+    x, w = torch.ones(m, 300), torch.zeros(50, 300)
+    x[:, 7] = 2.0 ** 127
+    w[:, 8], w[:, 200] = 2.0 ** 127, 1.0  # column 8 meets ones whose codes beside 2^127 are 0
+    assert (f64(dm.fp8_linear(x.cuda(), dm.fp8_quantize(w.cuda()))) == 1.0).all()
