@@ -237,6 +237,7 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   }
   DeviceInfo dev;
   if ((s = device_info(&dev)) != DEMO_OK) return s;
+  if (k == 0 && add) return DEMO_OK;  // adding zeros would turn -0 into 0
   MatmulParams q;
   std::memset(&q, 0, sizeof(q));
   q.kb = static_cast<int>(up(k, kBlock) / kBlock);

@@ -128,3 +128,30 @@ def test_linear_of_large_values_that_do_not_meet(m):
     x[:, 7] = 2.0 ** 127
     w[:, 8], w[:, 200] = 2.0 ** 127, 1.0  # column 8 meets ones whose codes beside 2^127 are 0
     assert (f64(dm.fp8_linear(x.cuda(), dm.fp8_quantize(w.cuda()))) == 1.0).all()
+
+
+@pytest.mark.parametrize("m,n", [(5, 7), (5, 8), (3000, 1301), (3000, 1304)])
+def test_an_empty_sum_leaves_out_as_it_is(m, n):
+    """To the bit: -0, subnormal values, NaN with their payloads."""
+    out = torch.full((m, n), -0.0, device="cuda")
+    out[::2, 3], out[1, 1] = 1e-42, 3.0
+    out.view(torch.int32)[2, 2] = 0x7FC12345
+    want = out.clone()
+    dm.fp8_matmul(dm.Fp8Matrix.empty(m, 0), dm.Fp8Matrix.empty(n, 0), out=out, add=True)
+    assert torch.equal(out.view(torch.int32), want.view(torch.int32))
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 300, 700), (200, 300, 2000), (2100, 1300, 700)])
+@pytest.mark.parametrize("pad", [0, 1, 4])
+def test_add_keeps_subnormal_values(m, n, k, pad):
+    """The addition is float32's with its subnormal values, whichever way the result is written (bulk
+    reductions of whole 16-byte units, single elements, the join of parts of k)."""
+    x, y = torch.zeros(m, k), torch.zeros(n, k)
+    x[:, 5], y[1::2, 5] = 1.0, 2.0 ** -126
+    out = torch.empty(m, n + pad, device="cuda")[:, :n]
+    out[:, ::2] = torch.tensor([1e-40, -1e-45], device="cuda").repeat(m)[:m, None]
+    out[:, 1::2] = -1.5 * 2.0 ** -126  # a subnormal sum
+    want = out.clone()
+    want[:, 1::2] = -(2.0 ** -127)
+    dm.fp8_matmul(dm.fp8_quantize(x.cuda()), dm.fp8_quantize(y.cuda()), out=out, add=True)
+    assert torch.equal(out, want)
