@@ -273,7 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           q[kRows + 8] = sum[t][3];
         }
       }
-      named_sync(2 + group, 32 * kQuad);
+      // The group goes on or stops as one: a warp that gave up must not leave the others at a barrier, and
+      // they may have found the stage it gave up on complete.
+      ok = named_all(2 + group, 32 * kQuad, ok);
       const long long n0 = static_cast<long long>(blockIdx.x + static_cast<long long>(first + group) * gridDim.x) * kRows;
       for (int i = 32 * w4 + lane; ok && i < p.m * kRows; i += 32 * kQuad) {
         const int m = i / kRows, r = i % kRows;

@@ -155,3 +155,17 @@ def test_add_keeps_subnormal_values(m, n, k, pad):
     want[:, 1::2] = -(2.0 ** -127)
     dm.fp8_matmul(dm.fp8_quantize(x.cuda()), dm.fp8_quantize(y.cuda()), out=out, add=True)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("item", [0, 13, 16, 23])
+def test_linear_ends_when_a_load_of_any_round_never_completes(item):
+    """Six row blocks on the first CTA, in two rounds of its groups of warps (16 and 8 loads): every group
+    stops as one, in either round, and the next call is right."""
+    n, k = 16 * (5 * torch.cuda.get_device_properties(0).multi_processor_count + 3), 2000
+    w, x = dm.fp8_quantize(normal(n, k, 21).cuda()), normal(3, k, 22).cuda()
+    want = dm.fp8_linear(x, w)
+    assert dm.device_fault() == 0
+    dm.test_stall_next_launch(item)
+    dm.fp8_linear(x, w)
+    assert dm.device_fault() == 1
+    assert torch.equal(dm.fp8_linear(x, w), want) and dm.device_fault() == 0
