@@ -155,9 +155,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           }
         }
       }
-      if (!ok)  // stopped early: wait (bounded) for the copies that are under way
-        for (int i = 0; i < kStages; ++i)
-          if (used >> i & 1u) mbar_wait_bounded(&s.full[i], last >> i & 1u);
+      // No copy may be under way when the CTA ends, and whoever waits for the last ones may give up: wait
+      // (bounded) here too.
+      for (int i = 0; i < kStages; ++i)
+        if (used >> i & 1u) mbar_wait_bounded(&s.full[i], last >> i & 1u);
     }
   } else {
     // ---- x: a warp quantizes eight blocks of 128 at a time, four lanes each, 32 elements a lane ----

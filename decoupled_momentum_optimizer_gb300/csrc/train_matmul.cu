@@ -377,23 +377,21 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           st.next();
         }
       }
-      // Stopped early: copies may be in flight into this CTA's shared memory.  Wait (bounded) for
-      // the last load of every stage: those before the ring's position are in its current phase,
-      // the others in the one before.  (A pair's stages complete on the even CTA's barriers; the odd
-      // one waits for it at the end.)
-      if (!ok) {
-        for (int i = 0; i < stages; ++i)
-          if (rank == 0 && (used >> i & 1u)) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
-      }
+      // No copy may be in flight into this CTA's shared memory when it ends, and whoever stopped early,
+      // here or among those who use the stages, waits for none.  Wait (bounded) for the last load of
+      // every stage: those before the ring's position are in its current phase, the others in the one
+      // before.  (A pair's stages complete on the even CTA's barriers; the odd one waits for it at the
+      // end.)
+      for (int i = 0; i < stages; ++i)
+        if (rank == 0 && (used >> i & 1u)) mbar_wait_bounded(&s.full[i], i < st.slot ? st.phase : st.phase ^ 1u);
     } else if (warp == kScaleLoadWarp && elect_one()) {
       // ---- loads of scales, in the same queue as the codes': a plain load would wait behind every
       // stage that is under way.  (From the codes' thread they cost it half of its time.) ----
       Chains in(work);
       Ring sc(kScaleSlots);
       uint32_t used = 0;
-      bool ok = true;
       for (; in.more(); in.next()) {
-        if (!(ok = wait_or_dead(s, &s.sempty[sc.slot], sc.phase ^ 1u, p.fault))) break;
+        if (!wait_or_dead(s, &s.sempty[sc.slot], sc.phase ^ 1u, p.fault)) break;
         const Tile tl = work.tile(in.t);
         const int kb = work.kb0 + kChain * in.c;  // rows past the last block are filled, or not used
         mbar_expect_tx(&s.sfull[sc.slot], kChain * (kBM + p.bn) * 4);
@@ -402,10 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         used |= 1u << sc.slot;
         sc.next();
       }
-      if (!ok) {
-        for (int i = 0; i < kScaleSlots; ++i)
-          if (used >> i & 1u) mbar_wait_bounded(&s.sfull[i], i < sc.slot ? sc.phase : sc.phase ^ 1u);
-      }
+      for (int i = 0; i < kScaleSlots; ++i)
+        if (used >> i & 1u) mbar_wait_bounded(&s.sfull[i], i < sc.slot ? sc.phase : sc.phase ^ 1u);
     } else if (warp == kMmaWarp && rank == 0 && elect_one()) {
       // ---- tensor-core instructions ----
       const uint32_t idesc = mxf8_instruction(p.a_fmt, p.b_fmt, G * kBM, p.bn);

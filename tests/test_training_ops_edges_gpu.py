@@ -169,3 +169,15 @@ def test_linear_ends_when_a_load_of_any_round_never_completes(item):
     dm.fp8_linear(x, w)
     assert dm.device_fault() == 1
     assert torch.equal(dm.fp8_linear(x, w), want) and dm.device_fault() == 0
+
+
+@pytest.mark.parametrize("m,n,k,item", [(2100, 1300, 700, 5), (200, 300, 2000, 1), (3, 300, 700, 5)])
+def test_matmul_ends_when_one_of_its_last_loads_never_completes(m, n, k, item):
+    """The thread that loads has nothing left to ask for by then: it stays until its copies have landed."""
+    a, b = dm.fp8_quantize(normal(m, k, 23).cuda()), dm.fp8_quantize(normal(n, k, 24).cuda())
+    want = dm.fp8_matmul(a, b)
+    assert dm.device_fault() == 0
+    dm.test_stall_next_launch(item)
+    dm.fp8_matmul(a, b)
+    assert dm.device_fault() == 1
+    assert torch.equal(dm.fp8_matmul(a, b), want) and dm.device_fault() == 0
