@@ -59,6 +59,17 @@ _SIGS = {
                                                   ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_vp,
                                                   ctypes.c_int, _c_vp, ctypes.c_int, _c_u64, _c_u64, ctypes.c_int,
                                                   ctypes.c_int, _c_vp, _c_vp]),
+    "demo_dropout": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, ctypes.c_int, _c_i64, _c_i64,
+                                    ctypes.c_double, _c_u64, _c_u64, _c_u64, _c_vp]),
+    "demo_fp8_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "demo_fp8_quantize": (ctypes.c_int, [_c_vp, _c_i64, ctypes.c_int, _c_i64, _c_i64, ctypes.c_int, _c_vp, _c_i64,
+                                         ctypes.c_double, _c_u64, _c_u64, _c_u64, ctypes.c_int, ctypes.c_int, _c_vp,
+                                         _c_vp, _c_vp, _c_vp, _c_vp]),
+    "demo_fp8_matmul": (ctypes.c_int, [_c_vp, _c_vp, ctypes.c_int, _c_vp, _c_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64,
+                                       _c_vp, _c_i64, ctypes.c_int, ctypes.c_int, _c_vp]),
+    "demo_fp8_linear_workspace": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
+    "demo_fp8_linear": (ctypes.c_int, [_c_vp, _c_i64, ctypes.c_int, _c_vp, _c_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64,
+                                       _c_vp, _c_i64, ctypes.c_int, _c_vp, ctypes.c_size_t, _c_vp]),
     "demo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "demo_device_fault": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint)]),
     "demo_test_stall_next_launch": (ctypes.c_int, [ctypes.c_longlong]),
@@ -87,9 +98,7 @@ def lib():
         except ImportError:  # pragma: no cover
             pass
         L = ctypes.CDLL(LIB_PATH)
-        from .training_ops import SIGS
-
-        for name, (res, args) in {**_SIGS, **SIGS}.items():
+        for name, (res, args) in _SIGS.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args

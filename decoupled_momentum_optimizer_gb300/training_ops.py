@@ -6,7 +6,6 @@ torch unless an ``out`` is given, the call runs on torch's current stream (or on
 were the current one) and raises :class:`DemoError` on a negative status.
 """
 
-import ctypes
 import functools
 
 import torch
@@ -301,18 +300,3 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     _run("demo_fp8_linear", (xp, ldx, _DTYPES[x.dtype], wc.data_ptr(), w.scales.data_ptr(), _FMT_OF[wc.dtype], m, n, k,
                              op, ldo, odt, wp, need), index)
     return out
-
-
-_c_i64, _c_u64, _c_vp, _c_int, _c_f64 = ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_int, ctypes.c_double
-SIGS = {
-    "demo_dropout": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_f64, _c_u64,
-                              _c_u64, _c_u64, _c_vp]),
-    "demo_fp8_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, ctypes.POINTER(ctypes.c_size_t)]),
-    "demo_fp8_quantize": (_c_int, [_c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_f64, _c_u64,
-                                   _c_u64, _c_u64, _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
-    "demo_fp8_matmul": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
-                                 _c_int, _c_int, _c_vp]),
-    "demo_fp8_linear_workspace": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
-    "demo_fp8_linear": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64,
-                                 _c_int, _c_vp, ctypes.c_size_t, _c_vp]),
-}
