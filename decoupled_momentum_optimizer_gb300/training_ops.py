@@ -4,6 +4,11 @@ Bindings of ``demo_dropout``, ``demo_fp8_quantize``, ``demo_fp8_matmul`` and ``d
 (``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
 torch unless an ``out`` is given, the call runs on torch's current stream (or on ``stream``, as if it
 were the current one) and raises :class:`DemoError` on a negative status.
+
+The calls record nothing for autograd.  A tensor that requires a gradient is refused while gradients are
+recorded (a result without history would end the branch's training without a word): call them from a
+``torch.autograd.Function``, whose backward is the call that each docstring names, or under
+``torch.no_grad()``.
 """
 
 import functools
@@ -63,6 +68,9 @@ def _matrix(t, name, like=None, shape=None):
         raise TypeError(f"{name} must be a torch.Tensor") from None
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, and this call records none: detach it, or call under "
+                         "torch.no_grad() or from a torch.autograd.Function")
     if like is not None:
         if dt != like.dtype:
             raise TypeError(f"{name} has dtype {dt}, expected {like.dtype}")
@@ -247,7 +255,11 @@ def _result_dtype(out, dtype, default):
 
 def fp8_matmul(a, b, *, out=None, dtype=None, add=False, stream=None):
     """``a b^T`` of two Fp8Matrix ([m, k] and [n, k]) into ``out`` or a new tensor of ``dtype``
-    (bfloat16 by default), or added to the float32 ``out`` (demo_fp8_matmul)."""
+    (bfloat16 by default), or added to the float32 ``out`` (demo_fp8_matmul).
+
+    With ``dy`` the result's gradient, that of ``a`` is ``dy b`` and that of ``b`` is ``dy^T a``: products of
+    ``dy`` quantized by rows, or by columns, with ``b``, or ``a``, quantized by columns.
+    """
     if stream is not None:
         return _on_stream(stream, a.codes.device, fp8_matmul, a, b, out=out, dtype=dtype, add=add)
     (m, k), (n, kb) = a.shape, b.shape
@@ -274,7 +286,7 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     """``x w^T`` for ``x`` [..., k] in 16 or 32 bits and an Fp8Matrix ``w`` [n, k] (demo_fp8_linear):
     ``x`` is quantized by rows to e4m3 within the call.  The result has x's dtype unless ``dtype``
     or ``out`` says otherwise; ``workspace`` (uint8, only used beyond a few rows) is allocated
-    through torch where it is not given.
+    through torch where it is not given.  The gradients are those of :func:`fp8_matmul`.
     """
     if stream is not None:
         return _on_stream(stream, x.device, fp8_linear, x, w, out=out, dtype=dtype, workspace=workspace)

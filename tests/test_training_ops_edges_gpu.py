@@ -181,3 +181,44 @@ def test_matmul_ends_when_one_of_its_last_loads_never_completes(m, n, k, item):
     dm.fp8_matmul(a, b)
     assert dm.device_fault() == 1
     assert torch.equal(dm.fp8_matmul(a, b), want) and dm.device_fault() == 0
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """A result without history would end a branch's training without a word."""
+    x, r = normal(4, 128, 31).cuda(), normal(4, 128, 32).cuda()
+    g = normal(4, 128, 33).cuda().requires_grad_()
+    w = dm.fp8_quantize(normal(6, 128, 34).cuda())
+    out = torch.empty(4, 6, device="cuda", requires_grad=True)
+    calls = [lambda: dm.dropout(g, 0.1, seed=0, step=0), lambda: dm.dropout(x, 0.1, seed=0, step=0, residual=g),
+             lambda: dm.dropout(x, 0.1, seed=0, step=0, out=g), lambda: dm.fp8_quantize(g),
+             lambda: dm.fp8_quantize(x, gate=g), lambda: dm.fp8_linear(g, w), lambda: dm.fp8_linear(x, w, out=out),
+             lambda: dm.fp8_matmul(dm.fp8_quantize(x), w, out=out),
+             lambda: dm.dropout(g, 0.1, seed=0, step=0, stream=torch.cuda.current_stream())]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+        with torch.no_grad():
+            call()
+    assert torch.equal(dm.dropout(g.detach(), 0.1, seed=0, step=0, residual=r),
+                       dm.dropout(g.data, 0.1, seed=0, step=0, residual=r))
+
+
+class Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, step):
+        ctx.args = p, seed, step
+        return dm.dropout(x, p, seed=seed, step=step, residual=residual)
+
+    @staticmethod
+    def backward(ctx, dy):
+        p, seed, step = ctx.args
+        return dm.dropout(dy, p, seed=seed, step=step), dy, None, None, None
+
+
+def test_dropout_from_an_autograd_function():
+    x, r, w = (normal(9, 130, s).cuda() for s in (35, 36, 37))
+    x.requires_grad_(), r.requires_grad_()
+    (Dropout.apply(x, r, 0.3, 5, 6) * w).sum().backward()
+    keep = torch.from_numpy(ref.keep_mask(9, 130, 0.3, 5, 6, 0)).cuda()
+    want = torch.where(keep, w * ref.drop_scale(0.3), torch.zeros_like(w))
+    assert torch.allclose(x.grad, want, rtol=2.0 ** -23, atol=0) and torch.equal(r.grad, w)
