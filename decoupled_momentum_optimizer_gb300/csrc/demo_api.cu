@@ -24,6 +24,7 @@ struct DeviceState {
   std::atomic<bool> ready{false};  // set last by demo_init (release), read by every call (acquire)
   int sms = 0;
   unsigned int* fault = nullptr;
+  Clusters clusters = {};  // of the products' CTAs
   cudaEvent_t ev_enc[kMaxBlocks];  // block b encoded (compute stream)
   cudaEvent_t ev_xch[kMaxBlocks];  // block b exchanged (communication stream)
   // Held while one pipelined call enqueues its work: the event pool is shared, and a
@@ -520,7 +521,7 @@ namespace demo {
 int device_info(DeviceInfo* out) {
   DeviceState* st = nullptr;
   const int s = current_state(&st);
-  if (s == DEMO_OK) *out = DeviceInfo{st->sms, st->fault, g_encode};
+  if (s == DEMO_OK) *out = DeviceInfo{st->sms, st->fault, g_encode, &st->clusters};
   return s;
 }
 
@@ -576,8 +577,7 @@ int demo_init(int device) {
     return DEMO_ECUDA;
   if (prepare_step_kernels() != cudaSuccess || prepare_encode_kernels() != cudaSuccess ||
       prepare_decode_kernels() != cudaSuccess || prepare_dense_kernels() != cudaSuccess ||
-      prepare_matmul_kernels(sms) != cudaSuccess ||
-      prepare_linear_kernels() != cudaSuccess)
+      prepare_matmul_kernels(sms, &st.clusters) != cudaSuccess || prepare_linear_kernels() != cudaSuccess)
     return DEMO_ECUDA;
   void* fault = nullptr;
   if (cudaGetSymbolAddress(&fault, g_fault_word) != cudaSuccess) return DEMO_ECUDA;

@@ -241,7 +241,8 @@ int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const
   MatmulParams q;
   std::memset(&q, 0, sizeof(q));
   q.kb = static_cast<int>(up(k, kBlock) / kBlock);
-  const MatmulPlan plan = plan_matmul(m, n, q.kb);
+  const MatmulPlan plan = plan_matmul(*dev.clusters, m, n, q.kb);
+  if (plan.grid == 0) return DEMO_ECUDA;
   const int64_t size = elem_size(out_dtype);
   // a bulk store writes whole units of 16 bytes, past the end of a row that is not a multiple of them
   q.bulk_out = at(out, 16) && n * size % 16 == 0 && (m == 1 || ldo * size % 16 == 0);

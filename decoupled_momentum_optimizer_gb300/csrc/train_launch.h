@@ -7,12 +7,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "train_plan.h"
+
 namespace demo {
 
 enum { kF32 = 0, kBF16 = 1, kF16 = 2 };
 enum { kE4M3 = 0, kE5M2 = 1 };
 
-constexpr int kBlock = 128;  // elements that share a scale
 // Exponent of each format's largest finite code, 1.75 * 2^top (448 and 57344).
 __host__ __device__ constexpr int fmt_top(int fmt) { return fmt == kE4M3 ? 8 : 15; }
 
@@ -25,6 +26,7 @@ struct DeviceInfo {
   int sms;
   unsigned int* fault;
   EncodeTiledFn encode;
+  const Clusters* clusters;
 };
 int device_info(DeviceInfo* out);
 // Test hook of the bounded waits (demo_test_stall_next_launch): 1 + the load of the next launch's first
@@ -77,15 +79,8 @@ struct MatmulParams {
   unsigned int* fault;
 };
 
-// How a product runs: CTAs that share a tile's rows (1 or 2), the tile's width, the parts k is cut
-// into, the stages, the grid; and the tensor maps' boxes (rows of codes, blocks of scales).
-struct MatmulPlan {
-  int group, bn, split, stages, rows_a, rows_b, chain;
-  unsigned int grid;
-};
-MatmulPlan plan_matmul(long long m, long long n, int kb);
 cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st);
-cudaError_t prepare_matmul_kernels(int sms);
+cudaError_t prepare_matmul_kernels(int sms, Clusters* clusters);
 
 // out = Q(x) w^T for few rows of x, whose codes and scales fit in shared memory: see train_linear.cu.
 // One launch and no workspace: a call takes 10 to 13 us from Python, of 17 as quantize and product, at

@@ -19,8 +19,6 @@
 // be next: a block of a 256 x 224 tile is 448 cycles of tensor core and 30 KB for either CTA, and takes
 // about 600; half of b per CTA of a pair is what keeps that near the tensor cores' pace (one CTA per
 // 128 x 224 tile reads 44 KB a block).
-#include <algorithm>
-
 #include "train_common.cuh"
 #include "train_tensor.cuh"
 
@@ -28,8 +26,6 @@ namespace demo {
 
 namespace {
 
-constexpr int kBM = 128, kBN = 224;  // rows of a CTA's tile, most columns
-constexpr int kChain = 4;  // blocks of 128 that one half of tensor memory sums
 constexpr int kSumWarps = 8, kScaleWarps = 2;
 constexpr int kLoadWarp = kSumWarps + kScaleWarps, kMmaWarp = kLoadWarp + 1, kScaleLoadWarp = kLoadWarp + 2;
 // Whole groups of four warps, launched with 128 registers a thread: the summing ones take 192, the
@@ -45,8 +41,6 @@ constexpr int kScaleSlots = kScaleWarps;  // chains whose words are ready in sha
 static_assert(kChain == 4, "a word holds the scales of a chain");
 constexpr int kCols = kBN / 2;  // most columns of a summing warp
 constexpr int kOutBytes = 32 * kBN;  // a warp's rows on their way out, bn bytes each
-constexpr int kMaxSplit = 8;  // portable cluster size
-constexpr int kMaxStages = 8;
 
 // G CTAs (1, or a cluster of 2) share a tile: each loads its 128 rows of a and bn / G of b, and the
 // rest of the shared memory is stages.
@@ -54,7 +48,7 @@ template <int G>
 struct Shared {
   // Stages: a's rows, then b's, whole units of 1024 bytes (swizzle atoms).  A pair has five; single CTAs
   // have as many as fit (at most kMaxStages), with only the rows of a that exist.
-  static constexpr int kRingBytes = G == 1 ? 3 * (kBM + kBN) * kBlock : 5 * (kBM + kBN / 2) * kBlock;
+  static constexpr int kRingBytes = G == 1 ? kRingBytesSingle : kPairStages * (kBM + kBN / 2) * kBlock;
   uint8_t ring[kRingBytes];  // 1024-byte aligned
   uint8_t out[kSumWarps][kOutBytes];
   // Scale words: row 32 c + l of an operand at [l][c] of its 512-byte unit of 128 rows (a's, then
@@ -274,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   // results are not used), and b's.
   const int a_bytes = (G == 1 ? p.rows_a : kBM) * kBlock;
   const int stage_bytes = a_bytes + (G == 1 ? p.bn : kBN / 2) * kBlock;
-  const int stages = G == 1 ? p.stages : 5;
+  const int stages = G == 1 ? p.stages : kPairStages;
   Work work;
   work.tiles_m = static_cast<int>((p.m + G * kBM - 1) / (G * kBM));
   work.tiles_n = static_cast<int>((p.n + p.bn - 1) / p.bn);
@@ -558,76 +552,6 @@ struct MatmulLaunch {
   }
 };
 
-// Clusters of 1 .. kMaxSplit single CTAs, and pairs (entry 0), that the device runs at one time: a
-// cluster stays within a group of SMs, so these are fewer than the SMs divided by the size.  Filled
-// once, by the first device that is initialised (every device the library runs on is the same GPU).
-static int g_clusters[kMaxSplit + 1];
-
-// Few tiles (128 x 224 ones that would leave half of the SMs idle, or m that fills no pair): one CTA
-// per tile, with k cut into parts where that pays.  Otherwise pairs.  Either way the cheapest width
-// (and number of parts) in cycles.
-//
-// A pair: a block costs max(2 bn, 256 + bn) (the tensor cores, or what a CTA reads at 64 bytes a
-// cycle), a tile about 2500 more.
-//
-// A single CTA: a block costs what the CTA reads, the tensor core, or a stage's round trip of about
-// 2200 shared by the stages, whichever is longest (at 1400, 8 x 2048 x 8192 was cut into too few parts
-// and took 13.8 us of 9.1; at 3200, 200 x 2048 x 8192 took 13.7 of 12.2).  Joining parts costs about
-// 9000 and the reading of a tile of sums.  A tile that is not cut is staged, where eight rows' 16-byte
-// stores of bn bytes apart meet in the same banks, 8 ways at widths of whole 128s, 4 of 64s, 2 of 32s:
-// 2 bn cycles for each way (32 x 1024 x 128 at widths 64, 96 .. 224: 3.75, 3.80, 4.76, 4.11, 4.65,
-// 4.45 us).  Stores in another order for each row have no conflicts, but the exchange of registers
-// before them cost every width 0.6 to 1 us: it is code that runs once.
-MatmulPlan plan_matmul(long long m, long long n, int kb) {
-  const int sms = g_clusters[1];
-  const auto tiles = [&](int rows, int bn) { return ((m + rows - 1) / rows) * ((n + bn - 1) / bn); };
-  MatmulPlan plan;
-  plan.split = 1;
-  plan.group = m <= kBM || 2 * tiles(kBM, kBN) <= sms ? 1 : 2;
-  int rows_a = kBM;
-  const auto stages_of = [&](int bn) {
-    const int fit = Shared<1>::kRingBytes / ((rows_a + bn) * kBlock);
-    return fit < kMaxStages ? fit : kMaxStages;
-  };
-  double best = 0;
-  const auto offer = [&](int bn, int split, double cost, long long grid) {
-    if (best == 0 || cost < best) {
-      best = cost;
-      plan.bn = bn;
-      plan.split = split;
-      plan.grid = static_cast<unsigned>(grid);
-    }
-  };
-  if (plan.group == 1) {
-    const int chains = (kb + kChain - 1) / kChain;
-    const double rows = m < kBM ? m : kBM;
-    rows_a = m < kBM ? static_cast<int>(m + 7) / 8 * 8 : kBM;
-    for (int bn = kBN; bn >= 64; bn -= 32) {
-      const long long t = tiles(kBM, bn);
-      for (int split = 1; split <= kMaxSplit && (split == 1 || (split <= chains && t <= g_clusters[split])); ++split) {
-        const double rounds = static_cast<double>((t + g_clusters[split] - 1) / g_clusters[split]);
-        const double ways = bn % 128 == 0 ? 8 : bn % 64 == 0 ? 4 : 2;
-        const double end = split > 1 ? 10000 + rows * bn / 8 : 500 + 2 * bn * ways;
-        const int bytes = (rows_a + bn) * kBlock;
-        const double block = std::max({bytes / 64.0, 2.0 * bn, 2200.0 / stages_of(bn)});
-        offer(bn, split, rounds * (((kb + split - 1) / split) * block + end), t * split);
-      }
-    }
-  } else {
-    const long long pairs = g_clusters[0];
-    for (int bn = kBN; bn >= 96; bn -= 32) {
-      const long long t = tiles(2 * kBM, bn), rounds = (t + pairs - 1) / pairs;
-      offer(bn, 1, static_cast<double>(rounds) * (2500.0 + static_cast<double>(kb) * (256 + bn)),
-            2 * (t < pairs ? t : pairs));
-    }
-  }
-  plan.rows_a = rows_a;
-  plan.stages = plan.group == 1 ? stages_of(plan.bn) : 5;
-  plan.rows_b = plan.bn / plan.group;
-  plan.chain = kChain;
-  return plan;
-}
-
 cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStream_t st) {
   if (plan.group == 1) {
     MatmulLaunch<1> l(plan.grid, plan.split, st);
@@ -637,24 +561,29 @@ cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStr
   return cudaLaunchKernelEx(&l.cfg, matmul_kernel<2>, p);
 }
 
-cudaError_t prepare_matmul_kernels(int sms) {
+// A count of 0 where the device has no place for such a cluster (a part of one, with few SMs or none that
+// are together): plan_matmul goes without it, and whatever else the library does is not concerned.
+template <int G>
+static int clusters_of(int sms, int size) {
+  if (sms < size) return 0;
+  MatmulLaunch<G> l(static_cast<unsigned>(sms / size * size), size, nullptr);
+  l.cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, matmul_kernel<G>, &l.cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+cudaError_t prepare_matmul_kernels(int sms, Clusters* clusters) {
   cudaError_t e = cudaFuncSetAttribute(matmul_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmem<1>));
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(matmul_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem<2>));
-  if (e != cudaSuccess || g_clusters[0] != 0) return e;
-  for (int size = kMaxSplit; size >= 1; --size) {
-    MatmulLaunch<1> l(static_cast<unsigned>(sms / size * size), size, nullptr);
-    l.cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&g_clusters[size], matmul_kernel<1>, &l.cfg)) != cudaSuccess) return e;
-    if (g_clusters[size] < 1) return cudaErrorInvalidConfiguration;
-  }
-  MatmulLaunch<2> l(static_cast<unsigned>(sms / 2 * 2), 2, nullptr);
-  l.cfg.numAttrs = 1;
-  int pairs = 0;
-  if ((e = cudaOccupancyMaxActiveClusters(&pairs, matmul_kernel<2>, &l.cfg)) != cudaSuccess) return e;
-  if (pairs < 1) return cudaErrorInvalidConfiguration;
-  g_clusters[0] = pairs;
+  if (e != cudaSuccess) return e;
+  for (int size = 1; size <= kMaxSplit; ++size) clusters->of[size] = clusters_of<1>(sms, size);
+  clusters->of[0] = clusters_of<2>(sms, 2);
   return cudaSuccess;
 }
 
