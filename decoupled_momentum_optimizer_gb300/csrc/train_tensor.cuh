@@ -109,9 +109,11 @@ __device__ __forceinline__ void tensor_copy_scales(uint32_t taddr, uint32_t sadd
 // (`bar` is this CTA's own, at the same offset).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
   asm volatile(
+      "{\n\t.reg .b32 even;\n\t"
+      "mapa.shared::cluster.u32 even, %2, 0;\n\t"
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar) & 0xfeffffffu), "r"(x), "r"(y)
+      " [%0], [%1, {%3, %4}], [even];\n\t}" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y)
       : "memory");
 }
 
