@@ -83,10 +83,17 @@ cudaError_t launch_matmul(const MatmulParams& p, const MatmulPlan& plan, cudaStr
 cudaError_t prepare_matmul_kernels(int sms, Clusters* clusters);
 
 // out = Q(x) w^T for few rows of x, whose codes and scales fit in shared memory: see train_linear.cu.
-// One launch and no workspace: a call takes 10 to 13 us from Python, of 17 as quantize and product, at
-// every size measured up to 40 rows.  On the device alone it is the faster one up to 16 rows (1000 x 768
-// 3.4 us of 6.7, 8192 x 2048 9.5 of 9.1), and at 24 to 40 where w is small (1000 x 768 5.3 .. 6.3 of 6.8;
-// 24 x 8192 x 2048 12.7 of 9.1).
+// One launch and no workspace: from Python a call takes 12 to 13 us, where quantize and product take 18 to 19,
+// as long as the device is not the longer of the two.  On the device, of the two kernels' time (us):
+//   rows           1            8            16           24           40
+//   1000 x 768     2.9 of 6.5   3.0 of 6.7   3.5 of 6.7   5.4 of 6.7   6.4 of 6.6
+//   4096 x 1024    3.2 of 6.6   3.4 of 6.8   4.2 of 6.9   6.3 of 7.0   8.5 of 6.8
+//   8192 x 2048    6.0 of 8.8   7.0 of 9.0   9.4 of 9.1   13.2 of 9.0
+//   4096 x 4096    6.3 of 11.2  8.4 of 11.3  12.4 of 11.3
+//   512 x 8192     6.4 of 8.2   11.2 of 8.5
+//   32128 x 768    9.2 of 10.1  9.8 of 10.3  12.1 of 10.4  17.9 of 10.4  22.0 of 10.5
+// So the limit is right for calls and small w; with many rows and a large w (and in a captured graph from 8
+// to 16 rows on) the two kernels would be faster, up to twice at 40 x 32128 x 768.
 constexpr int kLinearRows = 40, kLinearSmem = 90 * 1024;
 // Its sums (1024 bytes a row), codes and scales.
 constexpr long long linear_bytes(long long m, long long blocks) { return m * (1024 + blocks * (kBlock + 4)); }

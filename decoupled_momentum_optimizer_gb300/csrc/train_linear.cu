@@ -12,8 +12,8 @@
 //
 // The block's 128 products accumulate in the instruction's float32, blocks in IEEE float32.
 //
-// Measured on the device with weights larger than L2 in turn: 8192 x 8192, one token 14.5 us (4.8 TB/s),
-// 8192 x 2048 6.0 us, eight tokens 7.0 us; about 2.2 us of each is the launch.  Plain loads of w instead of
+// Measured on the device with weights larger than L2 in turn: 8192 x 8192, one token 14.7 us (4.7 TB/s),
+// 8192 x 2048 5.9 us, eight tokens 6.9 us; about 2.2 us of each is the launch.  Plain loads of w instead of
 // TMA stages left HBM idle (10.1 us for 8192 x 2048), and quantizing x in every CTA of a larger grid cost
 // up to 18 us more for eight tokens.
 #include "train_common.cuh"

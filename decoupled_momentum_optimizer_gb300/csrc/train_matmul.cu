@@ -14,9 +14,11 @@
 // 8192 took 170 us, and 250 us with a scale per row of b.)  224 columns leave room in tensor memory for
 // two halves and their scales.
 //
-// What bounds it: power.  8192 x 8192 x 2048 takes 91 us (3.0 PFLOP/s) in the first milliseconds and 103
-// over a second, at 1.37 kW with the SM clock down to 1.67 GHz.  At full clock the stages' arrival would
-// be next: a block of a 256 x 224 tile is 448 cycles of tensor core and 30 KB for either CTA, and takes
+// What bounds it: power, at n = 8192.  8192 x 8192 x 2048 takes 102 us (2.7 PFLOP/s) over a second, at 1.37 kW
+// with the SM clock down to 1.67 GHz, and 91 in the first milliseconds.  At n = 2048 the layout takes a share
+// as well: 8192 x 2048 x 8192 takes 105 to 110 us (2.5 to 2.6 PFLOP/s) at 1.8 GHz and 98 at first; its 352
+// tiles of 256 x 192 on 76 pairs are 4.6 rounds run as 5, over 2112 columns for 2048, 90% useful work where
+// n = 8192 has 96%.  At full clock the stages' arrival would be next: a block of a 256 x 224 tile is 448 cycles of tensor core and 30 KB for either CTA, and takes
 // about 600; half of b per CTA of a pair is what keeps that near the tensor cores' pace (one CTA per
 // 128 x 224 tile reads 44 KB a block).
 #include "train_common.cuh"

@@ -22,8 +22,9 @@
 //
 // Measured, both forms: 8192 x 2048 float32 tiles 16 us (6.2 TB/s, HBM's rate); 8192 x 8192 bfloat16 55 us
 // (4.8 TB/s; 62 with bounds checked in whole tiles too), with relu and dropout 82 us (68 without the
-// hash): there the integer and compare pipe, 65% busy with 17 of 32 instructions an element, sets the
-// pace.
+// hash).  Nothing is saturated there: the integer and compare pipe is 65% busy (17 of 32 instructions an
+// element), issue slots 61%, HBM 33%; a tile is loaded, computed and stored in turn, and only the SM's
+// other CTA overlaps that.
 #include "train_common.cuh"
 
 namespace demo {

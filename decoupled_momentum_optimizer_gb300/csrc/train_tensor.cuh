@@ -117,7 +117,8 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// A float32 tile in shared memory added to global memory (one addition per element, in L2).
+// A float32 tile in shared memory added to global memory (one addition per element, in L2, which keeps
+// subnormal values).
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int x, int y) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),

@@ -316,7 +316,7 @@ int demo_adamw_step(float* theta, int64_t n, float beta1, float beta2, float eps
  *
  * Dropout, matrices in 8-bit floating point with a scale for each block of 128, and their
  * products.  They follow the conventions above (device pointers, streams, statuses, no allocation
- * in the calls, graph capture, no floating-point atomics) except that
+ * in the calls, graph capture, results that are the same to the bit from call to call) except that
  *   - a matrix argument has a row stride `ld` in elements and needs only its element's alignment
  *     (whole 16-byte rows are faster); rows of an input may overlap or repeat (ld < cols, 0
  *     included), rows of an output may not (DEMO_EINVAL);
@@ -381,6 +381,8 @@ int demo_fp8_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64
  * demo_fp8_matmul -- out = A B^T (out += A B^T if add, float32 only): A [m, k] and B [n, k]
  * quantized by rows.
  *   out       [m, n] of out_dtype, apart from every input
+ *   add       one float32 addition per element and call, subnormal values kept (whole 16-byte units by
+ *             a reduction in the L2 cache, which no other addition competes with)
  * Sums over 512 of k run in the tensor core's float32 accumulator, longer ones in IEEE float32.  NaN
  * codes, and scales that are no power of two, give NaN results.  k = 0 gives zeros (or leaves out as it
  * is, if add).
