@@ -130,6 +130,15 @@ int check_quantized(const void* codes, const float* scales, int fmt) {
 int64_t code_bytes(int64_t rows, int64_t k) { return rows * up(k, kBlock); }
 int64_t scale_bytes(int64_t rows, int64_t k) { return up(k, kBlock) / kBlock * up(rows, 4) * 4; }
 
+int check_norm(int dtype, int weight_dtype, int64_t rows, int64_t cols) {
+  if (!valid_dtype(dtype) || (weight_dtype != DEMO_F32 && weight_dtype != dtype)) return DEMO_EINVAL;
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kNormCols) return DEMO_EINVAL;
+  return cols > 0 && up(rows, kBlock) > kMaxElems / up(cols, kBlock) ? DEMO_EINVAL : DEMO_OK;
+}
+
+// One row has no stride (whatever is given must not decide how it is read).
+int64_t row_stride(int64_t rows, int64_t ld) { return rows == 1 ? 0 : ld; }
+
 }  // namespace
 
 extern "C" {
@@ -215,6 +224,154 @@ int demo_fp8_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64
   q.codes_cols = codes_cols;
   q.scales_cols = scales_cols;
   return to_status(launch_quantize(q, dtype, fmt, static_cast<cudaStream_t>(stream)));
+}
+
+int demo_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype, const void* weight,
+                  int weight_dtype, int64_t rows, int64_t cols, double eps, void* total, int64_t ldt, void* out,
+                  int64_t ldo, float* rstd, int fmt, void* codes_rows, float* scales_rows, void* codes_cols,
+                  float* scales_cols, void* stream) {
+  int s = check_norm(dtype, weight_dtype, rows, cols);
+  if (s != DEMO_OK) return s;
+  if (!valid_fmt(fmt) || !(eps > 0.0) || !std::isfinite(eps)) return DEMO_EINVAL;
+  if ((codes_rows == nullptr) != (scales_rows == nullptr) || (codes_cols == nullptr) != (scales_cols == nullptr))
+    return DEMO_EINVAL;
+  if (residual == nullptr && total != nullptr) return DEMO_EINVAL;
+  if (codes_cols != nullptr && (rstd == nullptr || (residual != nullptr && total == nullptr))) return DEMO_EINVAL;
+  if (rows == 0 || cols == 0) return DEMO_OK;
+  if (total == nullptr && out == nullptr && rstd == nullptr && codes_rows == nullptr && codes_cols == nullptr)
+    return DEMO_EINVAL;
+  if ((s = check_matrix(x, rows, cols, ldx, dtype, false)) != DEMO_OK) return s;
+  if ((s = check_matrix(weight, 1, cols, cols, weight_dtype, false)) != DEMO_OK) return s;
+  if (residual != nullptr && (s = check_matrix(residual, rows, cols, ldr, dtype, false)) != DEMO_OK) return s;
+  if (total != nullptr && (s = check_matrix(total, rows, cols, ldt, dtype, true)) != DEMO_OK) return s;
+  if (out != nullptr && (s = check_matrix(out, rows, cols, ldo, dtype, true)) != DEMO_OK) return s;
+  if (rstd != nullptr && !at(rstd, 4)) return DEMO_EALIGN;
+  if (codes_rows != nullptr && (s = check_quantized(codes_rows, scales_rows, fmt)) != DEMO_OK) return s;
+  if (codes_cols != nullptr && (s = check_quantized(codes_cols, scales_cols, fmt)) != DEMO_OK) return s;
+  const int64_t size = elem_size(dtype);
+  const Region rx = matrix(x, rows, cols, ldx, size), rr = matrix(residual, rows, cols, ldr, size),
+               rw = flat(weight, cols * elem_size(weight_dtype)), rt = matrix(total, rows, cols, ldt, size),
+               ro = matrix(out, rows, cols, ldo, size);
+  // The sum, and the result of the fused kernel, may take an input's place; the column form reads x again.
+  for (const Region& in : {rx, rr}) {
+    if (!same(in, rt) && overlap(in, rt)) return DEMO_EINVAL;
+    if ((codes_cols != nullptr || !same(in, ro)) && overlap(in, ro)) return DEMO_EINVAL;
+  }
+  const Region made[7] = {rt, ro, flat(rstd, 4 * rows), flat(codes_rows, code_bytes(rows, cols)),
+                          flat(scales_rows, scale_bytes(rows, cols)), flat(codes_cols, code_bytes(cols, rows)),
+                          flat(scales_cols, scale_bytes(cols, rows))};
+  for (int i = 0; i < 7; ++i) {
+    if (overlap(made[i], rw) || (i >= 2 && (overlap(made[i], rx) || overlap(made[i], rr)))) return DEMO_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(made[i], made[j])) return DEMO_EINVAL;
+  }
+  DeviceInfo dev;
+  if ((s = device_info(&dev)) != DEMO_OK) return s;
+  NormParams q;
+  std::memset(&q, 0, sizeof(q));
+  q.x = x;
+  q.residual = residual;
+  q.weight = weight;
+  q.total = total;
+  q.out = out;
+  q.rstd = rstd;
+  q.codes = codes_cols == nullptr ? codes_rows : nullptr;
+  q.scales = scales_rows;
+  q.rows = rows;
+  q.cols = cols;
+  q.ldx = row_stride(rows, ldx);
+  q.ldr = row_stride(rows, ldr);
+  q.ldt = row_stride(rows, ldt);
+  q.ldo = row_stride(rows, ldo);
+  q.col_blocks = static_cast<unsigned int>(up(cols, kBlock) / kBlock);
+  q.fmt = fmt;
+  q.inv = 1.0 / static_cast<double>(cols);
+  q.eps = eps;
+  q.inv_hi = static_cast<float>(q.inv);
+  q.inv_lo = static_cast<float>(q.inv - static_cast<double>(q.inv_hi));
+  q.eps_hi = static_cast<float>(eps);
+  q.eps_lo = static_cast<float>(eps - static_cast<double>(q.eps_hi));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = to_status(launch_norm(q, dtype, weight_dtype, dev.sms, st))) != DEMO_OK || codes_cols == nullptr) return s;
+  QuantParams c;
+  std::memset(&c, 0, sizeof(c));
+  c.x = residual != nullptr ? total : x;
+  c.ldx = residual != nullptr ? q.ldt : q.ldx;
+  c.rows = rows;
+  c.cols = cols;
+  c.row_blocks = static_cast<unsigned int>(up(rows, kBlock) / kBlock);
+  c.col_blocks = q.col_blocks;
+  c.codes_rows = codes_rows;
+  c.scales_rows = scales_rows;
+  c.codes_cols = codes_cols;
+  c.scales_cols = scales_cols;
+  c.rstd = rstd;
+  c.weight = weight;
+  c.weight_dtype = weight_dtype;
+  return to_status(launch_quantize(c, dtype, fmt, st));
+}
+
+size_t demo_rms_norm_grad_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 1 || cols <= 0 || cols > kNormCols) return 0;
+  return static_cast<size_t>((rows < kNormParts ? rows : kNormParts) * cols * 4);
+}
+
+int demo_rms_norm_grad(const void* dy, int64_t lddy, const void* total, int64_t ldt, int dtype, const void* weight,
+                       int weight_dtype, const float* rstd, int64_t rows, int64_t cols, const void* past, int64_t ldp,
+                       void* dx, int64_t lddx, float* dweight, int add, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  int s = check_norm(dtype, weight_dtype, rows, cols);
+  if (s != DEMO_OK) return s;
+  if (add < 0 || add > 1) return DEMO_EINVAL;
+  if (cols == 0) return DEMO_OK;
+  if (dweight != nullptr && !at(dweight, 4)) return DEMO_EALIGN;
+  if (rows > 0) {
+    if ((s = check_matrix(dy, rows, cols, lddy, dtype, false)) != DEMO_OK) return s;
+    if ((s = check_matrix(total, rows, cols, ldt, dtype, false)) != DEMO_OK) return s;
+    if ((s = check_matrix(weight, 1, cols, cols, weight_dtype, false)) != DEMO_OK) return s;
+    if (past != nullptr && (s = check_matrix(past, rows, cols, ldp, dtype, false)) != DEMO_OK) return s;
+    if ((s = check_matrix(dx, rows, cols, lddx, dtype, true)) != DEMO_OK) return s;
+    if (rstd == nullptr) return DEMO_EINVAL;
+    if (!at(rstd, 4)) return DEMO_EALIGN;
+    const size_t need = dweight != nullptr ? demo_rms_norm_grad_workspace(rows, cols) : 0;
+    if (workspace_bytes < need) return DEMO_ENOSPACE;
+    if (need > 0 && workspace == nullptr) return DEMO_EINVAL;
+    if (need > 0 && !at(workspace, 16)) return DEMO_EALIGN;
+    const int64_t size = elem_size(dtype);
+    const Region rdx = matrix(dx, rows, cols, lddx, size), rdw = flat(dweight, 4 * cols),
+                 rwork = flat(need > 0 ? workspace : nullptr, static_cast<int64_t>(need));
+    for (const Region& in : {matrix(dy, rows, cols, lddy, size), matrix(total, rows, cols, ldt, size),
+                             matrix(past, rows, cols, ldp, size)}) {
+      if (!same(in, rdx) && overlap(in, rdx)) return DEMO_EINVAL;
+      if (overlap(in, rdw) || overlap(in, rwork)) return DEMO_EINVAL;
+    }
+    for (const Region& in : {flat(weight, cols * elem_size(weight_dtype)), flat(rstd, 4 * rows)})
+      if (overlap(in, rdx) || overlap(in, rdw) || overlap(in, rwork)) return DEMO_EINVAL;
+    if (overlap(rdx, rdw) || overlap(rdx, rwork) || overlap(rdw, rwork)) return DEMO_EINVAL;
+  } else if (dweight == nullptr || add) {
+    return DEMO_OK;  // a sum over nothing, added
+  }
+  DeviceInfo dev;
+  if ((s = device_info(&dev)) != DEMO_OK) return s;
+  NormGradParams q;
+  std::memset(&q, 0, sizeof(q));
+  q.dy = dy;
+  q.total = total;
+  q.weight = weight;
+  q.rstd = rstd;
+  q.past = past;
+  q.dx = dx;
+  q.dw = dweight;
+  q.partials = static_cast<float*>(workspace);
+  q.rows = rows;
+  q.cols = cols;
+  q.lddy = row_stride(rows, lddy);
+  q.ldt = row_stride(rows, ldt);
+  q.ldp = row_stride(rows, ldp);
+  q.lddx = row_stride(rows, lddx);
+  q.add = add;
+  q.inv = static_cast<float>(1.0 / static_cast<double>(cols));
+  return to_status(launch_norm_grad(q, dtype, weight_dtype, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,

@@ -1,5 +1,5 @@
 // Parameter blocks and launchers of the training operators' kernels (dropout, block-scaled 8-bit
-// quantization, products of quantized matrices), and what their C entry points need of the
+// quantization, products of quantized matrices, norms), and what their C entry points need of the
 // library's per-device state.
 #pragma once
 
@@ -60,9 +60,47 @@ struct QuantParams {
   float* scales_rows;  // [column blocks][rows up to 4]
   void* codes_cols;    // [cols][rows up to 128], may be NULL
   float* scales_cols;  // [row blocks][cols up to 4]
+  const float* rstd;   // NULL, or x is (x rstd[row]) weight[column] first (see train_norm.cu)
+  const void* weight;
+  int weight_dtype;
 };
 
 cudaError_t launch_quantize(const QuantParams& p, int dtype, int fmt, cudaStream_t st);
+
+// Root-mean-square norm of rows (see train_norm.cu).  inv = 1 / cols; it and eps also as pairs of floats.
+constexpr long long kNormCols = 32768;  // 32 warps of 32 elements a lane
+struct NormParams {
+  const void* x;
+  const void* residual;  // may be NULL
+  const void* weight;
+  void* total;  // x + residual, may be NULL
+  void* out;    // may be NULL
+  float* rstd;  // may be NULL
+  void* codes;  // by rows, may be NULL
+  float* scales;
+  long long rows, cols, ldx, ldr, ldt, ldo;
+  unsigned int col_blocks;
+  int fmt, warps;  // warps of a row: set by the launcher
+  float inv_hi, inv_lo, eps_hi, eps_lo;
+  double inv, eps;
+};
+cudaError_t launch_norm(NormParams& p, int dtype, int weight_dtype, int sms, cudaStream_t st);
+
+constexpr int kNormParts = 256;  // most CTAs of the gradient's kernel, whose sums over rows a second one joins
+struct NormGradParams {
+  const void* dy;
+  const void* total;
+  const void* weight;
+  const float* rstd;
+  const void* past;  // may be NULL
+  void* dx;
+  float* dw;        // may be NULL
+  float* partials;  // [CTAs][cols], unused with one CTA
+  long long rows, cols, lddy, ldt, ldp, lddx;
+  int add, warps;
+  float inv;
+};
+cudaError_t launch_norm_grad(NormGradParams& p, int dtype, int weight_dtype, int sms, cudaStream_t st);
 
 // out = a b^T (+ out): a [m][k], b [n][k] quantized by rows.
 struct MatmulParams {

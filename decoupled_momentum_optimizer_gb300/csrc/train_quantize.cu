@@ -1,7 +1,7 @@
 // Quantization of a matrix to 8-bit floating point with one power-of-two scale for each block of
 // 128, by rows, by columns (the codes of the transpose) or both from one read of the matrix:
 //
-//   v[r][c]  = x[r][c], then relu, dropout and a gate if asked
+//   v[r][c]  = x[r][c], then relu, dropout and a gate if asked (or (x[r][c] rstd[r]) w[c], a norm's result)
 //   s        = the smallest power of two >= 2^-126 with max |v| over the block <= s * largest code
 //   code     = v / s rounded to nearest even      (division by a power of two is exact)
 //
@@ -62,7 +62,7 @@ __device__ __forceinline__ void load4(const T* p, int live, float (&v)[4]) {
   }
 }
 
-template <typename T, int FMT, bool VEC, bool GATE>
+template <typename T, int FMT, bool VEC, bool GATE, bool NORM>
 __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid_constant__ QuantParams p) {
   __shared__ QuantShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -99,6 +99,20 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[i][e] = h[e] > 0.0f ? v[i][e] : 0.0f;
       }
+    }
+  }
+  if constexpr (NORM) {  // the products of the fused norm, in its order: the same codes to the bit
+    float w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = e >= live_cols                ? 0.0f
+             : p.weight_dtype == kF32 ? static_cast<const float*>(p.weight)[c0 + e]
+                                          : to_f32(static_cast<const T*>(p.weight)[c0 + e]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float r = i < live_rows ? p.rstd[r0 + i] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = i < live_rows && e < live_cols ? v[i][e] * r * w[e] : 0.0f;
     }
   }
   if (p.relu) {
@@ -235,8 +249,9 @@ static cudaError_t launch_quantize_t(const QuantParams& p, cudaStream_t st) {
   // Accesses of four elements where every row's groups of four are aligned and whole.
   const bool vec = p.cols % 4 == 0 && p.ldx % 4 == 0 && at(p.x) &&
                    (p.gate == nullptr || (p.ldg % 4 == 0 && at(p.gate)));
-  auto* kernel = p.gate != nullptr ? (vec ? quantize_kernel<T, FMT, true, true> : quantize_kernel<T, FMT, false, true>)
-                                   : (vec ? quantize_kernel<T, FMT, true, false> : quantize_kernel<T, FMT, false, false>);
+  auto* kernel = p.rstd != nullptr   ? (vec ? quantize_kernel<T, FMT, true, false, true> : quantize_kernel<T, FMT, false, false, true>)
+                 : p.gate != nullptr ? (vec ? quantize_kernel<T, FMT, true, true, false> : quantize_kernel<T, FMT, false, true, false>)
+                                     : (vec ? quantize_kernel<T, FMT, true, false, false> : quantize_kernel<T, FMT, false, false, false>);
   return launch_overlapped(kernel, grid, kQuantThreads, 0, st, p);
 }
 

@@ -1,7 +1,7 @@
-"""Training operators beside the shard step: dropout, 8-bit quantization and its products.
+"""Training operators beside the shard step: dropout, norms, 8-bit quantization and its products.
 
-Bindings of ``demo_dropout``, ``demo_fp8_quantize``, ``demo_fp8_matmul`` and ``demo_fp8_linear``
-(``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
+Bindings of ``demo_dropout``, ``demo_fp8_quantize``, ``demo_fp8_matmul``, ``demo_fp8_linear``, ``demo_rms_norm`` and
+``demo_rms_norm_grad`` (``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
 torch unless an ``out`` is given, the call runs on torch's current stream (or on ``stream``, as if it
 were the current one) and raises :class:`DemoError` on a negative status.
 
@@ -11,6 +11,7 @@ recorded (a result without history would end the branch's training without a wor
 ``torch.no_grad()``.
 """
 
+import collections
 import functools
 
 import torch
@@ -312,3 +313,153 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     _run("demo_fp8_linear", (xp, ldx, _DTYPES[x.dtype], wc.data_ptr(), w.scales.data_ptr(), _FMT_OF[wc.dtype], m, n, k,
                              op, ldo, odt, wp, need), index)
     return out
+
+
+Normed = collections.namedtuple("Normed", ("out", "quantized", "total", "rstd"))
+
+
+def _flat_rows(t):
+    """Rows of a tensor seen as rows of its last dimension (also where that has no elements)."""
+    return t.shape[:-1].numel()
+
+
+def _weight(weight, x, cols):
+    """(pointer, dtype's code) of a norm's weight: [cols], contiguous, float32 or x's type."""
+    if weight.dtype != torch.float32 and weight.dtype != x.dtype:
+        raise TypeError(f"weight has dtype {weight.dtype}, expected float32 or {x.dtype}")
+    if weight.get_device() != x.get_device():
+        raise ValueError(f"weight is on {weight.device}, x on {x.device}")
+    return _matrix(weight, "weight", None, (cols,))[0], _DTYPES[weight.dtype]
+
+
+def _row_values(t, name, rows, beside):
+    """Pointer of a contiguous float32 tensor with one element a row."""
+    if t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} elements")
+    if t.get_device() != beside.get_device():
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {beside.device}")
+    return t.data_ptr()
+
+
+def _workspace(workspace, need, beside):
+    """(tensor, pointer, bytes) of a call's workspace: the given one, or a new one where it needs any."""
+    if not need:
+        return None, None, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=beside.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != beside.get_device():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {beside.device}")
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def rms_norm(x, weight, *, eps=1e-6, residual=None, values=True, form=None, fmt="e4m3", save=False, out=None, total=None,
+             rstd=None, quantized=None, stream=None):
+    """Root-mean-square norm of the last dimension with the residual's addition before it (demo_rms_norm):
+    ``total = x + residual`` and ``out = total / sqrt(mean(total^2) + eps) * weight``.
+
+    ``weight``  [cols], float32 (a slice of the flat shard) or x's type
+    ``values``  whether ``out``, in x's type, is written
+    ``form``    None, or "rows", "cols", "both": the result as an :class:`Fp8Matrix` (or the pair), of the
+                values before their rounding to x's type, as :func:`fp8_quantize` makes them (2-D x)
+    ``save``    whether the rows' factors ``rstd``, which :func:`rms_norm_grad` takes, are returned
+    ``out``, ``total``, ``rstd``, ``quantized``   where the results go; new tensors otherwise.  ``total`` and
+                ``out`` may be ``x`` or ``residual`` themselves (``out`` not with "cols" or "both")
+
+    Returns ``Normed(out, quantized, total, rstd)``: ``total`` is ``x`` without a residual, what was not asked
+    for is None.
+    """
+    if stream is not None:
+        return _on_stream(stream, x.device, rms_norm, x, weight, eps=eps, residual=residual, values=values, form=form, fmt=fmt,
+                          save=save, out=out, total=total, rstd=rstd, quantized=quantized)
+    if fmt not in FP8_FORMATS:
+        raise ValueError(f"fmt is {fmt!r}, expected one of {tuple(FP8_FORMATS)}")
+    xp, ldx, rows, cols = _matrix(x, "x")
+    wp, wdt = _weight(weight, x, cols)
+    rp, ldr, tp, ldt = None, 0, None, 0
+    if residual is not None:
+        rp, ldr = _matrix(residual, "residual", x)[:2]
+        if total is None:
+            total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            tp, ldt = total.data_ptr(), cols
+        else:
+            tp, ldt = _matrix(total, "total", x)[:2]
+    elif total is not None:
+        raise ValueError("total is for a residual's sum")
+    op, ldo = None, 0
+    if out is not None:
+        op, ldo = _matrix(out, "out", x)[:2]
+    elif values:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        op, ldo = out.data_ptr(), cols
+    by_rows = by_cols = cr = sr = cc = sc = None
+    if form is not None:
+        if x.dim() != 2:
+            raise ValueError(f"x has {x.dim()} dimensions, expected 2 for the 8-bit forms")
+        if form == "both":
+            by_rows, by_cols = quantized if quantized is not None else (None, None)
+        elif form == "rows":
+            by_rows = quantized
+        elif form == "cols":
+            by_cols = quantized
+        else:
+            raise ValueError(f"form is {form!r}, expected rows, cols or both")
+        if form != "cols":
+            by_rows = _form(by_rows, rows, cols, fmt, False, x)
+            cr, sr = by_rows.codes.data_ptr(), by_rows.scales.data_ptr()
+        if form != "rows":
+            by_cols = _form(by_cols, cols, rows, fmt, False, x)
+            cc, sc = by_cols.codes.data_ptr(), by_cols.scales.data_ptr()
+    elif quantized is not None:
+        raise ValueError("quantized needs a form")
+    factors = rstd
+    if rstd is None and (save or by_cols is not None):
+        factors = torch.empty(_flat_rows(x), dtype=torch.float32, device=x.device)
+    sp = _row_values(factors, "rstd", _flat_rows(x), x) if factors is not None else None
+    _run("demo_rms_norm", (xp, ldx, rp, ldr, _DTYPES[x.dtype], wp, wdt, rows, cols, eps, tp, ldt, op, ldo, sp,
+                           FP8_FORMATS[fmt][0], cr, sr, cc, sc), x.get_device())
+    return Normed(out, (by_rows, by_cols) if form == "both" else by_cols if by_rows is None else by_rows,
+                  x if residual is None else total, factors if save or rstd is not None else None)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(rows, cols):
+    return _lib.demo_rms_norm_grad_workspace(rows, cols)
+
+
+def rms_norm_grad(dy, total, weight, rstd, *, past=None, out=None, dweight=None, add=False, weight_grad=True,
+                  workspace=None, stream=None):
+    """The gradients of :func:`rms_norm` (demo_rms_norm_grad): ``(dx, dweight)``.
+
+    ``dy`` is the result's gradient (for an 8-bit result, that of the values its codes stand for),
+    ``total`` and ``rstd`` are what the forward call returned; ``past`` is the gradient that reaches ``total``
+    by other ways, added to ``dx``.  ``dx`` is the gradient of both ``x`` and ``residual``; ``out`` receives it
+    and may be ``dy``, ``total`` or ``past`` themselves.  ``dweight`` is float32 [cols], written or (``add``)
+    added to; with ``weight_grad=False`` it is left out and None.
+    """
+    if stream is not None:
+        return _on_stream(stream, dy.device, rms_norm_grad, dy, total, weight, rstd, past=past, out=out, dweight=dweight,
+                          add=add, weight_grad=weight_grad, workspace=workspace)
+    dp, ldd, rows, cols = _matrix(dy, "dy")
+    tp, ldt = _matrix(total, "total", dy)[:2]
+    wp, wdt = _weight(weight, dy, cols)
+    sp = _row_values(rstd, "rstd", _flat_rows(dy), dy)
+    pp, ldp = _matrix(past, "past", dy)[:2] if past is not None else (None, 0)
+    if out is None:
+        out = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+        op, ldo = out.data_ptr(), cols
+    else:
+        op, ldo = _matrix(out, "out", dy)[:2]
+    gp = work = wsp = None
+    need = 0
+    if weight_grad:
+        if dweight is None:
+            if add:
+                raise ValueError("add needs a dweight to add to")
+            dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        gp = _row_values(dweight, "dweight", cols, dy)
+        work, wsp, need = _workspace(workspace, _norm_workspace(rows, cols), dy)
+    elif dweight is not None:
+        raise ValueError("dweight is given, and weight_grad is False")
+    _run("demo_rms_norm_grad", (dp, ldd, tp, ldt, _DTYPES[dy.dtype], wp, wdt, sp, rows, cols, pp, ldp, op, ldo, gp, bool(add),
+                                wsp, need), dy.get_device())
+    return out, dweight

@@ -405,6 +405,49 @@ int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, 
                     int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * demo_rms_norm -- root-mean-square norm of each row, with the residual's addition before it, into 16 or
+ * 32 bits and / or a quantized matrix.  For each row of x [rows, cols]:
+ *   s    = x + residual in float32, rounded to dtype (x itself without a residual)
+ *   r    = 1 / sqrt(mean(s^2) + eps), the float32 nearest to it (to about 2^-40 before that rounding)
+ *   v    = (s r) w, two float32 products;  out = v rounded to dtype;  codes and scales = those that
+ *          demo_fp8_quantize makes of v (rows scales)
+ *   weight      [cols] of weight_dtype: DEMO_F32 or dtype
+ *   eps         positive and finite
+ *   total       [rows, cols], receives s; NULL without a residual, may be NULL with one
+ *   out         [rows, cols] of dtype, or NULL
+ *   rstd        float32 [rows], receives r, or NULL
+ *   codes_rows, scales_rows / codes_cols, scales_cols   quantized matrices of v and of v transposed, in
+ *               fmt; a pair may be NULL.  The column form needs rstd, and total where there is a residual
+ * At least one result is asked for.  total may be x or residual itself (same stride), out too where no
+ * column form is asked for; otherwise results overlap neither each other nor an input (DEMO_EINVAL).
+ * cols is at most 32768.  A row with an infinity has r = 0, one with a NaN r = NaN; what is not finite in
+ * v becomes a NaN code.
+ */
+int demo_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype, const void* weight,
+                  int weight_dtype, int64_t rows, int64_t cols, double eps, void* total, int64_t ldt, void* out,
+                  int64_t ldo, float* rstd, int fmt, void* codes_rows, float* scales_rows, void* codes_cols,
+                  float* scales_cols, void* stream);
+
+/*
+ * demo_rms_norm_grad -- the gradients of demo_rms_norm.  With dy the gradient of v, xh = s rstd and
+ * c = mean(dy w xh) over the row:
+ *   dx      = rstd (dy w - xh c) + past, rounded once: the gradient of x and of the residual
+ *   dweight = the sum over the rows of dy xh (added to what it holds if add)
+ *   total, rstd   s and r of the forward call;  past [rows, cols] is what reaches s by other ways, or NULL
+ *   dx            [rows, cols] of dtype; may be dy, total or past itself (same stride)
+ *   dweight       float32 [cols], or NULL; 0 without rows (left as it is, if add)
+ *   workspace     device, 16-byte aligned, at least demo_rms_norm_grad_workspace(rows, cols) bytes (host
+ *                 only; 0 for one row, then it may be NULL, as it may without dweight), apart from the
+ *                 other buffers; fewer bytes give DEMO_ENOSPACE.  Its contents mean nothing between calls.
+ * Sums are float32.  cols is at most 32768.
+ */
+size_t demo_rms_norm_grad_workspace(int64_t rows, int64_t cols);
+int demo_rms_norm_grad(const void* dy, int64_t lddy, const void* total, int64_t ldt, int dtype, const void* weight,
+                       int weight_dtype, const float* rstd, int64_t rows, int64_t cols, const void* past, int64_t ldp,
+                       void* dx, int64_t lddx, float* dweight, int add, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 /* demo_status_string -- a static, human-readable name for a status code. */
 const char* demo_status_string(int status);
 
