@@ -72,6 +72,12 @@ _SIGS = {
     "demo_rms_norm_grad": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, ctypes.c_int, _c_vp, ctypes.c_int, _c_vp, _c_i64,
                                           _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, ctypes.c_int, _c_vp,
                                           ctypes.c_size_t, _c_vp]),
+    "demo_embedding": (ctypes.c_int, [_c_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, ctypes.c_int, _c_i64,
+                                      _c_i64, ctypes.c_float, _c_vp, _c_i64, ctypes.c_int, _c_vp]),
+    "demo_embedding_grad_workspace": (ctypes.c_size_t, [_c_i64, _c_i64]),
+    "demo_embedding_grad": (ctypes.c_int, [_c_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, ctypes.c_int, _c_i64,
+                                           _c_i64, ctypes.c_float, _c_vp, _c_i64, ctypes.c_int, _c_vp, ctypes.c_size_t,
+                                           _c_vp]),
     "demo_fp8_matmul": (ctypes.c_int, [_c_vp, _c_vp, ctypes.c_int, _c_vp, _c_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64,
                                        _c_vp, _c_i64, ctypes.c_int, ctypes.c_int, _c_vp]),
     "demo_fp8_linear_workspace": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
@@ -412,7 +418,8 @@ def test_stall_next_launch(item=0):
     _check(lib().demo_test_stall_next_launch(item), "demo_test_stall_next_launch")
 
 
-_TRAINING_OPS = ("dropout", "fp8_quantize", "fp8_matmul", "fp8_linear", "Fp8Matrix", "rms_norm", "rms_norm_grad")
+_TRAINING_OPS = ("dropout", "fp8_quantize", "fp8_matmul", "fp8_linear", "Fp8Matrix", "rms_norm", "rms_norm_grad",
+                 "embedding", "embedding_grad")
 
 
 def __getattr__(name):

@@ -577,7 +577,8 @@ int demo_init(int device) {
     return DEMO_ECUDA;
   if (prepare_step_kernels() != cudaSuccess || prepare_encode_kernels() != cudaSuccess ||
       prepare_decode_kernels() != cudaSuccess || prepare_dense_kernels() != cudaSuccess ||
-      prepare_matmul_kernels(sms, &st.clusters) != cudaSuccess || prepare_linear_kernels() != cudaSuccess)
+      prepare_matmul_kernels(sms, &st.clusters) != cudaSuccess || prepare_linear_kernels() != cudaSuccess ||
+      prepare_embedding_kernels() != cudaSuccess)
     return DEMO_ECUDA;
   void* fault = nullptr;
   if (cudaGetSymbolAddress(&fault, g_fault_word) != cudaSuccess) return DEMO_ECUDA;

@@ -136,6 +136,32 @@ int check_norm(int dtype, int weight_dtype, int64_t rows, int64_t cols) {
   return cols > 0 && up(rows, kBlock) > kMaxElems / up(cols, kBlock) ? DEMO_EINVAL : DEMO_OK;
 }
 
+// Tokens as rows of `per`: their region, and whether the arguments are in range.
+int check_tokens(const void* tokens, int token_bytes, int64_t rows, int64_t per, int64_t ld) {
+  if ((token_bytes != 4 && token_bytes != 8) || rows < 0 || per < 0 || rows > kMaxDim || per > kMaxDim) return DEMO_EINVAL;
+  if (rows == 0 || per == 0) return DEMO_OK;
+  if (tokens == nullptr || rows > kMaxDim / per || ld < 0 || ld > kMaxElems) return DEMO_EINVAL;
+  if (rows > 1 && ld > 0 && rows > kMaxElems / ld) return DEMO_EINVAL;
+  return at(tokens, static_cast<uintptr_t>(token_bytes)) ? DEMO_OK : DEMO_EALIGN;
+}
+Tokens tokens_of(const void* tokens, int token_bytes, int64_t rows, int64_t per, int64_t ld) {
+  return Tokens{tokens, per, rows == 1 ? per : ld, token_bytes == 8};
+}
+
+// The gradient's workspace: sorted tokens, their positions, parts of tokens that cross pieces.
+struct EmbedWorkspace {
+  int64_t batch, keys, positions, parts;
+  int piece;
+  EmbedWorkspace(int64_t n, int64_t cols) {
+    batch = n < kMaxSorted ? n : kMaxSorted;
+    piece = embed_piece(batch, cols);
+    keys = up(4 * batch, 16);
+    positions = up(2 * batch, 16);
+    const int64_t pieces = (batch + piece - 1) / piece;
+    parts = pieces > 1 ? pieces * 2 * up(cols, 256) * 4 : 0;
+  }
+};
+
 // One row has no stride (whatever is given must not decide how it is read).
 int64_t row_stride(int64_t rows, int64_t ld) { return rows == 1 ? 0 : ld; }
 
@@ -372,6 +398,106 @@ int demo_rms_norm_grad(const void* dy, int64_t lddy, const void* total, int64_t 
   q.add = add;
   q.inv = static_cast<float>(1.0 / static_cast<double>(cols));
   return to_status(launch_norm_grad(q, dtype, weight_dtype, dev.sms, static_cast<cudaStream_t>(stream)));
+}
+
+int demo_embedding(const void* tokens, int token_bytes, int64_t token_rows, int64_t token_cols, int64_t ldtokens,
+                   const void* table, int64_t ldt, int table_dtype, int64_t vocab, int64_t cols, float scale, void* out,
+                   int64_t ldo, int out_dtype, void* stream) {
+  if (!valid_dtype(table_dtype) || !valid_dtype(out_dtype) || !std::isfinite(scale)) return DEMO_EINVAL;
+  if (vocab < 0 || cols < 0 || vocab > kMaxDim || cols > kMaxDim) return DEMO_EINVAL;
+  int s = check_tokens(tokens, token_bytes, token_rows, token_cols, ldtokens);
+  if (s != DEMO_OK) return s;
+  const int64_t n = token_rows * token_cols;
+  if (n == 0 || cols == 0) return DEMO_OK;
+  if (n > kMaxElems / cols) return DEMO_EINVAL;
+  if (vocab > 0 && (s = check_matrix(table, vocab, cols, ldt, table_dtype, false)) != DEMO_OK) return s;
+  if ((s = check_matrix(out, n, cols, ldo, out_dtype, true)) != DEMO_OK) return s;
+  const Region ro = matrix(out, n, cols, ldo, elem_size(out_dtype));
+  if (overlap(ro, matrix(tokens, token_rows, token_cols, ldtokens, token_bytes)) ||
+      overlap(ro, matrix(table, vocab, cols, ldt, elem_size(table_dtype))))
+    return DEMO_EINVAL;
+  DeviceInfo dev;
+  if ((s = device_info(&dev)) != DEMO_OK) return s;
+  LookupParams q;
+  std::memset(&q, 0, sizeof(q));
+  q.tokens = tokens_of(tokens, token_bytes, token_rows, token_cols, ldtokens);
+  q.table = table;
+  q.out = out;
+  q.n = n;
+  q.vocab = vocab;
+  q.cols = cols;
+  q.ldt = row_stride(vocab, ldt);
+  q.ldo = row_stride(n, ldo);
+  q.scale = scale;
+  return to_status(launch_lookup(q, table_dtype, out_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t demo_embedding_grad_workspace(int64_t n, int64_t cols) {
+  if (n <= 0 || cols <= 0 || n > kMaxDim || cols > kMaxDim) return 0;
+  const EmbedWorkspace w(n, cols);
+  return static_cast<size_t>(w.keys + w.positions + w.parts);
+}
+
+int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows, int64_t token_cols, int64_t ldtokens,
+                        const void* dy, int64_t lddy, int dtype, int64_t vocab, int64_t cols, float scale, float* grad,
+                        int64_t ldg, int add, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(dtype) || !std::isfinite(scale) || add < 0 || add > 1) return DEMO_EINVAL;
+  if (vocab < 0 || cols < 0 || vocab > kMaxDim || cols > kMaxDim) return DEMO_EINVAL;
+  int s = check_tokens(tokens, token_bytes, token_rows, token_cols, ldtokens);
+  if (s != DEMO_OK) return s;
+  const int64_t n = token_rows * token_cols;
+  if (vocab == 0 || cols == 0 || (n == 0 && add)) return DEMO_OK;
+  if (n > kMaxElems / cols || vocab > kMaxElems / cols) return DEMO_EINVAL;
+  if ((s = check_matrix(grad, vocab, cols, ldg, DEMO_F32, true)) != DEMO_OK) return s;
+  const EmbedWorkspace w(n, cols);
+  if (n > 0) {
+    if ((s = check_matrix(dy, n, cols, lddy, dtype, false)) != DEMO_OK) return s;
+    const int64_t need = w.keys + w.positions + w.parts;
+    if (workspace_bytes < static_cast<size_t>(need)) return DEMO_ENOSPACE;
+    if (workspace == nullptr) return DEMO_EINVAL;
+    if (!at(workspace, 16)) return DEMO_EALIGN;
+    const Region rg = matrix(grad, vocab, cols, ldg, 4), rw = flat(workspace, need);
+    for (const Region& in : {matrix(tokens, token_rows, token_cols, ldtokens, token_bytes),
+                             matrix(dy, n, cols, lddy, elem_size(dtype))})
+      if (overlap(rg, in) || overlap(rw, in)) return DEMO_EINVAL;
+    if (overlap(rg, rw)) return DEMO_EINVAL;
+  }
+  DeviceInfo dev;
+  if ((s = device_info(&dev)) != DEMO_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* work = static_cast<char*>(workspace);
+  SortParams t;
+  std::memset(&t, 0, sizeof(t));
+  EmbedGradParams q;
+  std::memset(&q, 0, sizeof(q));
+  t.tokens = tokens_of(tokens, token_bytes, token_rows, token_cols, ldtokens);
+  t.vocab = vocab;
+  q.dy = dy;
+  q.grad = grad;
+  q.vocab = vocab;
+  q.cols = cols;
+  q.lddy = row_stride(n, lddy);
+  q.ldg = row_stride(vocab, ldg);
+  q.piece = w.piece;
+  q.add = add;
+  q.scale = scale;
+  if (n > 0) {
+    q.keys = t.keys = reinterpret_cast<int*>(work);
+    q.positions = t.positions = reinterpret_cast<unsigned short*>(work + w.keys);
+    q.parts = reinterpret_cast<float*>(work + w.keys + w.positions);
+  }
+  // As many tokens at a time as one cluster sorts; the later ones are added.
+  int64_t first = 0;
+  do {
+    const int64_t left = n - first;
+    t.n = q.n = static_cast<int>(left < w.batch ? left : w.batch);
+    t.first = q.first = first;
+    if (t.n > 0 && (s = to_status(launch_sort_tokens(t, st))) != DEMO_OK) return s;
+    if ((s = to_status(launch_embed_grad(q, dtype, st))) != DEMO_OK) return s;
+    q.add = 1;
+    first += t.n;
+  } while (first < n);
+  return DEMO_OK;
 }
 
 int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,

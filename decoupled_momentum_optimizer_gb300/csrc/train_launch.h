@@ -102,6 +102,53 @@ struct NormGradParams {
 };
 cudaError_t launch_norm_grad(NormGradParams& p, int dtype, int weight_dtype, int sms, cudaStream_t st);
 
+// Token tables (see train_embedding.cu).  Tokens are `per` consecutive ones in rows `ld` apart, 4 or 8 bytes each.
+struct Tokens {
+  const void* p;
+  long long per, ld;
+  int wide;
+};
+struct LookupParams {
+  Tokens tokens;
+  const void* table;
+  void* out;
+  long long n, vocab, cols, ldt, ldo;
+  float scale;
+};
+cudaError_t launch_lookup(const LookupParams& p, int table_dtype, int out_dtype, cudaStream_t st);
+
+constexpr int kMaxSorted = 65536;  // tokens that one cluster sorts
+struct SortParams {
+  Tokens tokens;
+  long long first, vocab;  // the first token's flat position
+  int n, passes, bits;     // passes over digits of `bits`: set by the launcher
+  int* keys;               // [n] sorted; vocab stands for tokens outside the table
+  unsigned short* positions;  // [n], from the first token on
+};
+cudaError_t launch_sort_tokens(const SortParams& p, cudaStream_t st);
+struct EmbedGradParams {
+  const int* keys;
+  const unsigned short* positions;
+  const void* dy;
+  float* grad;
+  float* parts;  // [pieces][2][ldparts]
+  long long first, vocab, cols, lddy, ldg, ldparts;
+  int n, piece, slabs, add;  // piece: 8, 16 or 32
+  unsigned int zero_blocks;
+  float scale;
+};
+cudaError_t launch_embed_grad(EmbedGradParams& p, int dtype, cudaStream_t st);
+cudaError_t prepare_embedding_kernels();
+
+// Sorted positions of a piece (one warp's work on 256 columns): 32, or fewer where those would leave most
+// SMs without sixteen warps.
+constexpr int embed_piece(long long n, long long cols) {
+  const long long slabs = (cols + 255) / 256;
+  int piece = 32;
+  while (piece > 8 && (n + piece - 1) / piece * slabs < 152 * 16) piece /= 2;
+  return piece;
+}
+
 // out = a b^T (+ out): a [m][k], b [n][k] quantized by rows.
 struct MatmulParams {
   CUtensorMap a, b;    // codes, unused without blocks

@@ -1,7 +1,7 @@
-"""Training operators beside the shard step: dropout, norms, 8-bit quantization and its products.
+"""Training operators beside the shard step: embedding, norms, dropout, 8-bit quantization and its products.
 
-Bindings of ``demo_dropout``, ``demo_fp8_quantize``, ``demo_fp8_matmul``, ``demo_fp8_linear``, ``demo_rms_norm`` and
-``demo_rms_norm_grad`` (``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
+Bindings of ``demo_dropout``, ``demo_fp8_quantize``, ``demo_fp8_matmul``, ``demo_fp8_linear``, ``demo_rms_norm``,
+``demo_rms_norm_grad``, ``demo_embedding`` and ``demo_embedding_grad`` (``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
 torch unless an ``out`` is given, the call runs on torch's current stream (or on ``stream``, as if it
 were the current one) and raises :class:`DemoError` on a negative status.
 
@@ -463,3 +463,87 @@ def rms_norm_grad(dy, total, weight, rstd, *, past=None, out=None, dweight=None,
     _run("demo_rms_norm_grad", (dp, ldd, tp, ldt, _DTYPES[dy.dtype], wp, wdt, sp, rows, cols, pp, ldp, op, ldo, gp, bool(add),
                                 wsp, need), dy.get_device())
     return out, dweight
+
+
+def _tokens(t):
+    """(pointer, bytes a token, rows, tokens a row, row stride) of an integer tensor of any shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("tokens must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("tokens must be on a CUDA device (there is no CPU path)")
+    size = 8 if t.dtype == torch.int64 else 4 if t.dtype == torch.int32 else 0
+    if not size:
+        raise TypeError(f"tokens have dtype {t.dtype}, expected int32 or int64")
+    n = t.numel()
+    if t.is_contiguous() or n <= 1:
+        return t.data_ptr(), size, 1, n, n
+    # Dimensions that make one run of tokens are one; what is left is a run, or rows of runs.
+    runs = []
+    for length, stride in zip(t.shape, t.stride()):
+        if length == 1:
+            continue
+        if runs and runs[-1][1] == length * stride:
+            runs[-1] = (runs[-1][0] * length, stride)
+        else:
+            runs.append((length, stride))
+    if len(runs) == 1:
+        return t.data_ptr(), size, n, 1, runs[0][1]
+    if len(runs) == 2 and runs[1][1] == 1:
+        return t.data_ptr(), size, runs[0][0], runs[1][0], runs[0][1]
+    raise ValueError("tokens must be rows of consecutive ones with one stride between rows")
+
+
+def embedding(tokens, table, *, scale=1.0, dtype=None, out=None, stream=None):
+    """``scale * table[tokens]`` (demo_embedding) as [*tokens.shape, cols]: rows of a [vocab, cols] table in
+    ``dtype`` (the table's by default), zeros for tokens outside [0, vocab).
+
+    The gradient of the table is :func:`embedding_grad`.
+    """
+    if stream is not None:
+        return _on_stream(stream, table.device, embedding, tokens, table, scale=scale, dtype=dtype, out=out)
+    kp, size, krows, kcols, ldk = _tokens(tokens)
+    tp, ldt, vocab, cols = _matrix(table, "table")
+    if table.dim() != 2:
+        raise ValueError(f"table has {table.dim()} dimensions, expected 2")
+    if tokens.get_device() != table.get_device():
+        raise ValueError(f"tokens are on {tokens.device}, the table on {table.device}")
+    out, op, ldo, odt = _out(out, (*tokens.shape, cols), _result_dtype(out, dtype, table.dtype), table)
+    _run("demo_embedding", (kp, size, krows, kcols, ldk, tp, ldt, _DTYPES[table.dtype], vocab, cols, scale, op, ldo, odt),
+         table.get_device())
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _embedding_workspace(n, cols):
+    return _lib.demo_embedding_grad_workspace(n, cols)
+
+
+def embedding_grad(tokens, dy, vocab=None, *, scale=1.0, out=None, add=False, workspace=None, stream=None):
+    """The gradient of :func:`embedding`'s table (demo_embedding_grad), float32 [vocab, cols]: ``scale`` times the
+    sum of the rows of ``dy`` [*tokens.shape, cols] for each token, in a fixed order.
+
+    ``out``   a float32 [vocab, cols] to write (a slice of the flat gradient, say); a new tensor otherwise.  With
+              ``add`` the sums are added to it, and rows that no token names stay as they are.
+    ``workspace``   uint8; allocated through torch where it is not given
+    """
+    if stream is not None:
+        return _on_stream(stream, dy.device, embedding_grad, tokens, dy, vocab, scale=scale, out=out, add=add,
+                          workspace=workspace)
+    kp, size, krows, kcols, ldk = _tokens(tokens)
+    dp, ldd, n, cols = _matrix(dy, "dy")
+    if dy.shape[:-1] != tokens.shape:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {(*tokens.shape, cols)}")
+    if tokens.get_device() != dy.get_device():
+        raise ValueError(f"tokens are on {tokens.device}, dy on {dy.device}")
+    if out is None:
+        if vocab is None or add:
+            raise ValueError("add needs an out to add to" if add else "vocab or out is needed")
+    elif out.dim() != 2 or (vocab is not None and vocab != out.shape[0]):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected [{'vocab' if vocab is None else vocab}, {cols}]")
+    else:
+        vocab = out.shape[0]
+    out, gp, ldg, _ = _out(out, (vocab, cols), torch.float32, dy)
+    workspace, wsp, need = _workspace(workspace, _embedding_workspace(n, cols), dy)
+    _run("demo_embedding_grad", (kp, size, krows, kcols, ldk, dp, ldd, _DTYPES[dy.dtype], vocab, cols, scale, gp, ldg,
+                                 bool(add), wsp, need), dy.get_device())
+    return out

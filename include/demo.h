@@ -448,6 +448,34 @@ int demo_rms_norm_grad(const void* dy, int64_t lddy, const void* total, int64_t 
                        void* dx, int64_t lddx, float* dweight, int add, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/*
+ * demo_embedding -- rows of a table by token: out[i] = scale table[t_i], one float32 product, rounded to
+ * out_dtype; zeros where t_i is outside [0, vocab) (padding has no embedding, and no gradient).
+ *   tokens   token_bytes 4 (int32) or 8 (int64) each, token_rows rows of token_cols consecutive ones,
+ *            ldtokens apart; their positions i = row * token_cols + column number the rows of out
+ *   table    [vocab, cols] of table_dtype;  out [token_rows * token_cols, cols] of out_dtype
+ *   scale    finite
+ */
+int demo_embedding(const void* tokens, int token_bytes, int64_t token_rows, int64_t token_cols, int64_t ldtokens,
+                   const void* table, int64_t ldt, int table_dtype, int64_t vocab, int64_t cols, float scale, void* out,
+                   int64_t ldo, int out_dtype, void* stream);
+
+/*
+ * demo_embedding_grad -- the gradient of demo_embedding's table: for every token v in [0, vocab)
+ *   grad[v] = scale * (the sum of dy[i] over the positions i with t_i = v)
+ * added to what grad holds if add (rows that no token names are then not touched; otherwise they are 0).
+ * Sums are float32 in an order that the tokens alone decide: no atomics, the same bits from call to call.
+ *   dy          [positions, cols] of dtype;  grad float32 [vocab, cols];  tokens as above
+ *   workspace   device, 16-byte aligned, at least demo_embedding_grad_workspace(positions, cols) bytes (host
+ *               only), apart from the other buffers; fewer bytes give DEMO_ENOSPACE.  Its contents mean
+ *               nothing between calls.
+ * More than 65536 positions are taken in runs of that many, the later ones added.
+ */
+size_t demo_embedding_grad_workspace(int64_t n, int64_t cols);
+int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows, int64_t token_cols, int64_t ldtokens,
+                        const void* dy, int64_t lddy, int dtype, int64_t vocab, int64_t cols, float scale, float* grad,
+                        int64_t ldg, int add, void* workspace, size_t workspace_bytes, void* stream);
+
 /* demo_status_string -- a static, human-readable name for a status code. */
 const char* demo_status_string(int status);
 

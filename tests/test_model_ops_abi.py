@@ -107,3 +107,62 @@ def test_reference_norm_is_the_formula():
     r = mr.norm_rstd(s, 1e-6)
     want = s * r[:, None] * w
     assert (abs(mr.norm_values(s, r.astype("f4"), w) - want) <= 3.01 * 2.0 ** -24 * abs(want)).all()
+
+
+def lookup(L, **kw):
+    a = dict(t=p(0x10000), tb=8, tr=1, tc=100, ldt=100, tab=p(0x100000), ld=300, td=0, vocab=50, cols=300, scale=1.0,
+             out=p(0x200000), ldo=300, od=1)
+    a.update(kw)
+    return L.demo_embedding(a["t"], a["tb"], a["tr"], a["tc"], a["ldt"], a["tab"], a["ld"], a["td"], a["vocab"], a["cols"],
+                            a["scale"], a["out"], a["ldo"], a["od"], None)
+
+
+def test_embedding_refusals(L):
+    assert lookup(L) in NODEV and lookup(L, tb=4, t=p(0x10004)) in NODEV and lookup(L, tr=5, tc=20, ldt=0) in NODEV
+    for bad in (dict(tb=2), dict(tr=-1), dict(tc=-1), dict(t=None), dict(ldt=-1), dict(td=3), dict(od=-1), dict(vocab=-1),
+                dict(cols=-1), dict(vocab=1 << 31), dict(scale=float("nan")), dict(scale=float("inf")), dict(tab=None),
+                dict(out=None), dict(ldo=299), dict(ld=-1), dict(out=p(0x100010)), dict(out=p(0x10000)),
+                dict(tr=1 << 20, tc=1 << 20), dict(cols=1 << 30, tc=1 << 20), dict(tr=1 << 20, tc=4, ldt=1 << 30)):
+        assert lookup(L, **{"tr": 2, **bad} if "ldt" in bad else bad) == EINVAL, bad
+    for bad in (dict(t=p(0x10004)), dict(tab=p(0x100002)), dict(out=p(0x200001))):
+        assert lookup(L, **bad) == EALIGN, bad
+    assert lookup(L, tc=0, t=None) == OK and lookup(L, cols=0) == OK and lookup(L, vocab=0, tab=None) in NODEV
+
+
+def embed_grad(L, **kw):
+    a = dict(t=p(0x10000), tb=8, tr=1, tc=1000, ldt=1000, dy=p(0x100000), ldd=300, dt=1, vocab=50, cols=300, scale=1.0,
+             g=p(0x800000), ldg=300, add=0, work=p(0x900000), bytes=None)
+    a.update(kw)
+    if a["bytes"] is None:
+        a["bytes"] = L.demo_embedding_grad_workspace(max(a["tr"], 0) * max(a["tc"], 0), a["cols"])
+    return L.demo_embedding_grad(a["t"], a["tb"], a["tr"], a["tc"], a["ldt"], a["dy"], a["ldd"], a["dt"], a["vocab"], a["cols"],
+                                 a["scale"], a["g"], a["ldg"], a["add"], a["work"], a["bytes"], None)
+
+
+def test_embedding_grad_refusals(L):
+    assert embed_grad(L) in NODEV and embed_grad(L, add=1) in NODEV
+    for bad in (dict(tb=1), dict(tr=-1), dict(t=None), dict(dt=3), dict(vocab=-1), dict(cols=-1), dict(add=2),
+                dict(scale=float("nan")), dict(dy=None), dict(g=None), dict(ldg=299), dict(work=None), dict(g=p(0x100000)),
+                dict(g=p(0x10000)), dict(work=p(0x800000)), dict(work=p(0x100000)), dict(work=p(0x10000)),
+                dict(vocab=1 << 30, cols=1 << 20)):
+        assert embed_grad(L, **bad) == EINVAL, bad
+    need = L.demo_embedding_grad_workspace(1000, 300)
+    assert embed_grad(L, bytes=need - 1) == ENOSPACE
+    for bad in (dict(t=p(0x10004)), dict(dy=p(0x100001)), dict(g=p(0x800002)), dict(work=p(0x900008))):
+        assert embed_grad(L, **bad) == EALIGN, bad
+    assert embed_grad(L, vocab=0, g=None) == OK and embed_grad(L, cols=0) == OK
+    assert embed_grad(L, tc=0, add=1) == OK and embed_grad(L, tc=0, dy=None, work=None) in NODEV
+    ws = L.demo_embedding_grad_workspace
+    # keys, positions, two parts of 512 columns for each of 125 pieces of 8
+    assert need == 4000 + 2000 + 125 * 2 * 512 * 4
+    assert ws(1, 300) == 32 and ws(0, 5) == ws(-1, 5) == ws(5, 0) == 0
+    assert ws(1 << 30, 2048) == ws(65536, 2048) == 65536 * 6 + 2048 * 2 * 2048 * 4
+
+
+def test_bindings_of_tokens_refuse_cpu_tensors():
+    import decoupled_momentum_optimizer_gb300 as dm
+
+    t, x = torch.zeros(4, dtype=torch.int64), torch.zeros(4, 8)
+    for call in (lambda: dm.embedding(t, x), lambda: dm.embedding_grad(t, x, 4)):
+        with pytest.raises(ValueError, match="no CPU path"):
+            call()
