@@ -78,6 +78,10 @@ _SIGS = {
     "demo_embedding_grad": (ctypes.c_int, [_c_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, ctypes.c_int, _c_i64,
                                            _c_i64, ctypes.c_float, _c_vp, _c_i64, ctypes.c_int, _c_vp, ctypes.c_size_t,
                                            _c_vp]),
+    "demo_grad_workspace": (ctypes.c_size_t, [ctypes.c_int]),
+    "demo_grad_norm": (ctypes.c_int, [ctypes.c_int, _c_vp, _c_vp, ctypes.c_int, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+    "demo_clip_grads": (ctypes.c_int, [ctypes.c_int, _c_vp, _c_vp, ctypes.c_int, _c_vp, ctypes.c_int, ctypes.c_double, _c_vp,
+                                       ctypes.c_int, _c_vp, ctypes.c_size_t, _c_vp]),
     "demo_fp8_matmul": (ctypes.c_int, [_c_vp, _c_vp, ctypes.c_int, _c_vp, _c_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64,
                                        _c_vp, _c_i64, ctypes.c_int, ctypes.c_int, _c_vp]),
     "demo_fp8_linear_workspace": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
@@ -419,7 +423,7 @@ def test_stall_next_launch(item=0):
 
 
 _TRAINING_OPS = ("dropout", "fp8_quantize", "fp8_matmul", "fp8_linear", "Fp8Matrix", "rms_norm", "rms_norm_grad",
-                 "embedding", "embedding_grad")
+                 "embedding", "embedding_grad", "grad_norm", "clip_grads")
 
 
 def __getattr__(name):

@@ -1,7 +1,10 @@
 // C ABI of the training operators: argument checks, tensor maps, launches.  What each call
 // computes is described in include/demo.h.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "../../include/demo.h"
 #include "train_launch.h"
@@ -161,6 +164,92 @@ struct EmbedWorkspace {
     parts = pieces > 1 ? pieces * 2 * up(cols, 256) * 4 : 0;
   }
 };
+
+// Whether a list of tensors may be read, and written, as one call does: a place that is written is apart from
+// every other place.
+struct Span {
+  uintptr_t begin, end;
+  bool written;
+};
+bool apart(Span* spans, int64_t count) {
+  const auto before = [](const Span& a, const Span& b) { return a.begin < b.begin; };
+  if (!std::is_sorted(spans, spans + count, before)) std::sort(spans, spans + count, before);
+  uintptr_t read = 0, written = 0;  // the ends of those so far
+  for (int64_t i = 0; i < count; ++i) {
+    if (spans[i].begin < written || (spans[i].written && spans[i].begin < read)) return false;
+    uintptr_t& end = spans[i].written ? written : read;
+    end = std::max(end, spans[i].end);
+  }
+  return true;
+}
+
+int64_t clip_launches(int64_t count) { return count > 0 ? (count + kClipTensors - 1) / kClipTensors : 1; }
+
+// The arguments that the norm and the clipping share.  `out` NULL: nothing but the norm is written.
+int check_grads(int count, const void* const* g, const int64_t* n, int dtype, void* const* out, int out_dtype, const float* norm,
+                bool needs_work, const void* workspace, size_t workspace_bytes) {
+  if (count < 0 || !valid_dtype(dtype) || norm == nullptr || (count > 0 && (g == nullptr || n == nullptr))) return DEMO_EINVAL;
+  const size_t need = needs_work ? demo_grad_workspace(count) : 0;
+  if (workspace_bytes < need) return DEMO_ENOSPACE;
+  if (need > 0 && workspace == nullptr) return DEMO_EINVAL;
+  if (!at(norm, 4) || (need > 0 && !at(workspace, 16))) return DEMO_EALIGN;
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[2 * static_cast<size_t>(count) + 2]);
+  if (spans == nullptr) return DEMO_ENOSPACE;
+  int64_t used = 0;
+  const auto span = [&](const void* p, int64_t bytes, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    spans[used++] = Span{a, a + static_cast<uintptr_t>(bytes), written};
+  };
+  const int64_t size = elem_size(dtype), osize = elem_size(out_dtype);
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (n[i] < 0 || n[i] > kMaxElems) return DEMO_EINVAL;
+    if (n[i] == 0) continue;
+    total += n[i];
+    if (g[i] == nullptr || total > kMaxElems) return DEMO_EINVAL;
+    if (!at(g[i], static_cast<uintptr_t>(size))) return DEMO_EALIGN;
+    if (out != nullptr) {
+      if (out[i] == nullptr) return DEMO_EINVAL;
+      if (!at(out[i], static_cast<uintptr_t>(osize))) return DEMO_EALIGN;
+    }
+    const bool here = out != nullptr && out[i] == g[i] && size == osize;
+    span(g[i], n[i] * size, here);
+    if (out != nullptr && !here) span(out[i], n[i] * osize, true);
+  }
+  span(norm, 4, true);
+  if (need > 0) span(workspace, static_cast<int64_t>(need), true);
+  return apart(spans.get(), used) ? DEMO_OK : DEMO_EINVAL;
+}
+
+// The tensors of one launch, from `from` on; returns the next one's index.
+int fill_clip(ClipParams* q, int from, int count, const void* const* g, const int64_t* n, void* const* out, int64_t size) {
+  q->count = 0;
+  q->chunks = 0;
+  for (; from < count && q->count < kClipTensors; ++from) {
+    if (n[from] == 0) continue;
+    q->g[q->count] = g[from];
+    q->out[q->count] = out != nullptr ? out[from] : nullptr;
+    q->n[q->count] = n[from];
+    q->start[q->count++] = q->chunks;
+    q->chunks += static_cast<unsigned int>(clip_chunks(reinterpret_cast<uintptr_t>(g[from]), n[from], static_cast<int>(size)));
+  }
+  return from;
+}
+
+// Launches the sums of squares of all tensors; *parts_used sums are left in `parts`.
+int launch_all_squares(ClipParams* q, int count, const void* const* g, const int64_t* n, int dtype, int sms, double* parts,
+                       int* parts_used, cudaStream_t st) {
+  *parts_used = 0;
+  for (int from = 0; from < count;) {
+    from = fill_clip(q, from, count, g, n, nullptr, elem_size(dtype));
+    if (q->count == 0) break;
+    q->parts = parts + *parts_used;
+    *parts_used += clip_parts(*q, sms);
+    const int s = to_status(launch_squares(*q, dtype, sms, st));
+    if (s != DEMO_OK) return s;
+  }
+  return DEMO_OK;
+}
 
 // One row has no stride (whatever is given must not decide how it is read).
 int64_t row_stride(int64_t rows, int64_t ld) { return rows == 1 ? 0 : ld; }
@@ -498,6 +587,59 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
     first += t.n;
   } while (first < n);
   return DEMO_OK;
+}
+
+size_t demo_grad_workspace(int count) {
+  return count < 0 ? 0 : static_cast<size_t>(clip_launches(count)) * kClipParts * sizeof(double);
+}
+
+int demo_grad_norm(int count, const void* const* g, const int64_t* n, int dtype, float* norm, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  int s = check_grads(count, g, n, dtype, nullptr, dtype, norm, true, workspace, workspace_bytes);
+  if (s != DEMO_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_info(&dev)) != DEMO_OK) return s;
+  ClipParams q;
+  double* parts = static_cast<double*>(workspace);
+  int used = 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = launch_all_squares(&q, count, g, n, dtype, dev.sms, parts, &used, st)) != DEMO_OK) return s;
+  return to_status(launch_norm_of_parts(parts, used, norm, st));
+}
+
+int demo_clip_grads(int count, const void* const* g, const int64_t* n, int dtype, void* const* out, int out_dtype,
+                    double max_norm, float* norm, int norm_given, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!(max_norm >= 0.0) || norm_given < 0 || norm_given > 1) return DEMO_EINVAL;
+  if (!valid_dtype(out_dtype) || (out_dtype != dtype && out_dtype != DEMO_F32)) return DEMO_EINVAL;
+  if (out == nullptr && (out_dtype != dtype || count < 0 || (count > 0 && g == nullptr))) return DEMO_EINVAL;
+  // Without `out` the gradients themselves are written.
+  void* const* to = out != nullptr ? out : const_cast<void* const*>(g);
+  int s = check_grads(count, g, n, dtype, to, out_dtype, norm, !norm_given, workspace, workspace_bytes);
+  if (s != DEMO_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_info(&dev)) != DEMO_OK) return s;
+  ClipParams q;
+  double* parts = static_cast<double*>(workspace);
+  int used = 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!norm_given && (s = launch_all_squares(&q, count, g, n, dtype, dev.sms, parts, &used, st)) != DEMO_OK) return s;
+  bool any = false;
+  for (int from = 0; from < count;) {
+    from = fill_clip(&q, from, count, g, n, to, elem_size(dtype));
+    if (q.count == 0) break;
+    q.part_count = used;
+    q.all_parts = parts;
+    q.given = norm_given;
+    q.first_launch = !any;
+    q.in_place = 1;
+    for (int i = 0; i < q.count; ++i) q.in_place = q.in_place && q.out[i] == q.g[i];
+    q.max_norm = max_norm;
+    q.norm = norm;
+    if ((s = to_status(launch_scale(q, dtype, out_dtype, dev.sms, st))) != DEMO_OK) return s;
+    any = true;
+  }
+  // Nothing to scale: the norm over nothing.
+  return any || norm_given ? DEMO_OK : to_status(launch_norm_of_parts(parts, 0, norm, st));
 }
 
 int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,

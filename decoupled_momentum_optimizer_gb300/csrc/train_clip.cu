@@ -1,0 +1,248 @@
+// The norm over all gradients of a model, and the gradients scaled to a largest norm:
+//
+//   norm = sqrt(sum over the tensors and their elements of g^2)
+//   out  = g * f,  f = max_norm / norm where max_norm < norm < infinity, else 1
+//
+// Bound by HBM: one read for the norm, another read and a write where something is scaled.  The tensors'
+// addresses and sizes are kernel parameters, so a list of them is one launch and no copy.  A tensor is
+// cut into chunks of 32 KB of whole 16-byte accesses (its first and last access may be partial), and CTAs take
+// every gridDim.x-th chunk of the list: which elements a thread sums, and in which order the sums are joined,
+// follow from the sizes and the grid alone.
+//
+// A thread squares and sums the 32 or 64 elements of a chunk in float32 (sums of four or eight, then a tree) and
+// adds that to a float64 sum: float64 for every element would take 1.9 ms for 2^30 elements (two lanes an SM),
+// three times what HBM takes.  A chunk sum that overflows, or that is so small that squares may have been lost
+// below float32's range, is done again in float64 from the registers the elements are in, so the norm is right
+// over all of float32's range.
+#include <type_traits>
+
+#include "train_common.cuh"
+
+namespace demo {
+
+constexpr int kClipThreads = 256, kClipUnroll = 8, kClipChunk = kClipThreads * kClipUnroll;  // in 16-byte accesses
+
+template <typename T>
+constexpr int kClipN = 16 / static_cast<int>(sizeof(T));
+
+// A chunk of a tensor: accesses [first, ...) counted from the 16-byte boundary at or below its start, `off`
+// elements before it.
+template <typename T>
+struct Chunk {
+  const T* base;  // element 0 of access 0 (may lie before the tensor)
+  long long off, end, first;  // the tensor is elements off .. end - 1 from base
+  int tensor;
+
+  __device__ __forceinline__ Chunk(const ClipParams& p, unsigned chunk) {
+    int lo = 0, hi = p.count - 1;  // the last tensor that starts at or before the chunk
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (p.start[mid] <= chunk)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    tensor = lo;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p.g[lo]);
+    off = static_cast<long long>((a & 15) / sizeof(T));
+    base = reinterpret_cast<const T*>(a & ~static_cast<uintptr_t>(15));
+    end = off + p.n[lo];
+    first = static_cast<long long>(chunk - p.start[lo]) * kClipChunk + threadIdx.x;
+  }
+  __device__ __forceinline__ long long access(int u) const { return first + u * kClipThreads; }
+  __device__ __forceinline__ bool whole(long long v) const {
+    return v * kClipN<T> >= off && (v + 1) * kClipN<T> <= end;
+  }
+  // Elements of a partial access, 0 around the tensor.
+  __device__ __forceinline__ uint4 load_part(long long v) const {
+    Vec<T, kClipN<T>> q;
+#pragma unroll
+    for (int e = 0; e < kClipN<T>; ++e) {
+      const long long i = v * kClipN<T> + e;
+      q.e[e] = i >= off && i < end ? base[i] : from_f32<T>(0.0f);
+    }
+    return *reinterpret_cast<const uint4*>(&q);
+  }
+  __device__ __forceinline__ void load(uint4 (&x)[kClipUnroll]) const {
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) {
+      const long long v = access(u);
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (whole(v))
+        x[u] = reinterpret_cast<const uint4*>(base)[v];
+      else if (v * kClipN<T> < end)
+        x[u] = load_part(v);
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& x, float (&v)[kClipN<T>]) {
+  const Vec<T, kClipN<T>> q = *reinterpret_cast<const Vec<T, kClipN<T>>*>(&x);
+#pragma unroll
+  for (int e = 0; e < kClipN<T>; ++e) v[e] = to_f32(q.e[e]);
+}
+
+// The sum of a CTA's threads' values, for all of them.
+__device__ __forceinline__ double cta_sum(double v, double* sh) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = sh[0];
+#pragma unroll
+  for (int w = 1; w < kClipThreads / 32; ++w) t += sh[w];
+  return t;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kClipThreads) squares_kernel(const __grid_constant__ ClipParams p) {
+  __shared__ double sh[kClipThreads / 32];
+  kernel_begin();
+  double total = 0.0;
+  for (unsigned c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+    const Chunk<T> chunk(p, c);
+    uint4 x[kClipUnroll];
+    chunk.load(x);
+    float s[kClipUnroll];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) {
+      float v[kClipN<T>];
+      unpack<T>(x[u], v);
+      s[u] = v[0] * v[0];
+#pragma unroll
+      for (int e = 1; e < kClipN<T>; ++e) s[u] = __fmaf_rn(v[e], v[e], s[u]);
+    }
+#pragma unroll
+    for (int d = 1; d < kClipUnroll; d *= 2)
+#pragma unroll
+      for (int u = 0; u < kClipUnroll; u += 2 * d) s[u] += s[u + d];
+    // At 2^-90 the squares lost below 2^-149, 64 of them, are 2^-53 of the sum.
+    if (s[0] >= 0x1p-90f && s[0] <= 0x1p120f) {
+      total += static_cast<double>(s[0]);
+    } else {
+      uint32_t any = 0;
+#pragma unroll
+      for (int u = 0; u < kClipUnroll; ++u) any |= x[u].x | x[u].y | x[u].z | x[u].w;
+      if (any != 0) {
+        double t = 0.0;
+#pragma unroll
+        for (int u = 0; u < kClipUnroll; ++u) {
+          float v[kClipN<T>];
+          unpack<T>(x[u], v);
+#pragma unroll
+          for (int e = 0; e < kClipN<T>; ++e) t += static_cast<double>(v[e]) * static_cast<double>(v[e]);
+        }
+        total += t;
+      }
+    }
+  }
+  total = cta_sum(total, sh);
+  if (threadIdx.x == 0) p.parts[blockIdx.x] = total;
+}
+
+// The norm from the CTAs' sums, for all threads of a CTA.
+__device__ __forceinline__ float norm_of(const double* parts, int count, double* sh) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < count; i += kClipThreads) v += parts[i];
+  return static_cast<float>(sqrt(cta_sum(v, sh)));
+}
+
+__global__ void __launch_bounds__(kClipThreads) norm_kernel_of_parts(const double* parts, int count, float* norm) {
+  __shared__ double sh[kClipThreads / 32];
+  kernel_begin();
+  const float n = norm_of(parts, count, sh);
+  if (threadIdx.x == 0) *norm = n;
+}
+
+// g f rounded to O; with f = 1 the element itself, a NaN's payload included, where O is its type.
+template <typename T, typename O>
+__device__ __forceinline__ O scaled(T g, float f) {
+  if constexpr (std::is_same_v<T, O>) {
+    if (f == 1.0f) return g;
+  }
+  return from_f32<O>(to_f32(g) * f);
+}
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_constant__ ClipParams p) {
+  __shared__ double sh[kClipThreads / 32];
+  __shared__ float factor;
+  kernel_begin();
+  const float norm = p.given ? *p.norm : norm_of(p.all_parts, p.part_count, sh);
+  if (threadIdx.x == 0) {
+    if (!p.given && blockIdx.x == 0 && p.first_launch) *p.norm = norm;
+    const bool some = static_cast<double>(norm) > p.max_norm && norm <= 3.402823466e38f;
+    factor = some ? static_cast<float>(p.max_norm / static_cast<double>(norm)) : 1.0f;
+  }
+  __syncthreads();
+  const float f = factor;
+  if (f == 1.0f && p.in_place) return;
+  // Backwards: what the norm read last is still in L2.
+  for (unsigned i = blockIdx.x; i < p.chunks; i += gridDim.x) {
+    const Chunk<T> chunk(p, p.chunks - 1 - i);
+    uint4 x[kClipUnroll];
+    chunk.load(x);
+    O* out = static_cast<O*>(p.out[chunk.tensor]);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(out) - static_cast<uintptr_t>(chunk.off) * sizeof(O)) & 15) == 0;
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) {
+      const long long v = chunk.access(u), i0 = v * kClipN<T> - chunk.off;
+      const Vec<T, kClipN<T>> g = *reinterpret_cast<const Vec<T, kClipN<T>>*>(&x[u]);
+      if (chunk.whole(v) && aligned) {
+        constexpr int P = 16 / static_cast<int>(sizeof(O));
+#pragma unroll
+        for (int k = 0; k < kClipN<T> / P; ++k) {
+          Vec<O, P> q;
+#pragma unroll
+          for (int e = 0; e < P; ++e) q.e[e] = scaled<T, O>(g.e[P * k + e], f);
+          *reinterpret_cast<Vec<O, P>*>(out + i0 + P * k) = q;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kClipN<T>; ++e)
+          if (i0 + e >= 0 && i0 + e < chunk.end - chunk.off) out[i0 + e] = scaled<T, O>(g.e[e], f);
+      }
+    }
+  }
+}
+
+namespace {
+
+unsigned clip_grid(unsigned chunks, int sms) {
+  const unsigned most = static_cast<unsigned>(4 * sms < kClipParts ? 4 * sms : kClipParts);
+  return chunks < most ? chunks : most;
+}
+
+template <typename T, typename O>
+cudaError_t launch_scale_t(const ClipParams& p, int sms, cudaStream_t st) {
+  return launch_overlapped(scale_kernel<T, O>, clip_grid(p.chunks, sms), kClipThreads, 0, st, p);
+}
+
+}  // namespace
+
+long long clip_chunks(uintptr_t address, long long n, int size) {
+  const long long per = 16 / size, off = static_cast<long long>(address & 15) / size;
+  return ((off + n + per - 1) / per + kClipChunk - 1) / kClipChunk;
+}
+
+int clip_parts(const ClipParams& p, int sms) { return static_cast<int>(clip_grid(p.chunks, sms)); }
+
+cudaError_t launch_squares(const ClipParams& p, int dtype, int sms, cudaStream_t st) {
+  auto* kernel = dtype == kF32 ? squares_kernel<float> : dtype == kBF16 ? squares_kernel<__nv_bfloat16> : squares_kernel<__half>;
+  return launch_overlapped(kernel, clip_grid(p.chunks, sms), kClipThreads, 0, st, p);
+}
+
+cudaError_t launch_norm_of_parts(const double* parts, int count, float* norm, cudaStream_t st) {
+  return launch_overlapped(norm_kernel_of_parts, 1, kClipThreads, 0, st, parts, count, norm);
+}
+
+cudaError_t launch_scale(const ClipParams& p, int dtype, int out_dtype, int sms, cudaStream_t st) {
+  if (dtype == kF32) return launch_scale_t<float, float>(p, sms, st);
+  if (dtype == kBF16)
+    return out_dtype == kF32 ? launch_scale_t<__nv_bfloat16, float>(p, sms, st)
+                             : launch_scale_t<__nv_bfloat16, __nv_bfloat16>(p, sms, st);
+  return out_dtype == kF32 ? launch_scale_t<__half, float>(p, sms, st) : launch_scale_t<__half, __half>(p, sms, st);
+}
+
+}  // namespace demo

@@ -149,6 +149,28 @@ constexpr int embed_piece(long long n, long long cols) {
   return piece;
 }
 
+// The gradients' norm and their scaling (see train_clip.cu): a launch takes up to kClipTensors tensors.
+constexpr int kClipTensors = 512;
+constexpr int kClipParts = 640;  // most CTAs of a launch, each of which leaves a sum
+struct ClipParams {
+  const void* g[kClipTensors];
+  void* out[kClipTensors];
+  long long n[kClipTensors];
+  unsigned int start[kClipTensors];  // the tensor's first chunk; empty tensors are left out
+  int count, part_count;
+  unsigned int chunks;
+  int given, first_launch, in_place;
+  double max_norm;
+  double* parts;            // this launch's sums
+  const double* all_parts;  // every launch's
+  float* norm;
+};
+long long clip_chunks(uintptr_t address, long long n, int size);  // chunks of a tensor
+int clip_parts(const ClipParams& p, int sms);                     // CTAs of its launch
+cudaError_t launch_squares(const ClipParams& p, int dtype, int sms, cudaStream_t st);
+cudaError_t launch_norm_of_parts(const double* parts, int count, float* norm, cudaStream_t st);
+cudaError_t launch_scale(const ClipParams& p, int dtype, int out_dtype, int sms, cudaStream_t st);
+
 // out = a b^T (+ out): a [m][k], b [n][k] quantized by rows.
 struct MatmulParams {
   CUtensorMap a, b;    // codes, unused without blocks

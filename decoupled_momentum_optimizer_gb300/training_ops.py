@@ -1,7 +1,9 @@
-"""Training operators beside the shard step: embedding, norms, dropout, 8-bit quantization and its products.
+"""Training operators beside the shard step: embedding, norms, dropout, 8-bit quantization and its products,
+and the clipping of what they leave.
 
 Bindings of ``demo_dropout``, ``demo_fp8_quantize``, ``demo_fp8_matmul``, ``demo_fp8_linear``, ``demo_rms_norm``,
-``demo_rms_norm_grad``, ``demo_embedding`` and ``demo_embedding_grad`` (``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
+``demo_rms_norm_grad``, ``demo_embedding``, ``demo_embedding_grad``, ``demo_grad_norm`` and ``demo_clip_grads``
+(``include/demo.h``), in the package's manner: tensors are checked, results are allocated through
 torch unless an ``out`` is given, the call runs on torch's current stream (or on ``stream``, as if it
 were the current one) and raises :class:`DemoError` on a negative status.
 
@@ -12,6 +14,7 @@ recorded (a result without history would end the branch's training without a wor
 """
 
 import collections
+import ctypes
 import functools
 
 import torch
@@ -547,3 +550,90 @@ def embedding_grad(tokens, dy, vocab=None, *, scale=1.0, out=None, add=False, wo
     _run("demo_embedding_grad", (kp, size, krows, kcols, ldk, dp, ldd, _DTYPES[dy.dtype], vocab, cols, scale, gp, ldg,
                                  bool(add), wsp, need), dy.get_device())
     return out
+
+
+def _grads(gs, name):
+    """(tensors, their count, pointers, sizes) of one gradient or a list of them: one dtype, one device, contiguous."""
+    gs = (gs,) if isinstance(gs, torch.Tensor) else gs
+    count = len(gs)
+    if not count:
+        raise ValueError(f"need at least one of {name}")
+    dt, index = gs[0].dtype, gs[0].get_device()
+    if dt not in _DTYPES:
+        raise TypeError(f"{name} have dtype {dt}, expected float32, bfloat16 or float16")
+    recorded = torch.is_grad_enabled()
+    for r, g in enumerate(gs):
+        if g.dtype != dt or g.get_device() != index or not g.is_cuda or not g.is_contiguous() or \
+                (recorded and g.requires_grad):
+            _refuse(g, f"{name}[{r}]", dt, gs[0].device)
+    return gs, count, (ctypes.c_void_p * count)(*[g.data_ptr() for g in gs]), \
+        (ctypes.c_int64 * count)(*[g.numel() for g in gs])
+
+
+def _refuse(g, name, dtype, device):
+    if not g.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
+    if g.dtype != dtype:
+        raise TypeError(f"{name} has dtype {g.dtype}, expected {dtype}")
+    if g.device != device:
+        raise ValueError(f"{name} is on {g.device}, the call's other tensors on {device}")
+    if not g.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} requires a gradient, and this call records none: detach it, or call under "
+                     "torch.no_grad() or from a torch.autograd.Function")
+
+
+def _scalar(t, name, beside):
+    """(tensor, pointer) of a float32 scalar on the device, a new one where none is given."""
+    if t is None:
+        t = torch.empty((), dtype=torch.float32, device=beside.device)
+    elif t.requires_grad and torch.is_grad_enabled():
+        _refuse(t, name, t.dtype, t.device)
+    return t, _row_values(t, name, 1, beside)
+
+
+@functools.lru_cache(maxsize=64)
+def _grad_workspace(count):
+    return _lib.demo_grad_workspace(count)
+
+
+def grad_norm(gs, *, out=None, workspace=None, stream=None):
+    """The norm over all elements of a gradient, or of a list of them (one dtype, contiguous), as a float32
+    scalar on the device (demo_grad_norm); ``out`` receives it."""
+    if stream is not None:
+        first = gs if isinstance(gs, torch.Tensor) else gs[0]
+        return _on_stream(stream, first.device, grad_norm, gs, out=out, workspace=workspace)
+    gs, count, ptrs, sizes = _grads(gs, "gradients")
+    out, op = _scalar(out, "out", gs[0])
+    workspace, wsp, need = _workspace(workspace, _grad_workspace(count), gs[0])
+    _run("demo_grad_norm", (count, ptrs, sizes, _DTYPES[gs[0].dtype], op, wsp, need), gs[0].get_device())
+    return out
+
+
+def clip_grads(gs, max_norm, *, norm=None, out=None, workspace=None, stream=None):
+    """Scales a gradient, or a list of them (one dtype, contiguous), to a norm of ``max_norm`` at most
+    (demo_clip_grads); returns the norm before, a float32 scalar on the device.  Nothing waits for the device.
+
+    ``norm``  the norm to clip by, where it is not that of ``gs`` alone (gradients in several shards); it is
+              computed otherwise
+    ``out``   tensors of the same sizes to write, in the gradients' dtype or float32; in place otherwise
+    A norm that is not finite scales nothing.
+    """
+    if stream is not None:
+        first = gs if isinstance(gs, torch.Tensor) else gs[0]
+        return _on_stream(stream, first.device, clip_grads, gs, max_norm, norm=norm, out=out, workspace=workspace)
+    gs, count, ptrs, sizes = _grads(gs, "gradients")
+    outs, odt = None, gs[0].dtype
+    if out is not None:
+        out, n, outs, to = _grads(out, "outs")
+        odt = out[0].dtype
+        if n != count or any(a != b for a, b in zip(sizes, to)):
+            raise ValueError("out must hold a tensor of the same size for each gradient")
+        if out[0].get_device() != gs[0].get_device():
+            raise ValueError(f"out is on {out[0].device}, the gradients on {gs[0].device}")
+    given = norm is not None
+    norm, normp = _scalar(norm, "norm", gs[0])
+    workspace, wsp, need = _workspace(workspace, 0 if given else _grad_workspace(count), gs[0])
+    _run("demo_clip_grads", (count, ptrs, sizes, _DTYPES[gs[0].dtype], outs, _DTYPES[odt], max_norm, normp, given, wsp, need),
+         gs[0].get_device())
+    return norm

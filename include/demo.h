@@ -476,6 +476,37 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
                         const void* dy, int64_t lddy, int dtype, int64_t vocab, int64_t cols, float scale, float* grad,
                         int64_t ldg, int add, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * demo_grad_norm -- the norm over all gradients: *norm = sqrt(sum over i and the n[i] elements of g[i] of
+ * their squares), float32 on the device, summed in float64 from float32 sums of 64 squares at most (whose
+ * squares neither overflow nor vanish below float32's range), in an order that the sizes, the addresses
+ * modulo 16 and the device decide.  A gradient that is listed twice counts twice; an infinity gives
+ * infinity, a NaN NaN; count 0 gives 0.
+ *   g, n        host arrays of count device pointers (element-aligned) and sizes; entries with n 0 are passed over
+ *   norm        device float32
+ *   workspace   device, 16-byte aligned, at least demo_grad_workspace(count) bytes (host only); fewer give
+ *               DEMO_ENOSPACE.  Its contents mean nothing between calls.
+ * norm and workspace are apart from each other and from the gradients (DEMO_EINVAL).
+ */
+size_t demo_grad_workspace(int count);
+int demo_grad_norm(int count, const void* const* g, const int64_t* n, int dtype, float* norm, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * demo_clip_grads -- the gradients scaled to a norm of max_norm at most: out[i] = g[i] f, rounded once, with
+ * f = max_norm / norm to float32 where max_norm < norm < infinity, and 1 elsewhere (a norm that is not
+ * finite scales nothing: the caller sees it in *norm).  Arguments as demo_grad_norm's, and
+ *   out          NULL: the gradients are scaled in place (with f = 1 nothing is written); or count device
+ *                pointers to n[i] elements of out_dtype (dtype or DEMO_F32), each g[i] itself (same dtype) or
+ *                apart from every gradient and every other out
+ *   max_norm     not negative (infinity scales nothing)
+ *   norm_given   0: *norm receives the gradients' norm; 1: *norm is read (the norm over several shards'
+ *                gradients, say), and workspace may be NULL
+ * What is written is listed once: the same gradient twice in place is refused (DEMO_EINVAL).
+ */
+int demo_clip_grads(int count, const void* const* g, const int64_t* n, int dtype, void* const* out, int out_dtype,
+                    double max_norm, float* norm, int norm_given, void* workspace, size_t workspace_bytes, void* stream);
+
 /* demo_status_string -- a static, human-readable name for a status code. */
 const char* demo_status_string(int status);
 

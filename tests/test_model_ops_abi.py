@@ -166,3 +166,63 @@ def test_bindings_of_tokens_refuse_cpu_tensors():
     for call in (lambda: dm.embedding(t, x), lambda: dm.embedding_grad(t, x, 4)):
         with pytest.raises(ValueError, match="no CPU path"):
             call()
+
+
+def arrays(ptrs, sizes):
+    return (ctypes.c_void_p * len(ptrs))(*ptrs), (ctypes.c_int64 * len(sizes))(*sizes)
+
+
+def clip(L, ptrs=(0x100000, 0x200000), sizes=(1000, 2000), out=None, **kw):
+    a = dict(count=len(ptrs), dt=0, od=None, mx=1.0, norm=p(0x50000), given=0, work=p(0x60000), bytes=None)
+    a.update(kw)
+    g, n = arrays(ptrs, sizes)
+    o = arrays(out, sizes)[0] if out is not None else None
+    if a["bytes"] is None:
+        a["bytes"] = L.demo_grad_workspace(max(a["count"], 0))
+    if a["od"] is None:
+        a["od"] = a["dt"]
+    return L.demo_clip_grads(a["count"], g, n, a["dt"], o, a["od"], a["mx"], a["norm"], a["given"], a["work"], a["bytes"], None)
+
+
+def grad_norm(L, ptrs=(0x100000, 0x200000), sizes=(1000, 2000), **kw):
+    a = dict(count=len(ptrs), dt=0, norm=p(0x50000), work=p(0x60000), bytes=1 << 20)
+    a.update(kw)
+    g, n = arrays(ptrs, sizes)
+    return L.demo_grad_norm(a["count"], g, n, a["dt"], a["norm"], a["work"], a["bytes"], None)
+
+
+def test_clip_refusals(L):
+    assert clip(L) in NODEV and grad_norm(L) in NODEV
+    for bad in (dict(count=-1), dict(dt=3), dict(norm=None), dict(work=None), dict(norm=p(0x100010)), dict(norm=p(0x60010)),
+                dict(work=p(0x200000))):
+        assert clip(L, **bad) == EINVAL and grad_norm(L, **bad) == EINVAL, bad
+    for bad in (dict(mx=-1.0), dict(mx=float("nan")), dict(given=2), dict(od=1), dict(dt=1, od=2), dict(od=0, dt=1)):
+        assert clip(L, **bad) == EINVAL, bad
+    for bad in (dict(norm=p(0x50002)), dict(work=p(0x60008))):
+        assert clip(L, **bad) == EALIGN and grad_norm(L, **bad) == EALIGN, bad
+    assert clip(L, ptrs=(0x100002, 0x200000)) == EALIGN and clip(L, ptrs=(0x100002, 0x200000), dt=1) in NODEV
+    assert clip(L, ptrs=(0x100000, None)) == EINVAL and clip(L, ptrs=(0x100000, None), sizes=(5, 0)) in NODEV
+    assert clip(L, sizes=(5, -1)) == EINVAL and clip(L, sizes=(1 << 39, 1)) == EINVAL
+    assert clip(L, bytes=639 * 8) == ENOSPACE and grad_norm(L, bytes=0) == ENOSPACE
+    assert clip(L, given=1, work=None, bytes=0) in NODEV and clip(L, mx=float("inf")) in NODEV
+    # the same twice, or overlapping: read in the norm, never written
+    assert clip(L, ptrs=(0x100000, 0x100000)) == EINVAL and grad_norm(L, ptrs=(0x100000, 0x100000)) in NODEV
+    assert clip(L, ptrs=(0x100000, 0x100000 + 3996)) == EINVAL and clip(L, ptrs=(0x200000, 0x100000)) in NODEV
+    # elsewhere: apart from every gradient and from each other, or in the gradient's own place
+    far = (0x300000, 0x400000)
+    assert clip(L, out=far) in NODEV and clip(L, out=far, dt=1, od=0) in NODEV
+    assert clip(L, out=(0x100000, 0x400000)) in NODEV and clip(L, out=(0x100000, 0x400000), dt=1, od=0) == EINVAL
+    assert clip(L, ptrs=(0x100000, 0x100000), out=far) in NODEV  # read twice, written apart
+    for out in ((0x300000, 0x300000), (0x200000, 0x100000), (0x100004, 0x400000), (None, 0x400000), (0x50000 - 400, 0x400000)):
+        assert clip(L, out=out) == EINVAL, out
+    assert clip(L, out=(0x300002, 0x400000)) == EALIGN
+    assert L.demo_grad_workspace(0) == L.demo_grad_workspace(512) == 5120 and L.demo_grad_workspace(513) == 10240
+    assert L.demo_grad_workspace(-1) == 0
+
+
+def test_bindings_of_gradients_refuse_cpu_tensors():
+    import decoupled_momentum_optimizer_gb300 as dm
+
+    for call in (lambda: dm.grad_norm(torch.zeros(4)), lambda: dm.clip_grads([torch.zeros(4)], 1.0)):
+        with pytest.raises(ValueError, match="no CPU path"):
+            call()
