@@ -18,7 +18,7 @@ LIB_NAME = "libdemo_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["demo_api.cu", "demo_step.cu", "demo_encode.cu", "demo_decode.cu", "demo_decode_lanes.cu",
            "demo_decode_groups.cu", "demo_dense.cu", "demo_adamw.cu", "train_api.cu", "train_dropout.cu",
-           "train_quantize.cu", "train_matmul.cu", "train_linear.cu", "train_norm.cu",
+           "train_quantize.cu", "train_matmul.cu", "train_linear.cu", "train_norm.cu", "train_norm_grad.cu",
            "train_embedding.cu", "train_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,196 @@
+// What the root-mean-square norm and its gradient share: how a row lies in registers, and arithmetic on pairs
+// of floats.
+#pragma once
+
+#include "train_common.cuh"
+
+namespace demo {
+
+template <typename T>
+constexpr bool is_bf16 = false;
+template <>
+constexpr bool is_bf16<__nv_bfloat16> = true;
+
+// ----------------------------------------------------------------------------
+// Two float32 operations in one instruction
+// ----------------------------------------------------------------------------
+
+// Each half rounds as the scalar operation does.  The norm's kernels are bound by the instructions an element
+// takes, not by HBM, without it.
+typedef unsigned long long F2;
+
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves_of(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The largest magnitude of m (not negative), a and b; NaN if one is.
+__device__ __forceinline__ float max_abs_nan(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+
+// ----------------------------------------------------------------------------
+// A row in registers
+// ----------------------------------------------------------------------------
+
+// Unit j of a row's warp w covers 32 N columns, from (j W + w) 32 N on; lane l holds N consecutive ones as one
+// 16-byte access, or, where rows are not whole aligned accesses, N columns 32 apart (N = 4, so that a block of
+// 128 is one unit of one warp).  Rows of less than a unit are held by `lanes` lanes, a power of two, and a
+// warp holds 32 / lanes of them.
+template <typename T, bool VEC>
+constexpr int kNormN = VEC ? 16 / static_cast<int>(sizeof(T)) : 4;
+
+template <bool VEC, int N>
+__device__ __forceinline__ int norm_column(int base, int lane, int lanes, int e) {
+  return VEC ? base + lane * N + e : base + lanes * e + lane;
+}
+
+// Two 16-bit elements in a word, the first in its low half.
+template <typename T>
+__device__ __forceinline__ F2 widen(uint32_t w) {
+  if constexpr (is_bf16<T>) return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f2(v.x, v.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t narrow(F2 p) {
+  const float2 v = halves_of(p);
+  if constexpr (is_bf16<T>) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __half2 r = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Sums and magnitudes of packed elements.  The sum of two 16-bit values rounded once is their float32 sum
+// rounded: 24 bits are at least 2 * 11 + 2.
+template <typename T>
+__device__ __forceinline__ uint32_t packed_add(uint32_t a, uint32_t b) {
+  using V = std::conditional_t<is_bf16<T>, __nv_bfloat162, __half2>;
+  const V r = __hadd2_rn(*reinterpret_cast<const V*>(&a), *reinterpret_cast<const V*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t packed_max_abs(uint32_t m, uint32_t a) {
+  using V = std::conditional_t<is_bf16<T>, __nv_bfloat162, __half2>;
+  const V r = __hmax2(*reinterpret_cast<const V*>(&m), __habs2(*reinterpret_cast<const V*>(&a)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// A lane's N elements of a unit: whole accesses of 16 bits stay packed in words (as an array of 16-bit elements
+// they took a register each), all others are float32.
+template <typename T, bool VEC, int N>
+struct Unit {
+  static constexpr bool kPacked = VEC && sizeof(T) == 2;
+  static constexpr int kWords = kPacked ? N / 2 : N;
+  uint32_t w[kWords];
+
+  // Elements 2 i and 2 i + 1.
+  __device__ __forceinline__ F2 get2(int i) const {
+    if constexpr (kPacked) return widen<T>(w[i]);
+    return f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  // Their float32 values rounded to T.
+  __device__ __forceinline__ void set2(int i, F2 v) {
+    if constexpr (kPacked) {
+      w[i] = narrow<T>(v);
+    } else {
+      const float2 h = halves_of(v);
+      w[2 * i] = __float_as_uint(to_f32(from_f32<T>(h.x)));
+      w[2 * i + 1] = __float_as_uint(to_f32(from_f32<T>(h.y)));
+    }
+  }
+  __device__ __forceinline__ void add(const Unit& o) {
+#pragma unroll
+    for (int i = 0; i < (kPacked ? kWords : N / 2); ++i) {
+      if constexpr (kPacked)
+        w[i] = packed_add<T>(w[i], o.w[i]);
+      else
+        set2(i, add2(get2(i), o.get2(i)));
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // N elements of a row at `base`, zero past its end.  CONST: memory that the kernel does not write.
+  template <bool CONST = false>
+  __device__ __forceinline__ void load(const T* row, int base, int lane, int lanes, int cols) {
+    if constexpr (VEC) {
+      if (base + lane * N < cols) {
+        const uint4* q = reinterpret_cast<const uint4*>(row + base + lane * N);
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+          const uint4 v = CONST ? __ldg(q + i) : q[i];
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+      } else {
+        clear();
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int c = norm_column<VEC, N>(base, lane, lanes, e);
+        w[e] = c < cols ? __float_as_uint(to_f32(CONST ? __ldg(row + c) : row[c])) : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int base, int lane, int lanes, int cols) const {
+    if constexpr (VEC) {
+      if (base + lane * N < cols) *reinterpret_cast<uint4*>(row + base + lane * N) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int c = norm_column<VEC, N>(base, lane, lanes, e);
+        if (c < cols) row[c] = from_f32<T>(__uint_as_float(w[e]));
+      }
+    }
+  }
+};
+
+template <typename V>
+__device__ __forceinline__ V lane_sum(V v, int lanes = 32) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    if (d < lanes) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// Host: whether rows are whole 16-byte accesses of n elements.
+inline bool whole_rows(const void* q, long long ld, int n) {
+  return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld % n == 0;
+}
+
+// Host: lanes of a row of `accesses` accesses, the next power of two.
+inline int row_lanes(long long accesses) {
+  int l = 1;
+  while (l < 32 && l < accesses) l *= 2;
+  return l;
+}
+
+}  // namespace demo
