@@ -80,7 +80,7 @@ struct NormParams {
   float* scales;
   long long rows, cols, ldx, ldr, ldt, ldo;
   unsigned int col_blocks;
-  int fmt, warps, lanes;  // warps of a row, lanes of one of less than a warp: set by the launcher
+  int fmt, warps, per, lanes;  // warps of a row, units of a warp, lanes of a short row: set by the launcher
   float inv_hi, inv_lo, eps_hi, eps_lo;
   double inv, eps;
 };
@@ -97,7 +97,7 @@ struct NormGradParams {
   float* dw;        // may be NULL
   float* partials;  // [CTAs][cols], unused with one CTA
   long long rows, cols, lddy, ldt, ldp, lddx;
-  int add, warps, lanes;  // warps of a row, lanes of one of less than a warp: set by the launcher
+  int add, warps, per, lanes;  // warps of a row, units of a warp, lanes of a short row: set by the launcher
   float inv;
 };
 cudaError_t launch_norm_grad(NormGradParams& p, int dtype, int weight_dtype, int sms, cudaStream_t st);

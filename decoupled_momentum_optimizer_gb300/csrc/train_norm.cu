@@ -84,35 +84,27 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
   long long row = blockIdx.x;
   if (warps == 1) row = (row * (blockDim.x >> 5) + in_cta) * (32 / lanes) + ((threadIdx.x & 31) / lanes);
   const int cols = static_cast<int>(p.cols);
+  Place at = Place::of<VEC, N>(warp, UNITS == 1 ? 1 : p.per, lane, lanes, cols);
   kernel_begin();
   if (__all_sync(0xffffffffu, row >= p.rows)) return;  // one warp to a row only: no barrier follows
   const bool live = UNITS > 1 || row < p.rows;
   Unit<T, VEC, N> s[UNITS];
   {
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const int reach = live ? cols : 0;
+    if (UNITS == 1 && !live) at.reach = 0;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx + at.first;
 #pragma unroll
-    for (int j = 0; j < UNITS; ++j) {
-      const int base = (j * warps + warp) * 32 * N;
-      s[j].clear();
-      if (base < cols) s[j].load(x, base, lane, lanes, reach);
-    }
+    for (int j = 0; j < UNITS; ++j) s[j].load(x, at, j);
     if (p.residual != nullptr) {
-      const T* res = static_cast<const T*>(p.residual) + row * p.ldr;
+      const T* res = static_cast<const T*>(p.residual) + row * p.ldr + at.first;
       Unit<T, VEC, N> r[UNITS];
 #pragma unroll
-      for (int j = 0; j < UNITS; ++j) {
-        const int base = (j * warps + warp) * 32 * N;
-        if (base < cols) r[j].load(res, base, lane, lanes, reach);
-      }
-      T* total = static_cast<T*>(p.total) + row * p.ldt;
+      for (int j = 0; j < UNITS; ++j) r[j].load(res, at, j);
 #pragma unroll
-      for (int j = 0; j < UNITS; ++j) {
-        const int base = (j * warps + warp) * 32 * N;
-        if (base < cols) {
-          s[j].add(r[j]);
-          if (p.total != nullptr) s[j].store(total, base, lane, lanes, reach);
-        }
+      for (int j = 0; j < UNITS; ++j) s[j].add(r[j]);
+      if (p.total != nullptr) {
+        T* total = static_cast<T*>(p.total) + row * p.ldt + at.first;
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) s[j].store(total, at, j);
       }
     }
   }
@@ -124,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
     for (int j = 0; j < UNITS; ++j)
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) m = packed_max_abs<T>(m, s[j].w[i]);
-    const float2 v = halves_of(widen<T>(m));
+    const float2 v = widen<T>(m);
     top = fmaxf(v.x, v.y);
   } else {
 #pragma unroll
@@ -139,7 +131,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
     F2 H = f2(c, c), L = f2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < UNITS; ++j) {
-      if ((j * warps + warp) * 32 * N < cols) {
+      if (UNITS == 1 || at.unit<VEC, N>(j, lane)) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
           const F2 v = s[j].get2(i), h = fma2(v, v, H);
@@ -148,7 +140,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
         }
       }
     }
-    const float2 h = halves_of(H), l = halves_of(L);
+    const float2 h = H, l = L;
     sum = Pair{h.x, l.x};
     sum.add(-c);
     Pair other{h.y, l.y};
@@ -170,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
     for (int j = 0; j < UNITS; ++j) {
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
-        const float2 v = halves_of(s[j].get2(i));
+        const float2 v = s[j].get2(i);
         total += static_cast<double>(v.x) * v.x + static_cast<double>(v.y) * v.y;
       }
     }
@@ -185,18 +177,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
   if (p.rstd != nullptr && warp == 0 && lane == 0 && live) p.rstd[row] = rstd;
   if (p.out == nullptr && p.codes == nullptr) return;
 
-  const W* weight = static_cast<const W*>(p.weight);
-  T* out = static_cast<T*>(p.out) + row * p.ldo;
+  const W* weight = static_cast<const W*>(p.weight) + at.first;
+  T* out = static_cast<T*>(p.out) + row * p.ldo + at.first;
   const int kp = static_cast<int>(p.col_blocks) * kBlock;
-  uint8_t* codes = static_cast<uint8_t*>(p.codes) + row * kp;
+  uint8_t* codes = static_cast<uint8_t*>(p.codes) + row * kp + at.first;
   const long long lds = (p.rows + 3) / 4 * 4;
   const F2 r2 = f2(rstd, rstd);
 #pragma unroll
   for (int j = 0; j < UNITS; ++j) {
-    const int base = (j * warps + warp) * 32 * N;
-    if (base < cols) {
+    if (UNITS == 1 || at.unit<VEC, N>(j, lane)) {
       Unit<W, VEC, N> w;
-      w.template load<true>(weight, base, lane, lanes, cols);
+      w.template load<true>(weight, at, j);
       F2 v[N / 2];
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) v[i] = mul2(mul2(s[j].get2(i), r2), w.get2(i));
@@ -204,13 +195,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
         Unit<T, VEC, N> o;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) o.set2(i, v[i]);
-        o.store(out, base, lane, lanes, live ? cols : 0);
+        o.store(out, at, j);
       }
       if (p.codes != nullptr) {
         float u[N], amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          const float2 h = halves_of(v[i]);
+          const float2 h = v[i];
           u[2 * i] = h.x;
           u[2 * i + 1] = h.y;
           amax = max_abs_nan(amax, h.x, h.y);
@@ -219,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
           amax = 0.0f;
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            u[e] = norm_column<VEC, N>(base, lane, lanes, e) < cols ? finite_or_nan(u[e]) : 0.0f;
+            u[e] = at.has<VEC, N>(j, e) ? finite_or_nan(u[e]) : 0.0f;
             amax = fmaxf(amax, fabsf(u[e]));  // passes over a NaN
           }
         }
@@ -238,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
         const F2 inv2 = f2(inv, inv);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          const float2 h = halves_of(mul2(f2(u[2 * i], u[2 * i + 1]), inv2));
+          const float2 h = mul2(f2(u[2 * i], u[2 * i + 1]), inv2);
           u[2 * i] = h.x;
           u[2 * i + 1] = h.y;
         }
@@ -247,21 +238,21 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
         for (int e = 0; e < N; e += 4)
           q[e / 4] = p.fmt == kE4M3 ? codes4<kE4M3>(u[e], u[e + 1], u[e + 2], u[e + 3])
                                     : codes4<kE5M2>(u[e], u[e + 1], u[e + 2], u[e + 3]);
-        const int c0 = norm_column<VEC, N>(base, lane, lanes, 0);
+        const int off = at.offset<VEC, N>(j, 0), c0 = at.first + off;
         if (live) {
           if constexpr (VEC) {
             if (c0 < kp) {
               if constexpr (N == 8)
-                *reinterpret_cast<uint2*>(codes + c0) = make_uint2(q[0], q[1]);
+                *reinterpret_cast<uint2*>(codes + off) = make_uint2(q[0], q[1]);
               else
-                *reinterpret_cast<uint32_t*>(codes + c0) = q[0];
+                *reinterpret_cast<uint32_t*>(codes + off) = q[0];
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) codes[c0 + lanes * e] = static_cast<uint8_t>(q[0] >> (8 * e));
+            for (int e = 0; e < 4; ++e) codes[off + lanes * e] = static_cast<uint8_t>(q[0] >> (8 * e));
           }
           if (lanes < kSpan)  // a short row's lanes also clear the rest of its one block
-            for (int c = lanes * N + lane; c < kBlock; c += lanes) codes[c] = 0;
+            for (int c = lanes * N + lane; c < kBlock; c += lanes) codes[c - at.first] = 0;
           if ((lane & (kSpan - 1)) == 0 && c0 < kp) {
             float* scale = p.scales + static_cast<long long>(c0 / kBlock) * lds;
             scale[row] = pow2f(exponent);
@@ -291,12 +282,12 @@ cudaError_t launch_norm_v(NormParams& p, int sms, cudaStream_t st) {
   constexpr int n = kNormN<T, VEC>;
   const long long units = (p.cols + 32 * n - 1) / (32 * n);
   p.warps = norm_warps(p.rows, units, sms);
-  const long long per = (units + p.warps - 1) / p.warps;  // units of a warp
+  p.per = static_cast<int>((units + p.warps - 1) / p.warps);
   p.lanes = units == 1 ? row_lanes((p.cols + n - 1) / n) : 32;
-  auto* kernel = p.warps > kNormThreads / 32 ? (per <= 4 ? norm_kernel<T, W, VEC, 4, kNormWide>
+  auto* kernel = p.warps > kNormThreads / 32 ? (p.per <= 4 ? norm_kernel<T, W, VEC, 4, kNormWide>
                                                          : norm_kernel<T, W, VEC, kNormUnits, kNormWide>)
-                 : per == 1                  ? norm_kernel<T, W, VEC, 1, kNormThreads>
-                 : per <= 4                  ? norm_kernel<T, W, VEC, 4, kNormThreads>
+                 : p.per == 1                 ? norm_kernel<T, W, VEC, 1, kNormThreads>
+                 : p.per <= 4                 ? norm_kernel<T, W, VEC, 4, kNormThreads>
                                              : norm_kernel<T, W, VEC, kNormUnits, kNormThreads>;
   if (p.warps > 1) return launch_overlapped(kernel, static_cast<unsigned>(p.rows), 32 * p.warps, 0, st, p);
   const long long rows = kNormThreads / p.lanes;  // of a CTA

@@ -17,33 +17,12 @@ constexpr bool is_bf16<__nv_bfloat16> = true;
 
 // Each half rounds as the scalar operation does.  The norm's kernels are bound by the instructions an element
 // takes, not by HBM, without it.
-typedef unsigned long long F2;
+typedef float2 F2;
 
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 halves_of(F2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
+__device__ __forceinline__ F2 f2(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
 // The largest magnitude of m (not negative), a and b; NaN if one is.
 __device__ __forceinline__ float max_abs_nan(float m, float a, float b) {
   float r;
@@ -55,28 +34,48 @@ __device__ __forceinline__ float max_abs_nan(float m, float a, float b) {
 // A row in registers
 // ----------------------------------------------------------------------------
 
-// Unit j of a row's warp w covers 32 N columns, from (j W + w) 32 N on; lane l holds N consecutive ones as one
-// 16-byte access, or, where rows are not whole aligned accesses, N columns 32 apart (N = 4, so that a block of
-// 128 is one unit of one warp).  Rows of less than a unit are held by `lanes` lanes, a power of two, and a
-// warp holds 32 / lanes of them.
+// A warp holds `per` units of 32 N consecutive columns of a row; in a unit, lane l holds N consecutive ones as
+// one 16-byte access, or, where rows are not whole aligned accesses, N columns 32 apart (N = 4, so that a block
+// of 128 is one unit of one warp).  Rows of less than a unit are held by `lanes` lanes, a power of two, and a
+// warp holds 32 / lanes of them.  A lane's pointers go to its first column, so that unit j is at a constant
+// offset, and one comparison per unit says whether it is in the row.
 template <typename T, bool VEC>
 constexpr int kNormN = VEC ? 16 / static_cast<int>(sizeof(T)) : 4;
 
-template <bool VEC, int N>
-__device__ __forceinline__ int norm_column(int base, int lane, int lanes, int e) {
-  return VEC ? base + lane * N + e : base + lanes * e + lane;
-}
+struct Place {
+  int first;  // column of the lane's first element
+  int reach;  // columns of the warp from there on; 0 or less where it has none
+  int lanes;
+  template <bool VEC, int N>
+  __device__ __forceinline__ static Place of(int warp, int per, int lane, int lanes, int cols) {
+    const int begin = warp * per * 32 * N, mine = cols - begin < per * 32 * N ? cols - begin : per * 32 * N;
+    const int at = VEC ? lane * N : lane;
+    return Place{begin + at, mine - at, lanes};
+  }
+  // Whether the warp has columns in unit j (the same for all of its lanes), lane being the lane in its row.
+  template <bool VEC, int N>
+  __device__ __forceinline__ bool unit(int j, int lane) const {
+    return reach + (VEC ? lane * N : lane) > j * 32 * N;
+  }
+  // Offset of element e of unit j from the lane's first, and whether it is in the row.
+  template <bool VEC, int N>
+  __device__ __forceinline__ int offset(int j, int e) const {
+    return j * 32 * N + (VEC ? e : lanes * e);
+  }
+  template <bool VEC, int N>
+  __device__ __forceinline__ bool has(int j, int e) const {
+    return offset<VEC, N>(j, VEC ? 0 : e) < reach;
+  }
+};
 
 // Two 16-bit elements in a word, the first in its low half.
 template <typename T>
 __device__ __forceinline__ F2 widen(uint32_t w) {
   if constexpr (is_bf16<T>) return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return f2(v.x, v.y);
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <typename T>
-__device__ __forceinline__ uint32_t narrow(F2 p) {
-  const float2 v = halves_of(p);
+__device__ __forceinline__ uint32_t narrow(F2 v) {
   if constexpr (is_bf16<T>) {
     const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&r);
@@ -117,9 +116,8 @@ struct Unit {
     if constexpr (kPacked) {
       w[i] = narrow<T>(v);
     } else {
-      const float2 h = halves_of(v);
-      w[2 * i] = __float_as_uint(to_f32(from_f32<T>(h.x)));
-      w[2 * i + 1] = __float_as_uint(to_f32(from_f32<T>(h.y)));
+      w[2 * i] = __float_as_uint(to_f32(from_f32<T>(v.x)));
+      w[2 * i + 1] = __float_as_uint(to_f32(from_f32<T>(v.y)));
     }
   }
   __device__ __forceinline__ void add(const Unit& o) {
@@ -135,12 +133,12 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-  // N elements of a row at `base`, zero past its end.  CONST: memory that the kernel does not write.
+  // The lane's elements of unit j, zero past the row's end.  CONST: memory that the kernel does not write.
   template <bool CONST = false>
-  __device__ __forceinline__ void load(const T* row, int base, int lane, int lanes, int cols) {
+  __device__ __forceinline__ void load(const T* p, const Place& at, int j) {
     if constexpr (VEC) {
-      if (base + lane * N < cols) {
-        const uint4* q = reinterpret_cast<const uint4*>(row + base + lane * N);
+      if (at.has<VEC, N>(j, 0)) {
+        const uint4* q = reinterpret_cast<const uint4*>(p + at.offset<VEC, N>(j, 0));
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) {
           const uint4 v = CONST ? __ldg(q + i) : q[i];
@@ -155,20 +153,21 @@ struct Unit {
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int c = norm_column<VEC, N>(base, lane, lanes, e);
-        w[e] = c < cols ? __float_as_uint(to_f32(CONST ? __ldg(row + c) : row[c])) : 0u;
+        w[e] = 0u;
+        if (at.has<VEC, N>(j, e)) {
+          const T* q = p + at.offset<VEC, N>(j, e);
+          w[e] = __float_as_uint(to_f32(CONST ? __ldg(q) : *q));
+        }
       }
     }
   }
-  __device__ __forceinline__ void store(T* row, int base, int lane, int lanes, int cols) const {
+  __device__ __forceinline__ void store(T* p, const Place& at, int j) const {
     if constexpr (VEC) {
-      if (base + lane * N < cols) *reinterpret_cast<uint4*>(row + base + lane * N) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (at.has<VEC, N>(j, 0)) *reinterpret_cast<uint4*>(p + at.offset<VEC, N>(j, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int c = norm_column<VEC, N>(base, lane, lanes, e);
-        if (c < cols) row[c] = from_f32<T>(__uint_as_float(w[e]));
-      }
+      for (int e = 0; e < N; ++e)
+        if (at.has<VEC, N>(j, e)) p[at.offset<VEC, N>(j, e)] = from_f32<T>(__uint_as_float(w[e]));
     }
   }
 };

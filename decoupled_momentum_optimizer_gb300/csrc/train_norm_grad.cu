@@ -33,8 +33,9 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
   const int group = in_cta / warps, warp = in_cta - group * warps, groups = (blockDim.x >> 5) / warps;
   const int cols = static_cast<int>(p.cols);
   const int share = 32 / lanes;  // rows that a warp shares (one where a row has several)
+  const Place mine = Place::of<VEC, N>(warp, p.per, lane, lanes, cols);
   kernel_begin();
-  const W* weight = static_cast<const W*>(p.weight);
+  const W* weight = static_cast<const W*>(p.weight) + mine.first;
   F2 acc[U][N / 2];
 #pragma unroll
   for (int j = 0; j < U; ++j)
@@ -50,36 +51,30 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const long long row = row0 + k * share;
-      const int reach = row < p.rows ? cols : 0;
-      const T* dyr = static_cast<const T*>(p.dy) + row * p.lddy;
-      const T* sr = static_cast<const T*>(p.total) + row * p.ldt;
+      Place at = mine;
+      if (row >= p.rows) at.reach = 0;
+      const T* dyr = static_cast<const T*>(p.dy) + row * p.lddy + at.first;
+      const T* sr = static_cast<const T*>(p.total) + row * p.ldt + at.first;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int base = (j * warps + warp) * 32 * N;
-        if (base < cols) {
-          dy[k][j].load(dyr, base, lane, lanes, reach);
-          s[k][j].load(sr, base, lane, lanes, reach);
-        }
+        dy[k][j].load(dyr, at, j);
+        s[k][j].load(sr, at, j);
       }
       if (p.past != nullptr) {
-        const T* pr = static_cast<const T*>(p.past) + row * p.ldp;
+        const T* pr = static_cast<const T*>(p.past) + row * p.ldp + at.first;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const int base = (j * warps + warp) * 32 * N;
-          if (base < cols) past[k][j].load(pr, base, lane, lanes, reach);
-        }
+        for (int j = 0; j < U; ++j) past[k][j].load(pr, at, j);
       }
-      rstd[k] = reach > 0 ? p.rstd[row] : 0.0f;
+      rstd[k] = row < p.rows ? p.rstd[row] : 0.0f;
     }
     F2 sum[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) sum[k] = f2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int base = (j * warps + warp) * 32 * N;
-      if (base < cols) {
+      if (U == 1 || mine.unit<VEC, N>(j, lane)) {
         Unit<W, VEC, N> w;
-        w.template load<true>(weight, base, lane, lanes, cols);
+        w.template load<true>(weight, mine, j);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           const F2 r2 = f2(rstd[k], rstd[k]);
@@ -94,7 +89,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const float2 h = halves_of(sum[k]);
+      const float2 h = sum[k];
       dot[k] = lane_sum(h.x + h.y, lanes);
     }
     if (warps > 1) {
@@ -109,10 +104,9 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int base = (j * warps + warp) * 32 * N;
-      if (base < cols) {
+      if (U == 1 || mine.unit<VEC, N>(j, lane)) {
         Unit<W, VEC, N> w;
-        w.template load<true>(weight, base, lane, lanes, cols);
+        w.template load<true>(weight, mine, j);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           const long long row = row0 + k * share;
@@ -126,7 +120,9 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
             if (p.past != nullptr) v = add2(v, past[k][j].get2(i));
             o.set2(i, v);
           }
-          o.store(static_cast<T*>(p.dx) + row * p.lddx, base, lane, lanes, row < p.rows ? cols : 0);
+          Place at = mine;
+          if (row >= p.rows) at.reach = 0;
+          o.store(static_cast<T*>(p.dx) + row * p.lddx + at.first, at, j);
         }
       }
     }
@@ -137,7 +133,8 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
     for (int d = 16; d > 0; d >>= 1) {
       if (d >= lanes) {
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) acc[0][i] = add2(acc[0][i], __shfl_xor_sync(0xffffffffu, acc[0][i], d));
+        for (int i = 0; i < N / 2; ++i) acc[0][i] = add2(acc[0][i], f2(__shfl_xor_sync(0xffffffffu, acc[0][i].x, d),
+                                                               __shfl_xor_sync(0xffffffffu, acc[0][i].y, d)));
       }
     }
   }
@@ -148,12 +145,11 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
     if (group == g && (threadIdx.x & 31) < lanes) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int base = (j * warps + warp) * 32 * N;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const int col = norm_column<VEC, N>(base, lane, lanes, e);
-          if (col < cols) {
-            const float2 h = halves_of(acc[j][e / 2]);
+          const int col = mine.first + mine.offset<VEC, N>(j, e);
+          if (mine.has<VEC, N>(j, e)) {
+            const float2 h = acc[j][e / 2];
             float v = e % 2 ? h.y : h.x;
             if (g > 0) v += joined[col];
             if (g + 1 < groups)
@@ -196,6 +192,7 @@ template <typename T, typename W, bool VEC, int U, int K, int THREADS>
 cudaError_t launch_norm_grad_u(NormGradParams& p, long long units, int sms, cudaStream_t st) {
   p.warps = static_cast<int>((units + U - 1) / U);
   p.lanes = U == 1 && units == 1 ? row_lanes((p.cols + kNormN<T, VEC> - 1) / kNormN<T, VEC>) : 32;
+  p.per = static_cast<int>((units + p.warps - 1) / p.warps);
   const long long rows = (32 / p.lanes) * K;  // of a group
   long long groups = THREADS == kGradThreads ? kGradThreads / 32 / p.warps : 1;
   while (groups > 1 && (groups - 1) * rows >= p.rows) --groups;
