@@ -72,145 +72,162 @@ __device__ __forceinline__ float rsqrt_pair(Pair m) {
 constexpr int kNormUnits = 8;
 constexpr int kNormThreads = 256, kNormWide = 1024;
 
-template <typename T, typename W, bool VEC, int UNITS, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1 ? 5 : UNITS == 4 ? 3 : 2)
+template <typename T, typename W, bool VEC, int UNITS, int K, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS * K == 1 ? 5 : UNITS * K == 4 ? 3 : 2)
     norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int N = kNormN<T, VEC>;
   __shared__ Pair part[THREADS / 32];
   __shared__ double wide[THREADS / 32];
-  const int lanes = UNITS == 1 ? p.lanes : 32, warps = p.warps;
+  const int lanes = UNITS == 1 ? p.lanes : 32, warps = K > 1 ? 1 : p.warps;
   const int in_cta = threadIdx.x >> 5, lane = threadIdx.x & (lanes - 1);
   const int warp = warps == 1 ? 0 : in_cta;  // of the row
-  long long row = blockIdx.x;
-  if (warps == 1) row = (row * (blockDim.x >> 5) + in_cta) * (32 / lanes) + ((threadIdx.x & 31) / lanes);
+  const int share = 32 / lanes;              // rows that a warp shares
+  long long row0 = blockIdx.x;               // and K - 1 more, every `share`-th
+  if (warps == 1) row0 = (row0 * (blockDim.x >> 5) + in_cta) * (share * K) + (threadIdx.x & 31) / lanes;
   const int cols = static_cast<int>(p.cols);
-  Place at = Place::of<VEC, N>(warp, UNITS == 1 ? 1 : p.per, lane, lanes, cols);
+  const Place mine = Place::of<VEC, N>(warp, UNITS == 1 ? 1 : p.per, lane, lanes, cols);
   kernel_begin();
-  if (__all_sync(0xffffffffu, row >= p.rows)) return;  // one warp to a row only: no barrier follows
-  const bool live = UNITS > 1 || row < p.rows;
-  Unit<T, VEC, N> s[UNITS];
-  {
-    if (UNITS == 1 && !live) at.reach = 0;
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx + at.first;
+  if (__all_sync(0xffffffffu, row0 >= p.rows)) return;  // one warp to a row only: no barrier follows
+  const auto place = [&](int k) {
+    Place at = mine;
+    if (UNITS == 1 && row0 + k * share >= p.rows) at.reach = 0;
+    return at;
+  };
+  Unit<T, VEC, N> s[K][UNITS];
 #pragma unroll
-    for (int j = 0; j < UNITS; ++j) s[j].load(x, at, j);
-    if (p.residual != nullptr) {
-      const T* res = static_cast<const T*>(p.residual) + row * p.ldr + at.first;
-      Unit<T, VEC, N> r[UNITS];
+  for (int k = 0; k < K; ++k) {
+    const T* x = static_cast<const T*>(p.x) + (row0 + k * share) * p.ldx + mine.first;
 #pragma unroll
-      for (int j = 0; j < UNITS; ++j) r[j].load(res, at, j);
+    for (int j = 0; j < UNITS; ++j) s[k][j].load(x, place(k), j);
+  }
+  if (p.residual != nullptr) {
+    Unit<T, VEC, N> r[K][UNITS];
 #pragma unroll
-      for (int j = 0; j < UNITS; ++j) s[j].add(r[j]);
+    for (int k = 0; k < K; ++k) {
+      const T* res = static_cast<const T*>(p.residual) + (row0 + k * share) * p.ldr + mine.first;
+#pragma unroll
+      for (int j = 0; j < UNITS; ++j) r[k][j].load(res, place(k), j);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int j = 0; j < UNITS; ++j) s[k][j].add(r[k][j]);
       if (p.total != nullptr) {
-        T* total = static_cast<T*>(p.total) + row * p.ldt + at.first;
+        T* total = static_cast<T*>(p.total) + (row0 + k * share) * p.ldt + mine.first;
 #pragma unroll
-        for (int j = 0; j < UNITS; ++j) s[j].store(total, at, j);
+        for (int j = 0; j < UNITS; ++j) s[k][j].store(total, place(k), j);
       }
     }
   }
-  // The largest magnitude of the lane; an infinity or NaN is met again in the sum.
-  float top = 0.0f;
-  if constexpr (Unit<T, VEC, N>::kPacked) {
-    uint32_t m = 0;
+  Pair sum[K];
 #pragma unroll
-    for (int j = 0; j < UNITS; ++j)
+  for (int k = 0; k < K; ++k) {
+    // The largest magnitude of the lane; an infinity or NaN is met again in the sum.
+    float top = 0.0f;
+    if constexpr (Unit<T, VEC, N>::kPacked) {
+      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) m = packed_max_abs<T>(m, s[j].w[i]);
-    const float2 v = widen<T>(m);
-    top = fmaxf(v.x, v.y);
-  } else {
+      for (int j = 0; j < UNITS; ++j)
 #pragma unroll
-    for (int j = 0; j < UNITS; ++j)
+        for (int i = 0; i < N / 2; ++i) m = packed_max_abs<T>(m, s[k][j].w[i]);
+      const F2 v = widen<T>(m);
+      top = fmaxf(v.x, v.y);
+    } else {
 #pragma unroll
-      for (int i = 0; i < N; i += 2) top = fmaxf(fmaxf(top, fabsf(__uint_as_float(s[j].w[i]))), fabsf(__uint_as_float(s[j].w[i + 1])));
-  }
-  Pair sum;
-  {
+      for (int j = 0; j < UNITS; ++j)
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+          top = fmaxf(fmaxf(top, fabsf(__uint_as_float(s[k][j].w[i]))), fabsf(__uint_as_float(s[k][j].w[i + 1])));
+    }
     const float c = top * top;
     const F2 minus = f2(-1.0f, -1.0f);
     F2 H = f2(c, c), L = f2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < UNITS; ++j) {
-      if (UNITS == 1 || at.unit<VEC, N>(j, lane)) {
+      if (UNITS == 1 || mine.unit<VEC, N>(j, lane)) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          const F2 v = s[j].get2(i), h = fma2(v, v, H);
+          const F2 v = s[k][j].get2(i), h = fma2(v, v, H);
           L = add2(L, fma2(v, v, fma2(h, minus, H)));  // v^2 - (h - H)
           H = h;
         }
       }
     }
-    const float2 h = H, l = L;
-    sum = Pair{h.x, l.x};
-    sum.add(-c);
-    Pair other{h.y, l.y};
+    sum[k] = Pair{H.x, L.x};
+    sum[k].add(-c);
+    Pair other{H.y, L.y};
     other.add(-c);
-    sum.join(other);
+    sum[k].join(other);
   }
-  sum = pair_sum(sum, lanes);
+#pragma unroll
+  for (int k = 0; k < K; ++k) sum[k] = pair_sum(sum[k], lanes);
   if (warps > 1) {
-    if (lane == 0) part[warp] = sum;
+    if (lane == 0) part[warp] = sum[0];
     __syncthreads();
-    sum = pair_sum(lane < warps ? part[lane] : Pair{0.0f, 0.0f});
+    sum[0] = pair_sum(lane < warps ? part[lane] : Pair{0.0f, 0.0f});
   }
-  bool fits;
-  const Pair m = mean_eps(p, sum, &fits);
-  float rstd = rsqrt_pair(m);
-  if (__any_sync(0xffffffffu, !fits)) {  // the same for all of the row's warps
-    double total = 0.0;
+  float rstd[K];
 #pragma unroll
-    for (int j = 0; j < UNITS; ++j) {
+  for (int k = 0; k < K; ++k) {
+    bool fits;
+    const Pair m = mean_eps(p, sum[k], &fits);
+    rstd[k] = rsqrt_pair(m);
+    if (__any_sync(0xffffffffu, !fits)) {  // the same for all of the row's warps
+      double total = 0.0;
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float2 v = s[j].get2(i);
-        total += static_cast<double>(v.x) * v.x + static_cast<double>(v.y) * v.y;
+      for (int j = 0; j < UNITS; ++j) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          const F2 v = s[k][j].get2(i);
+          total += static_cast<double>(v.x) * v.x + static_cast<double>(v.y) * v.y;
+        }
       }
+      total = lane_sum(total, lanes);
+      if (warps > 1) {
+        if (lane == 0) wide[warp] = total;
+        __syncthreads();
+        total = lane_sum(lane < warps ? wide[lane] : 0.0);
+      }
+      if (!fits) rstd[k] = static_cast<float>(1.0 / sqrt(total * p.inv + p.eps));
     }
-    total = lane_sum(total, lanes);
-    if (warps > 1) {
-      if (lane == 0) wide[warp] = total;
-      __syncthreads();
-      total = lane_sum(lane < warps ? wide[lane] : 0.0);
-    }
-    if (!fits) rstd = static_cast<float>(1.0 / sqrt(total * p.inv + p.eps));
+    if (p.rstd != nullptr && warp == 0 && lane == 0 && (UNITS > 1 || row0 + k * share < p.rows)) p.rstd[row0 + k * share] = rstd[k];
   }
-  if (p.rstd != nullptr && warp == 0 && lane == 0 && live) p.rstd[row] = rstd;
   if (p.out == nullptr && p.codes == nullptr) return;
 
-  const W* weight = static_cast<const W*>(p.weight) + at.first;
-  T* out = static_cast<T*>(p.out) + row * p.ldo + at.first;
+  const W* weight = static_cast<const W*>(p.weight) + mine.first;
   const int kp = static_cast<int>(p.col_blocks) * kBlock;
-  uint8_t* codes = static_cast<uint8_t*>(p.codes) + row * kp + at.first;
   const long long lds = (p.rows + 3) / 4 * 4;
-  const F2 r2 = f2(rstd, rstd);
 #pragma unroll
   for (int j = 0; j < UNITS; ++j) {
-    if (UNITS == 1 || at.unit<VEC, N>(j, lane)) {
-      Unit<W, VEC, N> w;
-      w.template load<true>(weight, at, j);
+    if (UNITS > 1 && !mine.unit<VEC, N>(j, lane)) continue;
+    Unit<W, VEC, N> w;
+    w.template load<true>(weight, mine, j);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const long long row = row0 + k * share;
+      const F2 r2 = f2(rstd[k], rstd[k]);
       F2 v[N / 2];
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) v[i] = mul2(mul2(s[j].get2(i), r2), w.get2(i));
+      for (int i = 0; i < N / 2; ++i) v[i] = mul2(mul2(s[k][j].get2(i), r2), w.get2(i));
       if (p.out != nullptr) {
         Unit<T, VEC, N> o;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) o.set2(i, v[i]);
-        o.store(out, at, j);
+        o.store(static_cast<T*>(p.out) + row * p.ldo + mine.first, place(k), j);
       }
       if (p.codes != nullptr) {
         float u[N], amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          const float2 h = v[i];
-          u[2 * i] = h.x;
-          u[2 * i + 1] = h.y;
-          amax = max_abs_nan(amax, h.x, h.y);
+          u[2 * i] = v[i].x;
+          u[2 * i + 1] = v[i].y;
+          amax = max_abs_nan(amax, v[i].x, v[i].y);
         }
         if (!(amax <= 3.402823466e38f)) {  // something is not finite, or NaN past the row (0 times a NaN rstd)
           amax = 0.0f;
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            u[e] = at.has<VEC, N>(j, e) ? finite_or_nan(u[e]) : 0.0f;
+            u[e] = mine.has<VEC, N>(j, e) ? finite_or_nan(u[e]) : 0.0f;
             amax = fmaxf(amax, fabsf(u[e]));  // passes over a NaN
           }
         }
@@ -229,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
         const F2 inv2 = f2(inv, inv);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          const float2 h = mul2(f2(u[2 * i], u[2 * i + 1]), inv2);
+          const F2 h = mul2(f2(u[2 * i], u[2 * i + 1]), inv2);
           u[2 * i] = h.x;
           u[2 * i + 1] = h.y;
         }
@@ -238,8 +255,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
         for (int e = 0; e < N; e += 4)
           q[e / 4] = p.fmt == kE4M3 ? codes4<kE4M3>(u[e], u[e + 1], u[e + 2], u[e + 3])
                                     : codes4<kE5M2>(u[e], u[e + 1], u[e + 2], u[e + 3]);
-        const int off = at.offset<VEC, N>(j, 0), c0 = at.first + off;
-        if (live) {
+        const int off = mine.offset<VEC, N>(j, 0), c0 = mine.first + off;
+        if (UNITS > 1 || row < p.rows) {
+          uint8_t* codes = static_cast<uint8_t*>(p.codes) + row * kp + mine.first;
           if constexpr (VEC) {
             if (c0 < kp) {
               if constexpr (N == 8)
@@ -252,7 +270,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS == 1
             for (int e = 0; e < 4; ++e) codes[off + lanes * e] = static_cast<uint8_t>(q[0] >> (8 * e));
           }
           if (lanes < kSpan)  // a short row's lanes also clear the rest of its one block
-            for (int c = lanes * N + lane; c < kBlock; c += lanes) codes[c - at.first] = 0;
+            for (int c = lanes * N + lane; c < kBlock; c += lanes) codes[c - mine.first] = 0;
           if ((lane & (kSpan - 1)) == 0 && c0 < kp) {
             float* scale = p.scales + static_cast<long long>(c0 / kBlock) * lds;
             scale[row] = pow2f(exponent);
@@ -284,13 +302,16 @@ cudaError_t launch_norm_v(NormParams& p, int sms, cudaStream_t st) {
   p.warps = norm_warps(p.rows, units, sms);
   p.per = static_cast<int>((units + p.warps - 1) / p.warps);
   p.lanes = units == 1 ? row_lanes((p.cols + n - 1) / n) : 32;
-  auto* kernel = p.warps > kNormThreads / 32 ? (p.per <= 4 ? norm_kernel<T, W, VEC, 4, kNormWide>
-                                                         : norm_kernel<T, W, VEC, kNormUnits, kNormWide>)
-                 : p.per == 1                 ? norm_kernel<T, W, VEC, 1, kNormThreads>
-                 : p.per <= 4                 ? norm_kernel<T, W, VEC, 4, kNormThreads>
-                                             : norm_kernel<T, W, VEC, kNormUnits, kNormThreads>;
+  // Four short rows at a time where that leaves every SM eight CTAs.
+  const bool several = units == 1 && p.rows / (kNormThreads / p.lanes) >= 32LL * sms;
+  auto* kernel = several                     ? norm_kernel<T, W, VEC, 1, 4, kNormThreads>
+                 : p.warps > kNormThreads / 32 ? (p.per <= 4 ? norm_kernel<T, W, VEC, 4, 1, kNormWide>
+                                                             : norm_kernel<T, W, VEC, kNormUnits, 1, kNormWide>)
+                 : p.per == 1                 ? norm_kernel<T, W, VEC, 1, 1, kNormThreads>
+                 : p.per <= 4                 ? norm_kernel<T, W, VEC, 4, 1, kNormThreads>
+                                             : norm_kernel<T, W, VEC, kNormUnits, 1, kNormThreads>;
   if (p.warps > 1) return launch_overlapped(kernel, static_cast<unsigned>(p.rows), 32 * p.warps, 0, st, p);
-  const long long rows = kNormThreads / p.lanes;  // of a CTA
+  const long long rows = kNormThreads / p.lanes * (several ? 4 : 1);  // of a CTA
   return launch_overlapped(kernel, static_cast<unsigned>((p.rows + rows - 1) / rows), kNormThreads, 0, st, p);
 }
 

@@ -19,6 +19,8 @@ constexpr int kGradThreads = 512, kGradWide = 1024;
 template <typename T, bool VEC, int THREADS>
 constexpr int kGradUnits = ((VEC && sizeof(T) == 2) || THREADS == kGradWide ? 32 : 16) / kNormN<T, VEC>;
 
+constexpr int kStagedWarps = 8;  // of a group whose sums pass through shared memory
+
 __device__ __forceinline__ void group_barrier(int group, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
 }
@@ -26,7 +28,7 @@ __device__ __forceinline__ void group_barrier(int group, int threads) {
 template <typename T, typename W, bool VEC, int U, int K, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_constant__ NormGradParams p) {
   constexpr int N = kNormN<T, VEC>;
-  extern __shared__ float joined[];  // the CTA's dw, where it has several groups
+  extern __shared__ float joined[];  // sums over rows on their way
   __shared__ float part[2][K][THREADS / 32];
   const int lanes = U == 1 ? p.lanes : 32, warps = p.warps;
   const int in_cta = threadIdx.x >> 5, lane = threadIdx.x & (lanes - 1);
@@ -138,29 +140,58 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
       }
     }
   }
+  // The groups' sums, halving their number: the later half writes, the earlier half adds.  A lane's elements lie
+  // 33 floats apart, lanes one apart: no two lanes meet in a bank, here or when the columns are read in order.
+  const auto slot = [](int warp, int j, int e, int lane) { return ((warp * U + j) * N + e) * 33 + lane; };
+  const int last_lane = threadIdx.x & 31;
+  for (int left = groups; left > 1;) {
+    const int half = (left + 1) / 2;
+    if (group >= half && group < left) {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          joined[slot((group - half) * warps + warp, j, e, last_lane)] = e % 2 ? acc[j][e / 2].y : acc[j][e / 2].x;
+    }
+    __syncthreads();
+    if (group < left - half) {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+          acc[j][i] = add2(acc[j][i], f2(joined[slot(group * warps + warp, j, 2 * i, last_lane)],
+                                         joined[slot(group * warps + warp, j, 2 * i + 1, last_lane)]));
+    }
+    __syncthreads();
+    left = half;
+  }
   // One CTA writes dw itself.
   const bool last = gridDim.x == 1;
   float* dst = last ? p.dw : p.partials + static_cast<long long>(blockIdx.x) * cols;
-  for (int g = 0; g < groups; ++g) {
-    if (group == g && (threadIdx.x & 31) < lanes) {
+  if (warps > kStagedWarps) {  // one group, whose registers do not fit
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
+    for (int j = 0; j < U; ++j)
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const int col = mine.first + mine.offset<VEC, N>(j, e);
-          if (mine.has<VEC, N>(j, e)) {
-            const float2 h = acc[j][e / 2];
-            float v = e % 2 ? h.y : h.x;
-            if (g > 0) v += joined[col];
-            if (g + 1 < groups)
-              joined[col] = v;
-            else
-              dst[col] = last && p.add ? dst[col] + v : v;
-          }
+      for (int e = 0; e < N; ++e) {
+        if (mine.has<VEC, N>(j, e)) {
+          float* d = dst + mine.first + mine.offset<VEC, N>(j, e);
+          const float v = e % 2 ? acc[j][e / 2].y : acc[j][e / 2].x;
+          *d = last && p.add ? *d + v : v;
         }
       }
-    }
-    if (groups > 1) __syncthreads();
+    return;
+  }
+  if (group == 0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int e = 0; e < N; ++e) joined[slot(warp, j, e, last_lane)] = e % 2 ? acc[j][e / 2].y : acc[j][e / 2].x;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+    const int unit = c / (32 * N), in = c - unit * 32 * N, w = U == 1 ? unit : unit / p.per, j = unit - w * p.per;
+    const float v = VEC ? joined[slot(w, j, in % N, in / N)] : joined[slot(w, j, in / lanes, in % lanes)];
+    dst[c] = last && p.add ? dst[c] + v : v;
   }
 }
 
@@ -194,13 +225,17 @@ cudaError_t launch_norm_grad_u(NormGradParams& p, long long units, int sms, cuda
   p.lanes = U == 1 && units == 1 ? row_lanes((p.cols + kNormN<T, VEC> - 1) / kNormN<T, VEC>) : 32;
   p.per = static_cast<int>((units + p.warps - 1) / p.warps);
   const long long rows = (32 / p.lanes) * K;  // of a group
-  long long groups = THREADS == kGradThreads ? kGradThreads / 32 / p.warps : 1;
-  while (groups > 1 && (groups - 1) * rows >= p.rows) --groups;
+  // As many groups as fit, but no more than give every SM a CTA.
+  const long long most = THREADS == kGradThreads ? kGradThreads / 32 / p.warps : 1;
+  const long long spread = (p.rows + rows * sms - 1) / (rows * sms);
+  const long long groups = spread < 1 ? 1 : spread < most ? spread : most;
   long long grid = (p.rows + groups * rows - 1) / (groups * rows);
   if (grid > sms) grid = sms;
   if (grid > kNormParts) grid = kNormParts;
   if (grid < 1) grid = 1;  // no rows: dw is 0
-  const size_t smem = groups > 1 ? static_cast<size_t>(p.cols) * sizeof(float) : 0;
+  // half of the groups' registers, or one group's: 33 KB at most
+  const long long kept = p.warps > kStagedWarps ? 0 : groups > 1 ? groups / 2 : 1;
+  const size_t smem = p.dw != nullptr ? static_cast<size_t>(kept * p.warps * U * kNormN<T, VEC> * 33) * sizeof(float) : 0;
   const cudaError_t e = launch_overlapped(norm_grad_kernel<T, W, VEC, U, K, THREADS>, static_cast<unsigned>(grid),
                                           static_cast<unsigned>(32 * p.warps * groups), smem, st, p);
   if (e != cudaSuccess || p.dw == nullptr || grid == 1) return e;
