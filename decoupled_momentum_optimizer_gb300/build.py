@@ -7,15 +7,18 @@ generator first, so the constants always come from gen_dct_factors.py.
 """
 
 import concurrent.futures
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_NAME = "libdemo_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+BIND_PATH = os.path.join(HERE, "_bind_ops.so")  # Python's way to the norm, embedding and clipping calls
 SOURCES = ["demo_api.cu", "demo_step.cu", "demo_encode.cu", "demo_decode.cu", "demo_decode_lanes.cu",
            "demo_decode_groups.cu", "demo_dense.cu", "demo_adamw.cu", "train_api.cu", "train_dropout.cu",
            "train_quantize.cu", "train_matmul.cu", "train_linear.cu", "train_norm.cu", "train_norm_grad.cu",
@@ -50,16 +53,47 @@ def _compile(src, build_dir, verbose):
     return obj, r.stderr
 
 
+def _bind(verbose):
+    """Compile and link the extension module against the library and the torch that is installed."""
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    tmp = BIND_PATH + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           os.path.join(CSRC, "bind_ops.cpp"), "-o", tmp, "-L", HERE, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN", "-L", lib,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the extension module did not build:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, BIND_PATH)
+
+
+def _torch():
+    """Whether torch is installed (the library itself does without)."""
+    return importlib.util.find_spec("torch") is not None
+
+
 def build(verbose=False, force=False):
-    """Compile and link the library; returns its path."""
+    """Compile and link the library, and the extension module where torch is installed; returns the library's path."""
     _regen_factors()
     build_dir = os.path.join(os.path.dirname(HERE), "_build")
     os.makedirs(build_dir, exist_ok=True)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "demo.h")]
-    if not force and os.path.exists(LIB_PATH):
-        newest = max(os.path.getmtime(d) for d in deps)
-        if os.path.getmtime(LIB_PATH) >= newest:
-            return LIB_PATH
+    newest = max(os.path.getmtime(d) for d in deps)
+
+    def current(path):
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= newest
+
+    if current(LIB_PATH):
+        if _torch() and not current(BIND_PATH):
+            _bind(verbose)
+        return LIB_PATH
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(lambda s: _compile(s, build_dir, verbose), SOURCES))
     if verbose:
@@ -72,6 +106,8 @@ def build(verbose=False, force=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    if _torch():
+        _bind(verbose)
     return LIB_PATH
 
 

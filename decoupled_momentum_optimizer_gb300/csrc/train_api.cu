@@ -169,16 +169,24 @@ struct EmbedWorkspace {
 // every other place.
 struct Span {
   uintptr_t begin, end;
-  bool written;
 };
-bool apart(Span* spans, int64_t count) {
+// `reads` spans that are read only, then `writes` that are written.  Lists usually come in ascending order, so
+// nothing but two walks is left.
+bool apart(Span* spans, int64_t reads, int64_t writes) {
   const auto before = [](const Span& a, const Span& b) { return a.begin < b.begin; };
-  if (!std::is_sorted(spans, spans + count, before)) std::sort(spans, spans + count, before);
+  Span* const r = spans;
+  Span* const w = spans + reads;
+  if (!std::is_sorted(r, r + reads, before)) std::sort(r, r + reads, before);
+  if (!std::is_sorted(w, w + writes, before)) std::sort(w, w + writes, before);
   uintptr_t read = 0, written = 0;  // the ends of those so far
-  for (int64_t i = 0; i < count; ++i) {
-    if (spans[i].begin < written || (spans[i].written && spans[i].begin < read)) return false;
-    uintptr_t& end = spans[i].written ? written : read;
-    end = std::max(end, spans[i].end);
+  for (int64_t i = 0, j = 0; i < reads || j < writes;) {
+    if (j == writes || (i < reads && r[i].begin < w[j].begin)) {
+      if (r[i].begin < written) return false;
+      read = std::max(read, r[i++].end);
+    } else {
+      if (w[j].begin < written || w[j].begin < read) return false;
+      written = std::max(written, w[j++].end);
+    }
   }
   return true;
 }
@@ -195,10 +203,11 @@ int check_grads(int count, const void* const* g, const int64_t* n, int dtype, vo
   if (!at(norm, 4) || (need > 0 && !at(workspace, 16))) return DEMO_EALIGN;
   const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[2 * static_cast<size_t>(count) + 2]);
   if (spans == nullptr) return DEMO_ENOSPACE;
-  int64_t used = 0;
-  const auto span = [&](const void* p, int64_t bytes, bool written) {
+  int64_t reads = 0, writes = 0;  // reads from the front; writes from the middle on, moved behind the reads below
+  Span* const written = spans.get() + count;
+  const auto span = [](const void* p, int64_t bytes) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    spans[used++] = Span{a, a + static_cast<uintptr_t>(bytes), written};
+    return Span{a, a + static_cast<uintptr_t>(bytes)};
   };
   const int64_t size = elem_size(dtype), osize = elem_size(out_dtype);
   int64_t total = 0;
@@ -211,14 +220,14 @@ int check_grads(int count, const void* const* g, const int64_t* n, int dtype, vo
     if (out != nullptr) {
       if (out[i] == nullptr) return DEMO_EINVAL;
       if (!at(out[i], static_cast<uintptr_t>(osize))) return DEMO_EALIGN;
+      written[writes++] = span(out[i], n[i] * osize);
     }
-    const bool here = out != nullptr && out[i] == g[i] && size == osize;
-    span(g[i], n[i] * size, here);
-    if (out != nullptr && !here) span(out[i], n[i] * osize, true);
+    if (out == nullptr || out[i] != g[i] || size != osize) spans[reads++] = span(g[i], n[i] * size);
   }
-  span(norm, 4, true);
-  if (need > 0) span(workspace, static_cast<int64_t>(need), true);
-  return apart(spans.get(), used) ? DEMO_OK : DEMO_EINVAL;
+  written[writes++] = span(norm, 4);
+  if (need > 0) written[writes++] = span(workspace, static_cast<int64_t>(need));
+  std::copy(written, written + writes, spans.get() + reads);
+  return apart(spans.get(), reads, writes) ? DEMO_OK : DEMO_EINVAL;
 }
 
 // The tensors of one launch, from `from` on; returns the next one's index.

@@ -37,6 +37,36 @@ class _Library:
 
 
 _lib = _Library()
+
+
+class _Bindings:
+    """The extension module's functions (csrc/bind_ops.cpp), bound on first use.  They take the plain calls,
+    several times faster than ctypes does, and answer NotImplemented to all others, which the Python code
+    below each of their calls then takes or refuses."""
+
+    def __getattr__(self, name):
+        import decoupled_momentum_optimizer_gb300 as dm
+
+        dm.lib()
+        try:
+            from decoupled_momentum_optimizer_gb300 import _bind_ops
+        except ImportError as e:
+            raise RuntimeError("the extension module is missing or was built for another torch: build it with "
+                               "python -m decoupled_momentum_optimizer_gb300.build") from e
+        setattr(self, name, getattr(_bind_ops, name))
+        return getattr(self, name)
+
+
+_bind = _Bindings()
+
+
+def _refused(status, name):
+    """Raises for the status that a call of the extension module came back with."""
+    _lib.dm__check(status, name)
+
+
+_FORM_CODES = {None: 0, "rows": 1, "cols": 2, "both": 3}
+_FMT_CODES = {"e4m3": 0, "e5m2": 1}
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -131,6 +161,13 @@ def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
 def _empty(rows, cols, dtype, device):
     """torch.empty, by the form of it that parses its arguments fastest."""
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _made(codes, scales, rows, k):
+    """An Fp8Matrix of buffers that are known to be right."""
+    q = Fp8Matrix.__new__(Fp8Matrix)
+    q.codes, q.scales, q.shape, q.tiles = codes, scales, (rows, k), False
+    return q
 
 
 class Fp8Matrix:
@@ -371,6 +408,17 @@ def rms_norm(x, weight, *, eps=1e-6, residual=None, values=True, form=None, fmt=
     Returns ``Normed(out, quantized, total, rstd)``: ``total`` is ``x`` without a residual, what was not asked
     for is None.
     """
+    if stream is None and quantized is None:
+        r = _bind.rms_norm(x, weight, eps, residual, values, _FORM_CODES.get(form, -1), _FMT_CODES.get(fmt, -1), save, out, total,
+                           rstd)
+        if r.__class__ is tuple:
+            if form is None:
+                return Normed(r[0], None, r[1], r[2])
+            by_rows = _made(r[3], r[4], *x.shape) if form != "cols" else None
+            by_cols = _made(r[5], r[6], x.shape[1], x.shape[0]) if form != "rows" else None
+            return Normed(r[0], (by_rows, by_cols) if form == "both" else by_cols if by_rows is None else by_rows, r[1], r[2])
+        if r is not NotImplemented:
+            _refused(r, "demo_rms_norm")
     if stream is not None:
         return _on_stream(stream, x.device, rms_norm, x, weight, eps=eps, residual=residual, values=values, form=form, fmt=fmt,
                           save=save, out=out, total=total, rstd=rstd, quantized=quantized)
@@ -439,6 +487,12 @@ def rms_norm_grad(dy, total, weight, rstd, *, past=None, out=None, dweight=None,
     and may be ``dy``, ``total`` or ``past`` themselves.  ``dweight`` is float32 [cols], written or (``add``)
     added to; with ``weight_grad=False`` it is left out and None.
     """
+    if stream is None and workspace is None:
+        r = _bind.rms_norm_grad(dy, total, weight, rstd, past, out, dweight, add, weight_grad)
+        if r.__class__ is tuple:
+            return r
+        if r is not NotImplemented:
+            _refused(r, "demo_rms_norm_grad")
     if stream is not None:
         return _on_stream(stream, dy.device, rms_norm_grad, dy, total, weight, rstd, past=past, out=out, dweight=dweight,
                           add=add, weight_grad=weight_grad, workspace=workspace)
@@ -502,6 +556,12 @@ def embedding(tokens, table, *, scale=1.0, dtype=None, out=None, stream=None):
 
     The gradient of the table is :func:`embedding_grad`.
     """
+    if stream is None:
+        r = _bind.embedding(tokens, table, scale, dtype, out)
+        if r.__class__ is int:
+            _refused(r, "demo_embedding")
+        if r is not NotImplemented:
+            return r
     if stream is not None:
         return _on_stream(stream, table.device, embedding, tokens, table, scale=scale, dtype=dtype, out=out)
     kp, size, krows, kcols, ldk = _tokens(tokens)
@@ -529,6 +589,12 @@ def embedding_grad(tokens, dy, vocab=None, *, scale=1.0, out=None, add=False, wo
               ``add`` the sums are added to it, and rows that no token names stay as they are.
     ``workspace``   uint8; allocated through torch where it is not given
     """
+    if stream is None and workspace is None:
+        r = _bind.embedding_grad(tokens, dy, vocab, scale, out, add)
+        if r.__class__ is int:
+            _refused(r, "demo_embedding_grad")
+        if r is not NotImplemented:
+            return r
     if stream is not None:
         return _on_stream(stream, dy.device, embedding_grad, tokens, dy, vocab, scale=scale, out=out, add=add,
                           workspace=workspace)
@@ -600,6 +666,12 @@ def _grad_workspace(count):
 def grad_norm(gs, *, out=None, workspace=None, stream=None):
     """The norm over all elements of a gradient, or of a list of them (one dtype, contiguous), as a float32
     scalar on the device (demo_grad_norm); ``out`` receives it."""
+    if stream is None and workspace is None:
+        r = _bind.grad_norm(gs, out)
+        if r.__class__ is int:
+            _refused(r, "demo_grad_norm")
+        if r is not NotImplemented:
+            return r
     if stream is not None:
         first = gs if isinstance(gs, torch.Tensor) else gs[0]
         return _on_stream(stream, first.device, grad_norm, gs, out=out, workspace=workspace)
@@ -619,6 +691,12 @@ def clip_grads(gs, max_norm, *, norm=None, out=None, workspace=None, stream=None
     ``out``   tensors of the same sizes to write, in the gradients' dtype or float32; in place otherwise
     A norm that is not finite scales nothing.
     """
+    if stream is None and workspace is None:
+        r = _bind.clip_grads(gs, max_norm, norm, out)
+        if r.__class__ is int:
+            _refused(r, "demo_clip_grads")
+        if r is not NotImplemented:
+            return r
     if stream is not None:
         first = gs if isinstance(gs, torch.Tensor) else gs[0]
         return _on_stream(stream, first.device, clip_grads, gs, max_norm, norm=norm, out=out, workspace=workspace)
