@@ -253,7 +253,7 @@ int launch_all_squares(ClipParams* q, int count, const void* const* g, const int
     from = fill_clip(q, from, count, g, n, nullptr, elem_size(dtype));
     if (q->count == 0) break;
     q->parts = parts + *parts_used;
-    *parts_used += clip_parts(*q, sms);
+    *parts_used += clip_parts(*q, dtype, sms);
     const int s = to_status(launch_squares(*q, dtype, sms, st));
     if (s != DEMO_OK) return s;
   }
@@ -586,12 +586,17 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
   }
   // As many tokens at a time as one cluster sorts; the later ones are added.
   int64_t first = 0;
+  t.grad = add ? nullptr : grad;
+  t.cols = cols;
+  t.ldg = q.ldg;
   do {
     const int64_t left = n - first;
     t.n = q.n = static_cast<int>(left < w.batch ? left : w.batch);
     t.first = q.first = first;
-    if (t.n > 0 && (s = to_status(launch_sort_tokens(t, st))) != DEMO_OK) return s;
+    if ((s = to_status(launch_sort_tokens(t, dev.sms, st))) != DEMO_OK) return s;
+    if (t.n == 0) break;  // no tokens: the table is filled, nothing is summed
     if ((s = to_status(launch_embed_grad(q, dtype, st))) != DEMO_OK) return s;
+    t.grad = nullptr;
     q.add = 1;
     first += t.n;
   } while (first < n);

@@ -16,11 +16,15 @@
 // over all of float32's range.
 #include <type_traits>
 
-#include "train_common.cuh"
+#include "train_pairs.cuh"
 
 namespace demo {
 
 constexpr int kClipThreads = 256, kClipUnroll = 8, kClipChunk = kClipThreads * kClipUnroll;  // in 16-byte accesses
+// CTAs an SM: what 64 or 84 registers a thread leave room for (16-bit elements spill with 64).  2^27 elements,
+// the norm: float32 80 us (6.7 TB/s, three CTAs the same), bfloat16 44 us (6.1 TB/s; 71 with four).
+template <typename T>
+constexpr int kClipCtas = sizeof(T) == 4 ? 4 : 3;
 
 template <typename T>
 constexpr int kClipN = 16 / static_cast<int>(sizeof(T));
@@ -76,11 +80,12 @@ struct Chunk {
   }
 };
 
+// Elements 2 i and 2 i + 1 of an access.
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4& x, float (&v)[kClipN<T>]) {
-  const Vec<T, kClipN<T>> q = *reinterpret_cast<const Vec<T, kClipN<T>>*>(&x);
-#pragma unroll
-  for (int e = 0; e < kClipN<T>; ++e) v[e] = to_f32(q.e[e]);
+__device__ __forceinline__ F2 pair_of(const uint4& x, int i) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (sizeof(T) == 2) return widen<T>(w[i]);
+  return f2(__uint_as_float(w[(2 * i) & 3]), __uint_as_float(w[(2 * i + 1) & 3]));
 }
 
 // The sum of a CTA's threads' values, for all of them.
@@ -96,7 +101,7 @@ __device__ __forceinline__ double cta_sum(double v, double* sh) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kClipThreads) squares_kernel(const __grid_constant__ ClipParams p) {
+__global__ void __launch_bounds__(kClipThreads, kClipCtas<T>) squares_kernel(const __grid_constant__ ClipParams p) {
   __shared__ double sh[kClipThreads / 32];
   kernel_begin();
   double total = 0.0;
@@ -104,22 +109,24 @@ __global__ void __launch_bounds__(kClipThreads) squares_kernel(const __grid_cons
     const Chunk<T> chunk(p, c);
     uint4 x[kClipUnroll];
     chunk.load(x);
-    float s[kClipUnroll];
+    F2 s[kClipUnroll];
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) {
-      float v[kClipN<T>];
-      unpack<T>(x[u], v);
-      s[u] = v[0] * v[0];
+      s[u] = f2(0.0f, 0.0f);
 #pragma unroll
-      for (int e = 1; e < kClipN<T>; ++e) s[u] = __fmaf_rn(v[e], v[e], s[u]);
+      for (int i = 0; i < kClipN<T> / 2; ++i) {
+        const F2 v = pair_of<T>(x[u], i);
+        s[u] = fma2(v, v, s[u]);
+      }
     }
 #pragma unroll
     for (int d = 1; d < kClipUnroll; d *= 2)
 #pragma unroll
-      for (int u = 0; u < kClipUnroll; u += 2 * d) s[u] += s[u + d];
+      for (int u = 0; u < kClipUnroll; u += 2 * d) s[u] = add2(s[u], s[u + d]);
+    const float sum = s[0].x + s[0].y;
     // At 2^-90 the squares lost below 2^-149, 64 of them, are 2^-53 of the sum.
-    if (s[0] >= 0x1p-90f && s[0] <= 0x1p120f) {
-      total += static_cast<double>(s[0]);
+    if (sum >= 0x1p-90f && sum <= 0x1p120f) {
+      total += static_cast<double>(sum);
     } else {
       uint32_t any = 0;
 #pragma unroll
@@ -128,10 +135,11 @@ __global__ void __launch_bounds__(kClipThreads) squares_kernel(const __grid_cons
         double t = 0.0;
 #pragma unroll
         for (int u = 0; u < kClipUnroll; ++u) {
-          float v[kClipN<T>];
-          unpack<T>(x[u], v);
 #pragma unroll
-          for (int e = 0; e < kClipN<T>; ++e) t += static_cast<double>(v[e]) * static_cast<double>(v[e]);
+          for (int i = 0; i < kClipN<T> / 2; ++i) {
+            const F2 v = pair_of<T>(x[u], i);
+            t += static_cast<double>(v.x) * v.x + static_cast<double>(v.y) * v.y;
+          }
         }
         total += t;
       }
@@ -155,17 +163,8 @@ __global__ void __launch_bounds__(kClipThreads) norm_kernel_of_parts(const doubl
   if (threadIdx.x == 0) *norm = n;
 }
 
-// g f rounded to O; with f = 1 the element itself, a NaN's payload included, where O is its type.
 template <typename T, typename O>
-__device__ __forceinline__ O scaled(T g, float f) {
-  if constexpr (std::is_same_v<T, O>) {
-    if (f == 1.0f) return g;
-  }
-  return from_f32<O>(to_f32(g) * f);
-}
-
-template <typename T, typename O>
-__global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_constant__ ClipParams p) {
+__global__ void __launch_bounds__(kClipThreads, kClipCtas<T>) scale_kernel(const __grid_constant__ ClipParams p) {
   __shared__ double sh[kClipThreads / 32];
   __shared__ float factor;
   kernel_begin();
@@ -177,6 +176,7 @@ __global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_consta
   }
   __syncthreads();
   const float f = factor;
+  const bool copy = f == 1.0f;  // the elements themselves, a NaN's payload included, where O is their type
   if (f == 1.0f && p.in_place) return;
   // Backwards: what the norm read last is still in L2.
   for (unsigned i = blockIdx.x; i < p.chunks; i += gridDim.x) {
@@ -188,20 +188,34 @@ __global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_consta
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) {
       const long long v = chunk.access(u), i0 = v * kClipN<T> - chunk.off;
-      const Vec<T, kClipN<T>> g = *reinterpret_cast<const Vec<T, kClipN<T>>*>(&x[u]);
       if (chunk.whole(v) && aligned) {
-        constexpr int P = 16 / static_cast<int>(sizeof(O));
+        if constexpr (std::is_same_v<T, float> || !std::is_same_v<T, O>) {
+          float4* to = reinterpret_cast<float4*>(out + i0);
 #pragma unroll
-        for (int k = 0; k < kClipN<T> / P; ++k) {
-          Vec<O, P> q;
+          for (int k = 0; k < kClipN<T> / 4; ++k) {
+            const F2 a = mul2(pair_of<T>(x[u], 2 * k), f2(f, f)), b = mul2(pair_of<T>(x[u], 2 * k + 1), f2(f, f));
+            to[k] = copy && std::is_same_v<T, O> ? *reinterpret_cast<const float4*>(&x[u]) : make_float4(a.x, a.y, b.x, b.y);
+          }
+        } else {
+          uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < P; ++e) q.e[e] = scaled<T, O>(g.e[P * k + e], f);
-          *reinterpret_cast<Vec<O, P>*>(out + i0 + P * k) = q;
+          for (int i = 0; i < 4; ++i) w[i] = narrow<T>(mul2(pair_of<T>(x[u], i), f2(f, f)));
+          *reinterpret_cast<uint4*>(out + i0) = copy ? x[u] : make_uint4(w[0], w[1], w[2], w[3]);
         }
-      } else {
+      } else if (v * kClipN<T> < chunk.end) {
 #pragma unroll
-        for (int e = 0; e < kClipN<T>; ++e)
-          if (i0 + e >= 0 && i0 + e < chunk.end - chunk.off) out[i0 + e] = scaled<T, O>(g.e[e], f);
+        for (int e = 0; e < kClipN<T>; ++e) {
+          if (i0 + e >= 0 && i0 + e < chunk.end - chunk.off) {
+            const F2 g = pair_of<T>(x[u], e / 2);
+            if constexpr (std::is_same_v<T, O>) {
+              if (copy) {
+                out[i0 + e] = chunk.base[chunk.off + i0 + e];
+                continue;
+              }
+            }
+            out[i0 + e] = from_f32<O>((e % 2 ? g.y : g.x) * f);
+          }
+        }
       }
     }
   }
@@ -209,14 +223,15 @@ __global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_consta
 
 namespace {
 
-unsigned clip_grid(unsigned chunks, int sms) {
-  const unsigned most = static_cast<unsigned>(4 * sms < kClipParts ? 4 * sms : kClipParts);
+unsigned clip_grid(unsigned chunks, int dtype, int sms) {
+  const int ctas = sms * (dtype == kF32 ? kClipCtas<float> : kClipCtas<__half>);
+  const unsigned most = static_cast<unsigned>(ctas < kClipParts ? ctas : kClipParts);
   return chunks < most ? chunks : most;
 }
 
 template <typename T, typename O>
 cudaError_t launch_scale_t(const ClipParams& p, int sms, cudaStream_t st) {
-  return launch_overlapped(scale_kernel<T, O>, clip_grid(p.chunks, sms), kClipThreads, 0, st, p);
+  return launch_overlapped(scale_kernel<T, O>, clip_grid(p.chunks, sizeof(T) == 4 ? kF32 : kF16, sms), kClipThreads, 0, st, p);
 }
 
 }  // namespace
@@ -226,11 +241,11 @@ long long clip_chunks(uintptr_t address, long long n, int size) {
   return ((off + n + per - 1) / per + kClipChunk - 1) / kClipChunk;
 }
 
-int clip_parts(const ClipParams& p, int sms) { return static_cast<int>(clip_grid(p.chunks, sms)); }
+int clip_parts(const ClipParams& p, int dtype, int sms) { return static_cast<int>(clip_grid(p.chunks, dtype, sms)); }
 
 cudaError_t launch_squares(const ClipParams& p, int dtype, int sms, cudaStream_t st) {
   auto* kernel = dtype == kF32 ? squares_kernel<float> : dtype == kBF16 ? squares_kernel<__nv_bfloat16> : squares_kernel<__half>;
-  return launch_overlapped(kernel, clip_grid(p.chunks, sms), kClipThreads, 0, st, p);
+  return launch_overlapped(kernel, clip_grid(p.chunks, dtype, sms), kClipThreads, 0, st, p);
 }
 
 cudaError_t launch_norm_of_parts(const double* parts, int count, float* norm, cudaStream_t st) {

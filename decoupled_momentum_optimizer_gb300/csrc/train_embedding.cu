@@ -13,7 +13,7 @@
 // table may take a tenth of all positions: cutting by position, not by token, keeps the warps' work equal.
 #include <cooperative_groups.h>
 
-#include "train_common.cuh"
+#include "train_norm.cuh"
 
 namespace demo {
 
@@ -148,7 +148,8 @@ cudaError_t launch_lookup(const LookupParams& p, int table_dtype, int out_dtype,
 
 // A radix sort, least digit first, within one cluster: CTA r holds a run of positions, a warp a run of
 // those, 32 at a time, so that (CTA, warp, round, lane) is their order.  In each pass a warp counts its
-// digits (lanes with the same digit find each other by match and take consecutive ranks), the warps' counts
+// digits (lanes with the same digit find each other by a ballot for each of its bits and take consecutive
+// ranks; a match instruction takes a step for each different digit: 8 us for 16384 tokens), the warps' counts
 // become offsets within the CTA, the CTAs exchange their totals through distributed shared memory, and every
 // item goes straight to its place in the CTA that will hold it.  Up to 2^16 tokens: 8 CTAs x 1024 threads x 8.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortRounds = 8;
@@ -166,6 +167,35 @@ struct SortShared {
   uint32_t scan[kSortWarps];
 };
 
+// Writes 0 to every row of the table, `part` of `parts`.
+__device__ __forceinline__ void fill_rows(const SortParams& p, long long part, long long parts) {
+  if (p.ldg == p.cols) {  // one run of floats: whole 16-byte accesses, and what is off them at either end
+    float* base = p.grad;
+    const long long total = p.vocab * p.cols, head = (4 - (reinterpret_cast<uintptr_t>(base) / 4 & 3)) & 3;
+    const long long first = head < total ? head : total, units = (total - first) / 4;
+    for (long long u = part * kSortThreads + threadIdx.x; u < units; u += parts * kSortThreads)
+      reinterpret_cast<float4*>(base + first)[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (part == 0) {
+      if (threadIdx.x < first) base[threadIdx.x] = 0.0f;
+      const long long tail = first + 4 * units + threadIdx.x;
+      if (tail < total && threadIdx.x < 4) base[tail] = 0.0f;
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const bool wide = p.cols % 4 == 0 && p.ldg % 4 == 0 && (reinterpret_cast<uintptr_t>(p.grad) & 15) == 0;
+  for (long long r = part * kSortWarps + (threadIdx.x >> 5); r < p.vocab; r += parts * kSortWarps) {
+    float* row = p.grad + r * p.ldg;
+    if (wide) {
+      for (long long c = 4 * lane; c < p.cols; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
+      for (long long c = lane; c < p.cols; c += 32) row[c] = 0.0f;
+    }
+  }
+}
+
+// The first cluster sorts.  Where the table's gradient is written anew, the other SMs fill it with zeros meanwhile
+// (the sums then overwrite the rows that have tokens), which hides the sort behind the fill.
 __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ __align__(16) unsigned char raw[];
   SortShared& sh = *reinterpret_cast<SortShared*>(raw);
@@ -178,6 +208,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __gr
   const int mine = p.n - begin < per_cta ? (p.n > begin ? p.n - begin : 0) : per_cta;
   const int per_warp = (per_cta / 32 + kSortWarps - 1) / kSortWarps * 32;  // at most 32 * kSortRounds
   kernel_begin();
+  if (blockIdx.x >= static_cast<unsigned>(ctas)) {
+    fill_rows(p, blockIdx.x - ctas, gridDim.x - ctas);
+    return;
+  }
   for (int i = tid; i < mine; i += kSortThreads) {
     const long long t = token_at(p.tokens, p.first + begin + i);
     sh.key[0][i] = t >= 0 && t < p.vocab ? static_cast<uint32_t>(t) : static_cast<uint32_t>(p.vocab);  // others last
@@ -197,16 +231,20 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __gr
       const bool live = in_warp < per_warp && i < mine;
       rank[j] = -1;
       const unsigned there = __ballot_sync(0xffffffffu, live);
-      if (live) {
-        key[j] = sh.key[from][i];
-        const uint32_t d = (key[j] >> shift) & (digits - 1);
-        const unsigned same = __match_any_sync(there, d);
-        const int before = __popc(same & ((1u << lane) - 1));
-        rank[j] = count[d] + before;
-        __syncwarp(there);
-        if (before == 0) count[d] = static_cast<uint16_t>(rank[j] + __popc(same));
-        __syncwarp(there);
+      if (there == 0) continue;
+      key[j] = live ? sh.key[from][i] : 0;
+      const uint32_t d = (key[j] >> shift) & (digits - 1);
+      unsigned same = there;
+      for (int b = 0; b < p.bits; ++b) {
+        const bool one = d >> b & 1;
+        const unsigned ones = __ballot_sync(0xffffffffu, one);
+        same &= one ? ones : ~ones;
       }
+      const int before = __popc(same & ((1u << lane) - 1));
+      if (live) rank[j] = count[d] + before;
+      __syncwarp();
+      if (live && before == 0) count[d] = static_cast<uint16_t>(rank[j] + __popc(same));
+      __syncwarp();
     }
     __syncthreads();
     if (tid < digits) {
@@ -222,10 +260,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __gr
     // Where digit d begins: all items of smaller digits, then the earlier CTAs' of d.
     uint32_t before = 0, all = 0;
     if (tid < digits) {
-      for (int r = 0; r < ctas; ++r) {
-        const uint32_t c = cluster.map_shared_rank(sh.total, r)[tid];
-        if (r < me) before += c;
-        all += c;
+      uint32_t c[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) c[r] = r < ctas ? cluster.map_shared_rank(sh.total, r)[tid] : 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r < me) before += c[r];
+        all += c[r];
       }
     }
     uint32_t sum = all;
@@ -275,192 +316,230 @@ cudaError_t prepare_embedding_kernels() {
 // ----------------------------------------------------------------------------
 
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
-constexpr int kAhead = 8;  // rows of dy in flight a warp
+constexpr int kAhead = 4;  // rows of dy, and of the gradient that is added to, in flight a warp
 
-// A lane's columns of one row of dy: eight consecutive ones, or four 32 apart.
-template <typename T, bool VEC>
-struct Slab {
-  static constexpr int N = VEC ? 8 : 4, kCols = 32 * N;
-  __device__ static __forceinline__ int column(int slab, int lane, int e) {
-    return VEC ? slab * kCols + lane * N + e : slab * kCols + 32 * e + lane;
-  }
-  __device__ static __forceinline__ void load(const T* row, int slab, int lane, int cols, float (&v)[N]) {
-    if constexpr (VEC) {
-      const int c = column(slab, lane, 0);
-      if (c < cols) {
-        load_wide<T, N>(row + c, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = 0.0f;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int c = column(slab, lane, e);
-        v[e] = c < cols ? to_f32(row[c]) : 0.0f;
-      }
-    }
-  }
-};
+// A warp's columns of a row: eight a lane as 16-byte accesses, or four a lane 32 apart.
+template <bool VEC>
+constexpr int kSlabN = VEC ? 8 : 4;
 
-// Adds scale * v to, or writes it to, a row of the gradient (16-byte accesses where VEC).
 template <bool VEC, int N>
-__device__ __forceinline__ void put_row(float* row, int slab, int lane, int cols, bool add, float scale, const float (&v)[N]) {
+__device__ __forceinline__ void put_row(float* row, const Place& at, const F2 (&v)[N / 2]) {
   if constexpr (VEC) {
-    const int c = slab * 32 * N + lane * N;
-    if (c >= cols) return;
-    float o[N];
-    if (add) load_wide<float, N>(row + c, o);
+    if (at.reach > 0) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = add ? o[e] + v[e] * scale : v[e] * scale;
-    store_wide<float, N>(row + c, o);
+      for (int i = 0; i < N / 4; ++i)
+        reinterpret_cast<float4*>(row)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int c = slab * 32 * N + 32 * e + lane;
-      if (c < cols) row[c] = add ? row[c] + v[e] * scale : v[e] * scale;
-    }
+    for (int e = 0; e < N; ++e)
+      if (at.has<VEC, N>(0, e)) row[32 * e] = e % 2 ? v[e / 2].y : v[e / 2].x;
   }
 }
 
-// Parts of tokens that cross pieces: [piece][0: goes on from the piece before, 1: starts here][padded columns].
+// Parts of tokens that cross pieces: [piece][0: goes on from the piece before, 1: starts here][padded columns],
+// a lane's N side by side.
 template <int N>
 __device__ __forceinline__ float* part_of(const EmbedGradParams& p, long long piece, int which, int slab, int lane) {
   return p.parts + (2 * piece + which) * p.ldparts + static_cast<long long>(slab) * 32 * N + lane * N;
 }
-
-// The first of `zero_blocks` blocks write the rows of the table that no token names; the others sum.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_constant__ EmbedGradParams p) {
-  using S = Slab<T, VEC>;
-  constexpr int N = S::N;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cols = static_cast<int>(p.cols);
-  kernel_begin();
-  if (blockIdx.x < p.zero_blocks) {
-    // 32 rows a warp: each lane looks its row up in the sorted keys, then the warp writes the absent ones.
-    const long long r0 = (static_cast<long long>(blockIdx.x) * kSumWarps + warp) * 32, r = r0 + lane;
-    int lo = 0, hi = p.n;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (p.keys[mid] < r)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    unsigned absent = __ballot_sync(0xffffffffu, r < p.vocab && !(lo < p.n && p.keys[lo] == r));
-    while (absent != 0) {
-      const int i = __ffs(static_cast<int>(absent)) - 1;
-      absent &= absent - 1;
-      float* row = p.grad + (r0 + i) * p.ldg;
-      if constexpr (VEC) {
-        for (int c = 4 * lane; c < cols; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      } else {
-        for (int c = lane; c < cols; c += 32) row[c] = 0.0f;
-      }
-    }
-    return;
-  }
-  const long long item = static_cast<long long>(blockIdx.x - p.zero_blocks) * kSumWarps + warp;
-  const int piece = static_cast<int>(item / p.slabs), slab = static_cast<int>(item - static_cast<long long>(piece) * p.slabs);
-  const int at = piece * p.piece;
-  if (at >= p.n) return;
-  const int here = p.n - at < p.piece ? p.n - at : p.piece;  // at most 32
-  const int key = lane < here ? p.keys[at + lane] : -1;
-  const int pos = lane < here ? p.positions[at + lane] : 0;
-  const int before = at > 0 ? p.keys[at - 1] : -1, after = at + here < p.n ? p.keys[at + here] : -1;
-  const T* dy = static_cast<const T*>(p.dy);
-  float sum[N];
+template <int N>
+__device__ __forceinline__ void add_part(const float4 (&v)[N / 4], F2 (&sum)[N / 2]) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) sum[e] = 0.0f;
-  const int vocab = static_cast<int>(p.vocab);
-  bool whole = __shfl_sync(0xffffffffu, key, 0) != before;  // the token's rows began in this piece
-  for (int i0 = 0; i0 < here; i0 += kAhead) {
-    float v[kAhead][N];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = __shfl_sync(0xffffffffu, key, i0 + j);
-      const long long q = __shfl_sync(0xffffffffu, pos, i0 + j);
-      if (i0 + j < here && k < vocab) S::load(dy + (p.first + q) * p.lddy, slab, lane, cols, v[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = __shfl_sync(0xffffffffu, key, i0 + j);
-      const int next = __shfl_sync(0xffffffffu, key, (i0 + j + 1) & 31);
-      if (i0 + j < here && k < vocab) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) sum[e] += v[j][e];
-        const bool end_of_piece = i0 + j + 1 == here;
-        if (!end_of_piece && next == k) continue;
-        const bool goes_on = end_of_piece && after == k;
-        if (whole && !goes_on) {
-          put_row<VEC, N>(p.grad + static_cast<long long>(k) * p.ldg, slab, lane, cols, p.add != 0, p.scale, sum);
-        } else {
-          float* part = part_of<N>(p, piece, whole ? 1 : 0, slab, lane);
-#pragma unroll
-          for (int e = 0; e < N; e += 4) *reinterpret_cast<float4*>(part + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-        }
-        whole = true;
-#pragma unroll
-        for (int e = 0; e < N; ++e) sum[e] = 0.0f;
-      }
-    }
+  for (int i = 0; i < N / 4; ++i) {
+    sum[2 * i] = add2(sum[2 * i], f2(v[i].x, v[i].y));
+    sum[2 * i + 1] = add2(sum[2 * i + 1], f2(v[i].z, v[i].w));
   }
 }
+template <int N>
+__device__ __forceinline__ void read_part(const float* part, float4 (&v)[N / 4]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) v[i] = reinterpret_cast<const float4*>(part)[i];
+}
 
-// A token that starts in a piece and goes on: its part there, then the following pieces', in their order.
-template <bool VEC>
-__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const __grid_constant__ EmbedGradParams p) {
-  constexpr int N = VEC ? 8 : 4;
+// scale * sum, added to what the row holds if asked.
+template <bool VEC, int N>
+__device__ __forceinline__ void finish_row(const EmbedGradParams& p, long long token, const Place& at, F2 (&sum)[N / 2]) {
+  float* row = p.grad + token * p.ldg + at.first;
+  Unit<float, VEC, N> old;
+  if (p.add) old.load(row, at, 0);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    sum[i] = mul2(sum[i], f2(p.scale, p.scale));
+    if (p.add) sum[i] = add2(old.get2(i), sum[i]);
+  }
+  put_row<VEC, N>(row, at, sum);
+}
+
+enum : int { kEnds = 1 << 16, kFinal = 1 << 17, kStarts = 1 << 18, kLive = 1 << 19 };
+
+// A warp sums one piece over one slab of columns.  What becomes of an entry follows from its key and those around
+// the piece, so every row that a batch needs is asked for at once: the rows of dy, and those of the gradient
+// that a token's sum is added to.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kSumThreads, 2) embed_sum_kernel(const __grid_constant__ EmbedGradParams p) {
+  constexpr int N = kSlabN<VEC>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   kernel_begin();
   const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + warp;
   const int piece = static_cast<int>(item / p.slabs), slab = static_cast<int>(item - static_cast<long long>(piece) * p.slabs);
-  const int at = piece * p.piece, end = at + p.piece;
-  if (end >= p.n) return;  // the last piece goes nowhere
-  const int key = p.keys[end - 1];
-  if (key >= p.vocab || p.keys[end] != key) return;
-  if (at > 0 && p.keys[at - 1] == key) return;  // a later part, joined from where the token starts
-  // Pieces that the token reaches: 32 piece ends at a time.
-  int last = piece + 1;
-  for (;;) {
-    const int q = last + lane, e = (q + 1) * p.piece;  // does the token fill piece q and go on?
-    const unsigned on = __ballot_sync(0xffffffffu, e < p.n && p.keys[e] == key);
-    const int run = on == 0xffffffffu ? 32 : __ffs(static_cast<int>(~on)) - 1;
-    last += run;
-    if (run < 32) break;
+  const int begin = piece * p.piece;
+  if (begin >= p.n) return;
+  const Place at = Place::of<VEC, N>(slab, 1, lane, 32, static_cast<int>(p.cols));
+  const int here = p.n - begin < p.piece ? p.n - begin : p.piece;  // at most 32
+  const int key = lane < here ? p.keys[begin + lane] : -1;
+  int info = lane < here ? p.positions[begin + lane] : 0;
+  {
+    const int before = begin > 0 ? p.keys[begin - 1] : -1, after = begin + here < p.n ? p.keys[begin + here] : -1;
+    const int next = __shfl_down_sync(0xffffffffu, key, 1);
+    if (lane < here && key < p.vocab) {
+      info |= kLive;
+      const bool ends = lane == here - 1 || next != key;
+      if (key != before) info |= kStarts;
+      if (ends) info |= kEnds;
+      if (ends && key != before && key != after) info |= kFinal;
+    }
   }
-  float sum[N];
-  load_wide<float, N>(part_of<N>(p, piece, 1, slab, lane), sum);
-  for (int q0 = piece + 1; q0 <= last; q0 += kAhead) {
-    float v[kAhead][N];
+  const T* dy = static_cast<const T*>(p.dy) + at.first;
+  F2 sum[N / 2];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (q0 + j <= last) load_wide<float, N>(part_of<N>(p, q0 + j, 0, slab, lane), v[j]);
+  for (int i = 0; i < N / 2; ++i) sum[i] = f2(0.0f, 0.0f);
+  for (int i0 = 0; i0 < here; i0 += kAhead) {
+    Unit<T, VEC, N> v[kAhead];
+    Unit<float, VEC, N> old[kAhead];
+    int what[kAhead];
+    float* row[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (q0 + j <= last) {
+      what[j] = __shfl_sync(0xffffffffu, info, i0 + j);
+      row[j] = p.grad + static_cast<long long>(__shfl_sync(0xffffffffu, key, i0 + j)) * p.ldg + at.first;
+      if (what[j] & kLive) v[j].load(dy + (p.first + (what[j] & 0xffff)) * p.lddy, at, 0);
+    }
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum[e] += v[j][e];
+    for (int j = 0; j < kAhead; ++j)
+      if (p.add && (what[j] & kFinal)) old[j].load(row[j], at, 0);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (!(what[j] & kLive)) continue;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) sum[i] = add2(sum[i], v[j].get2(i));
+      if (!(what[j] & kEnds)) continue;
+      if (what[j] & kFinal) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          sum[i] = mul2(sum[i], f2(p.scale, p.scale));
+          if (p.add) sum[i] = add2(old[j].get2(i), sum[i]);
+        }
+        put_row<VEC, N>(row[j], at, sum);
+      } else {
+        float4* part = reinterpret_cast<float4*>(part_of<N>(p, piece, what[j] & kStarts ? 1 : 0, slab, lane));
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) part[i] = make_float4(sum[2 * i].x, sum[2 * i].y, sum[2 * i + 1].x, sum[2 * i + 1].y);
+      }
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) sum[i] = f2(0.0f, 0.0f);
+    }
+  }
+}
+
+// A token that starts in a piece and goes on: its part there, then the following pieces', in their order.  A
+// warp finds where a piece's last token ends; few parts it adds alone, of many every warp of the CTA takes
+// every sixteenth (one token in 5461 of 16384 positions took 68 us with one warp).
+constexpr int kJoinWarps = 16, kAlone = 16;
+constexpr int kJoinAhead = 4;
+
+template <bool VEC>
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const __grid_constant__ EmbedGradParams p) {
+  constexpr int N = kSlabN<VEC>;
+  __shared__ __align__(16) float sums[kJoinWarps][32 * N];
+  __shared__ int2 run[kJoinWarps];  // token and last piece of a long run
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  kernel_begin();
+  const int group = static_cast<int>(blockIdx.x / p.slabs), slab = static_cast<int>(blockIdx.x - static_cast<unsigned>(group) * p.slabs);
+  const Place at = Place::of<VEC, N>(slab, 1, lane, 32, static_cast<int>(p.cols));
+  // Parts q0, q0 + step, ... of a token, up to the last.
+  const auto add_parts = [&](int q0, int step, int last, F2(&sum)[N / 2]) {
+    for (int q = q0; q <= last; q += kJoinAhead * step) {
+      float4 v[kJoinAhead][N / 4];
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j)
+        if (q + j * step <= last) read_part<N>(part_of<N>(p, q + j * step, 0, slab, lane), v[j]);
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j)
+        if (q + j * step <= last) add_part<N>(v[j], sum);
+    }
+  };
+  const int mine = group * kJoinWarps + warp, begin = mine * p.piece, end = begin + p.piece;
+  int last = -1, key = -1;
+  if (end < p.n) {  // the last piece goes nowhere
+    key = p.keys[end - 1];
+    // A token outside the table has no sum; one that began before is joined from where it did.
+    if (key < p.vocab && p.keys[end] == key && (begin == 0 || p.keys[begin - 1] != key)) {
+      last = mine + 1;
+      for (;;) {  // pieces that the token reaches, 32 piece ends at a time
+        const int e = (last + lane + 1) * p.piece;  // does the token fill this piece and go on?
+        const unsigned on = __ballot_sync(0xffffffffu, e < p.n && p.keys[e] == key);
+        const int filled = on == 0xffffffffu ? 32 : __ffs(static_cast<int>(~on)) - 1;
+        last += filled;
+        if (filled < 32) break;
       }
     }
   }
-  put_row<VEC, N>(p.grad + static_cast<long long>(key) * p.ldg, slab, lane, static_cast<int>(p.cols), p.add != 0, p.scale, sum);
+  const bool alone = last >= 0 && last - mine <= kAlone;
+  if (lane == 0) run[warp] = alone ? make_int2(-1, -1) : make_int2(key, last);
+  if (alone) {
+    F2 sum[N / 2];
+    float4 v[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) sum[i] = f2(0.0f, 0.0f);
+    read_part<N>(part_of<N>(p, mine, 1, slab, lane), v);
+    add_part<N>(v, sum);
+    add_parts(mine + 1, 1, last, sum);
+    finish_row<VEC, N>(p, key, at, sum);
+  }
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (run[w].y < 0) continue;  // the same for the CTA
+    const int from = group * kJoinWarps + w;
+    F2 sum[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) sum[i] = f2(0.0f, 0.0f);
+    if (warp == 0) {
+      float4 v[N / 4];
+      read_part<N>(part_of<N>(p, from, 1, slab, lane), v);
+      add_part<N>(v, sum);
+    }
+    add_parts(from + 1 + warp, kJoinWarps, run[w].y, sum);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<float4*>(&sums[warp][lane * N])[i] = make_float4(sum[2 * i].x, sum[2 * i].y, sum[2 * i + 1].x, sum[2 * i + 1].y);
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int k = 1; k < kJoinWarps; ++k) {
+        float4 v[N / 4];
+        read_part<N>(&sums[k][lane * N], v);
+        add_part<N>(v, sum);
+      }
+      finish_row<VEC, N>(p, run[w].x, at, sum);
+    }
+    __syncthreads();
+  }
 }
 
 namespace {
 
 template <typename T, bool VEC>
 cudaError_t launch_sums(EmbedGradParams& p, cudaStream_t st) {
-  constexpr int cols = Slab<T, VEC>::kCols;
+  constexpr int cols = 32 * kSlabN<VEC>;
   p.slabs = static_cast<int>((p.cols + cols - 1) / cols);
   p.ldparts = static_cast<long long>(p.slabs) * cols;
   const long long pieces = (p.n + p.piece - 1) / p.piece, items = pieces * p.slabs;
-  const unsigned blocks = static_cast<unsigned>((items + kSumWarps - 1) / kSumWarps);
-  p.zero_blocks = p.add ? 0 : static_cast<unsigned>((p.vocab + 32 * kSumWarps - 1) / (32 * kSumWarps));
-  cudaError_t e = launch_overlapped(embed_sum_kernel<T, VEC>, p.zero_blocks + blocks, kSumThreads, 0, st, p);
+  const cudaError_t e = launch_overlapped(embed_sum_kernel<T, VEC>, static_cast<unsigned>((items + kSumWarps - 1) / kSumWarps),
+                                          kSumThreads, 0, st, p);
   if (e != cudaSuccess || pieces <= 1) return e;
-  return launch_overlapped(embed_join_kernel<VEC>, blocks, kSumThreads, 0, st, p);
+  return launch_overlapped(embed_join_kernel<VEC>, static_cast<unsigned>((pieces + kJoinWarps - 1) / kJoinWarps * p.slabs),
+                           32 * kJoinWarps, 0, st, p);
 }
 
 template <typename T>
@@ -474,7 +553,7 @@ cudaError_t launch_sums_t(EmbedGradParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_sort_tokens(const SortParams& p, cudaStream_t st) {
+cudaError_t launch_sort_tokens(const SortParams& p, int sms, cudaStream_t st) {
   SortParams q = p;
   int bits = 1;
   while ((p.vocab >> bits) != 0) ++bits;  // vocab itself is the key of tokens outside the table
@@ -482,7 +561,14 @@ cudaError_t launch_sort_tokens(const SortParams& p, cudaStream_t st) {
   q.bits = (bits + q.passes - 1) / q.passes;
   const int ctas = p.n <= kSortThreads ? 1 : p.n <= 2 * kSortThreads ? 2 : p.n <= 4 * kSortThreads ? 4 : 8;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  // Three quarters of the SMs fill (clusters of eight do not fit on all of them at one time), 64 KB each at least.
+  long long fill = 0;
+  if (p.grad != nullptr) {
+    const long long worth = (p.vocab * p.cols + 16383) / 16384, most = sms * 3 / 4 / ctas - 1;
+    fill = (worth + ctas - 1) / ctas;
+    fill = fill < 1 || most < 1 ? 1 : fill < most ? fill : most;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas * (1 + fill)));
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = sizeof(SortShared);
   cfg.stream = st;

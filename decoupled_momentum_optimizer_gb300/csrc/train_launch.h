@@ -124,8 +124,10 @@ struct SortParams {
   int n, passes, bits;     // passes over digits of `bits`: set by the launcher
   int* keys;               // [n] sorted; vocab stands for tokens outside the table
   unsigned short* positions;  // [n], from the first token on
+  float* grad;                // not NULL: the table's gradient, filled with zeros meanwhile
+  long long cols, ldg;
 };
-cudaError_t launch_sort_tokens(const SortParams& p, cudaStream_t st);
+cudaError_t launch_sort_tokens(const SortParams& p, int sms, cudaStream_t st);
 struct EmbedGradParams {
   const int* keys;
   const unsigned short* positions;
@@ -134,7 +136,6 @@ struct EmbedGradParams {
   float* parts;  // [pieces][2][ldparts]
   long long first, vocab, cols, lddy, ldg, ldparts;
   int n, piece, slabs, add;  // piece: 8, 16 or 32
-  unsigned int zero_blocks;
   float scale;
 };
 cudaError_t launch_embed_grad(EmbedGradParams& p, int dtype, cudaStream_t st);
@@ -166,7 +167,7 @@ struct ClipParams {
   float* norm;
 };
 long long clip_chunks(uintptr_t address, long long n, int size);  // chunks of a tensor
-int clip_parts(const ClipParams& p, int sms);                     // CTAs of its launch
+int clip_parts(const ClipParams& p, int dtype, int sms);                    // CTAs of its launch
 cudaError_t launch_squares(const ClipParams& p, int dtype, int sms, cudaStream_t st);
 cudaError_t launch_norm_of_parts(const double* parts, int count, float* norm, cudaStream_t st);
 cudaError_t launch_scale(const ClipParams& p, int dtype, int out_dtype, int sms, cudaStream_t st);
