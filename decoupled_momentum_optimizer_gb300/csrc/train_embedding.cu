@@ -159,8 +159,7 @@ static_assert(kMaxSorted <= 65536, "positions are 16 bits");
 static_assert(kDigits <= kSortThreads, "a thread for each digit");
 
 struct SortShared {
-  uint32_t key[2][kSortThreads * kSortRounds];
-  uint16_t pos[2][kSortThreads * kSortRounds];
+  uint64_t item[2][kSortThreads * kSortRounds];  // token << 16 | position
   uint16_t count[kSortWarps][kDigits];  // of a warp's items, then the warps' before it
   uint32_t total[kDigits];              // of the CTA
   uint32_t base[kDigits];               // where the CTA's items of a digit begin
@@ -214,15 +213,14 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __gr
   }
   for (int i = tid; i < mine; i += kSortThreads) {
     const long long t = token_at(p.tokens, p.first + begin + i);
-    sh.key[0][i] = t >= 0 && t < p.vocab ? static_cast<uint32_t>(t) : static_cast<uint32_t>(p.vocab);  // others last
-    sh.pos[0][i] = static_cast<uint16_t>(begin + i);
+    sh.item[0][i] = static_cast<uint64_t>(t >= 0 && t < p.vocab ? t : p.vocab) << 16 | (begin + i);  // others last
   }
   int from = 0;
   for (int pass = 0; pass < p.passes; ++pass, from ^= 1) {
-    const int shift = pass * p.bits, digits = 1 << p.bits;
+    const int shift = 16 + pass * p.bits, digits = 1 << p.bits;
     for (int i = tid; i < kSortWarps * kDigits / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(sh.count)[i] = 0;
     __syncthreads();  // counts cleared; and, in the first pass, the items are there
-    uint32_t key[kSortRounds];
+    uint64_t item[kSortRounds];
     int rank[kSortRounds];
     uint16_t* count = sh.count[warp];
 #pragma unroll
@@ -232,8 +230,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __gr
       rank[j] = -1;
       const unsigned there = __ballot_sync(0xffffffffu, live);
       if (there == 0) continue;
-      key[j] = live ? sh.key[from][i] : 0;
-      const uint32_t d = (key[j] >> shift) & (digits - 1);
+      item[j] = live ? sh.item[from][i] : 0;
+      const uint32_t d = static_cast<uint32_t>(item[j] >> shift) & (digits - 1);
       unsigned same = there;
       for (int b = 0; b < p.bits; ++b) {
         const bool one = d >> b & 1;
@@ -248,11 +246,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __gr
     }
     __syncthreads();
     if (tid < digits) {
-      uint32_t sum = 0;
+      uint32_t c[kSortWarps], sum = 0;  // all read before any is written
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[w] = sh.count[w][tid];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = sh.count[w][tid];
         sh.count[w][tid] = static_cast<uint16_t>(sum);
-        sum += c;
+        sum += c[w];
       }
       sh.total[tid] = sum;
     }
@@ -292,18 +292,18 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __gr
 #pragma unroll
     for (int j = 0; j < kSortRounds; ++j) {
       if (rank[j] >= 0) {
-        const uint32_t d = (key[j] >> shift) & (digits - 1);
+        const uint32_t d = static_cast<uint32_t>(item[j] >> shift) & (digits - 1);
         const uint32_t to = sh.base[d] + sh.count[warp][d] + static_cast<uint32_t>(rank[j]);
         const uint32_t r = to / static_cast<uint32_t>(per_cta), i = to - r * static_cast<uint32_t>(per_cta);
-        cluster.map_shared_rank(sh.key[from ^ 1], r)[i] = key[j];
-        cluster.map_shared_rank(sh.pos[from ^ 1], r)[i] = sh.pos[from][warp * per_warp + 32 * j + lane];
+        cluster.map_shared_rank(sh.item[from ^ 1], r)[i] = item[j];
       }
     }
     cluster.sync();  // every item has arrived, and nobody reads this CTA's totals any more
   }
   for (int i = tid; i < mine; i += kSortThreads) {
-    p.keys[begin + i] = static_cast<int>(sh.key[from][i]);
-    p.positions[begin + i] = sh.pos[from][i];
+    const uint64_t v = sh.item[from][i];
+    p.keys[begin + i] = static_cast<int>(v >> 16);
+    p.positions[begin + i] = static_cast<unsigned short>(v);
   }
 }
 
@@ -315,7 +315,7 @@ cudaError_t prepare_embedding_kernels() {
 // Sums over equal tokens
 // ----------------------------------------------------------------------------
 
-constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+constexpr int kSumThreads = 128, kSumWarps = kSumThreads / 32;
 constexpr int kAhead = 4;  // rows of dy, and of the gradient that is added to, in flight a warp
 
 // A warp's columns of a row: eight a lane as 16-byte accesses, or four a lane 32 apart.
@@ -377,7 +377,7 @@ enum : int { kEnds = 1 << 16, kFinal = 1 << 17, kStarts = 1 << 18, kLive = 1 << 
 // the piece, so every row that a batch needs is asked for at once: the rows of dy, and those of the gradient
 // that a token's sum is added to.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kSumThreads, 2) embed_sum_kernel(const __grid_constant__ EmbedGradParams p) {
+__global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_constant__ EmbedGradParams p) {
   constexpr int N = kSlabN<VEC>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   kernel_begin();
@@ -559,7 +559,11 @@ cudaError_t launch_sort_tokens(const SortParams& p, int sms, cudaStream_t st) {
   while ((p.vocab >> bits) != 0) ++bits;  // vocab itself is the key of tokens outside the table
   q.passes = (bits + kDigitBits - 1) / kDigitBits;
   q.bits = (bits + q.passes - 1) / q.passes;
-  const int ctas = p.n <= kSortThreads ? 1 : p.n <= 2 * kSortThreads ? 2 : p.n <= 4 * kSortThreads ? 4 : 8;
+  // As few CTAs as hold the tokens where a long fill hides the sort (its clusters are small then, and fit on every
+  // SM: 822 MB and 16384 tokens 165 us, with eight CTAs 177); else two rounds of 32 a warp (13 us; eight rounds 22).
+  const long long table = p.grad != nullptr ? p.vocab * p.cols * 4 : 0;
+  const int each = kSortThreads * (table > (32 << 20) ? kSortRounds : 2);
+  const int ctas = p.n <= each ? 1 : p.n <= 2 * each ? 2 : p.n <= 4 * each ? 4 : 8;
   cudaLaunchConfig_t cfg = {};
   // Three quarters of the SMs fill (clusters of eight do not fit on all of them at one time), 64 KB each at least.
   long long fill = 0;

@@ -141,12 +141,13 @@ struct EmbedGradParams {
 cudaError_t launch_embed_grad(EmbedGradParams& p, int dtype, cudaStream_t st);
 cudaError_t prepare_embedding_kernels();
 
-// Sorted positions of a piece (one warp's work on 256 columns): 32, or fewer where those would leave most
-// SMs without sixteen warps.
+// Sorted positions of a piece (one warp's work on 256 columns): 32, or fewer where those would leave an SM fewer
+// than three warps.  Sums and join, bfloat16 dy, us with 8 / 16 / 32 positions: 16384 x 2048 48 / 43 / 39, 4096 x
+// 768 10.3 / 10.8 / 11.7, 128 x 768 7.2 / 9.2 / 12.7; three tokens, 16384 x 32, 19 / 15 / 14.
 constexpr int embed_piece(long long n, long long cols) {
   const long long slabs = (cols + 255) / 256;
   int piece = 32;
-  while (piece > 8 && (n + piece - 1) / piece * slabs < 152 * 16) piece /= 2;
+  while (piece > 8 && (n + piece - 1) / piece * slabs < 152 * 3) piece /= 2;
   return piece;
 }
 
