@@ -29,6 +29,17 @@ __device__ __forceinline__ float max_abs_nan(float m, float a, float b) {
   return r;
 }
 
+// The same passing over a NaN.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+
+// ----------------------------------------------------------------------------
+// 16-bit elements
+// ----------------------------------------------------------------------------
+
 // Two 16-bit elements in a word, the first in its low half.
 template <typename T>
 __device__ __forceinline__ F2 widen(uint32_t w) {

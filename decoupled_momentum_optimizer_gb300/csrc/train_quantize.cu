@@ -25,7 +25,7 @@
 // hash).  Nothing is saturated there: the integer and compare pipe is 65% busy (17 of 32 instructions an
 // element), issue slots 61%, HBM 33%; a tile is loaded, computed and stored in turn, and only the SM's
 // other CTA overlaps that.
-#include "train_common.cuh"
+#include "train_pairs.cuh"
 
 namespace demo {
 
@@ -111,8 +111,17 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const float r = i < live_rows ? p.rstd[r0 + i] : 0.0f;
+      const F2 r2 = f2(r, r), a = mul2(mul2(f2(v[i][0], v[i][1]), r2), f2(w[0], w[1])),
+               b = mul2(mul2(f2(v[i][2], v[i][3]), r2), f2(w[2], w[3]));
+      v[i][0] = a.x;
+      v[i][1] = a.y;
+      v[i][2] = b.x;
+      v[i][3] = b.y;
+      if (!whole) {  // 0 past the matrix, whatever a factor is
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] = i < live_rows && e < live_cols ? v[i][e] * r * w[e] : 0.0f;
+        for (int e = 0; e < 4; ++e)
+          if (i >= live_rows || e >= live_cols) v[i][e] = 0.0f;
+      }
     }
   }
   if (p.relu) {
@@ -133,27 +142,23 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid
       for (int e = 0; e < 4; ++e) v[i][e] = keep[e] ? v[i][e] * d.scale : 0.0f;
     }
   }
-  {
-    float odd = 0.0f;  // NaN once an element is infinite or NaN
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) odd = fmaf(v[i][e], 0.0f, odd);
-    if (__any_sync(0xffffffffu, odd != odd)) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[i][e] = finite_or_nan(v[i][e]);
-    }
-  }
 
   constexpr int top = fmt_top(FMT);
-  // Float bits of non-negative values order as unsigned integers.  (fmaxf passes over a NaN.)
-  uint32_t rowbits[kPer];
+  // Float bits of non-negative values order as unsigned integers, infinity and NaN above all others.
+  uint32_t rowbits[kPer], most = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    rowbits[i] = __float_as_uint(
-        fmaxf(fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3]))), 0.0f));
+  for (int i = 0; i < kPer; ++i) {
+    rowbits[i] = __float_as_uint(max_abs_nan(max_abs_nan(0.0f, v[i][0], v[i][1]), v[i][2], v[i][3]));
+    most = umax32(most, rowbits[i]);
+  }
+  if (__any_sync(0xffffffffu, most >= 0x7f800000u)) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = finite_or_nan(v[i][e]);
+      rowbits[i] = __float_as_uint(max_abs(max_abs(0.0f, v[i][0], v[i][1]), v[i][2], v[i][3]));
+    }
+  }
   int tile_e = 0;
   if (p.tiles) {
     uint32_t m = 0;
@@ -184,7 +189,8 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const float inv = __shfl_sync(0xffffffffu, inverse, i);
-      if (i < live_rows) *reinterpret_cast<uint32_t*>(dst) = codes4<FMT>(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+      const F2 a = mul2(f2(v[i][0], v[i][1]), f2(inv, inv)), b = mul2(f2(v[i][2], v[i][3]), f2(inv, inv));
+      if (i < live_rows) *reinterpret_cast<uint32_t*>(dst) = codes4<FMT>(a.x, a.y, b.x, b.y);
       dst += kp;
     }
     // rows past the matrix up to the scales' stride hold 1
@@ -196,11 +202,11 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid
     float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (!p.tiles) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        m.x = fmaxf(m.x, fabsf(v[i][0]));
-        m.y = fmaxf(m.y, fabsf(v[i][1]));
-        m.z = fmaxf(m.z, fabsf(v[i][2]));
-        m.w = fmaxf(m.w, fabsf(v[i][3]));
+      for (int i = 0; i < kPer; i += 2) {
+        m.x = max_abs(m.x, v[i][0], v[i + 1][0]);
+        m.y = max_abs(m.y, v[i][1], v[i + 1][1]);
+        m.z = max_abs(m.z, v[i][2], v[i + 1][2]);
+        m.w = max_abs(m.w, v[i][3], v[i + 1][3]);
       }
     }
     *reinterpret_cast<float4*>(&sh.colmax[warp][4 * lane]) = m;
@@ -217,14 +223,20 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quantize_kernel(const __grid
     }
     __syncthreads();
     const float4 q4 = *reinterpret_cast<const float4*>(&sh.colinv[4 * lane]);
-    const float inv[4] = {q4.x, q4.y, q4.z, q4.w};
+    // The products two columns at a time: their registers are those of the rows.
+    F2 lo[kPer], hi[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      lo[i] = mul2(f2(v[i][0], v[i][1]), f2(q4.x, q4.y));
+      hi[i] = mul2(f2(v[i][2], v[i][3]), f2(q4.z, q4.w));
+    }
+    const auto at = [&](int i, int e) { return e == 0 ? lo[i].x : e == 1 ? lo[i].y : e == 2 ? hi[i].x : hi[i].y; };
     // Column 4 l + e, unit `warp` (its rows 8 w ..): stored at unit w ^ (l & 15), so that the sixteen
     // lanes of an 8-byte store phase reach different banks.
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       sh.codes[(4 * lane + e) * kQuantWarps + (warp ^ (lane & 15))] =
-          make_uint2(codes4<FMT>(v[0][e] * inv[e], v[1][e] * inv[e], v[2][e] * inv[e], v[3][e] * inv[e]),
-                     codes4<FMT>(v[4][e] * inv[e], v[5][e] * inv[e], v[6][e] * inv[e], v[7][e] * inv[e]));
+          make_uint2(codes4<FMT>(at(0, e), at(1, e), at(2, e), at(3, e)), codes4<FMT>(at(4, e), at(5, e), at(6, e), at(7, e)));
     __syncthreads();
     const long long rp = static_cast<long long>(p.row_blocks) * kBlock;
     const long long col0 = static_cast<long long>(tile_c) * kBlock;
