@@ -124,6 +124,11 @@ PyObject* none() {
   Py_INCREF(Py_None);
   return Py_None;
 }
+PyObject* whole_number(int64_t v) {
+  PyObject* o = PyLong_FromLongLong(v);
+  if (o == nullptr) throw Other();
+  return o;
+}
 PyObject* wrap_or_none(const at::Tensor& t) {
   if (!t.defined()) return none();
   PyObject* o = THPVariable_Wrap(t);
@@ -187,7 +192,7 @@ PyObject* plain(Py_ssize_t n, Py_ssize_t want, F body) {
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // (x, weight, eps, residual, values, form, fmt, save, out, total, rstd) with form 0 none, 1 rows, 2 columns, 3 both ->
-// (out, total, rstd, row codes, row scales, column codes, column scales)
+// (out, total, rstd, and with a form: row codes, row scales, column codes, column scales, rows, columns)
 PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return plain(n, 11, [&]() -> PyObject* {
     Call call;
@@ -234,13 +239,14 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       factors = static_cast<float*>(rstd.data_ptr());
     }
     const auto at_ptr = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-    Results r(form == 0 ? 3 : 7);
+    Results r(form == 0 ? 3 : 9);
     r.set(0, passed(a[8], out));
     r.set(1, given(a[3]) ? passed(a[9], total) : passed(a[0], total));
     r.set(2, given(a[10]) || save ? passed(a[10], rstd) : none());
     for (int f = 0; form != 0 && f < 2; ++f) {
       r.set(3 + 2 * f, wrap_or_none(codes[f]));
       r.set(4 + 2 * f, wrap_or_none(scales[f]));
+      r.set(7 + f, whole_number(sizes[f]));
     }
     return r.after(demo_rms_norm(mx.p, mx.ld, mr.p, mr.ld, dtype, weight, weight_dtype, mx.rows, mx.cols, eps, mt.p, mt.ld, mo.p,
                                  mo.ld, factors, static_cast<int>(fmt), at_ptr(codes[0]),

@@ -586,9 +586,12 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
   }
   // As many tokens at a time as one cluster sorts; the later ones are added.
   int64_t first = 0;
-  t.grad = add ? nullptr : grad;
+  t.grad = grad;
   t.cols = cols;
   t.ldg = q.ldg;
+  // Written anew: what no token names is 0.  Without tokens the first kernel fills everything.
+  if (!add) t.filled = n == 0 ? vocab : std::min<int64_t>(vocab, (kFillBytes / 4 + cols - 1) / cols);
+  q.zero_from = add ? vocab : t.filled;
   do {
     const int64_t left = n - first;
     t.n = q.n = static_cast<int>(left < w.batch ? left : w.batch);
@@ -596,7 +599,8 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
     if ((s = to_status(launch_sort_tokens(t, dev.sms, st))) != DEMO_OK) return s;
     if (t.n == 0) break;  // no tokens: the table is filled, nothing is summed
     if ((s = to_status(launch_embed_grad(q, dtype, st))) != DEMO_OK) return s;
-    t.grad = nullptr;
+    t.filled = 0;
+    q.zero_from = vocab;
     q.add = 1;
     first += t.n;
   } while (first < n);

@@ -59,7 +59,9 @@ __device__ __forceinline__ void store_wide(T* p, const float (&v)[N]) {
 // Lookup
 // ----------------------------------------------------------------------------
 
-constexpr int kLookThreads = 256, kLookUnroll = 2;
+// 16384 x 2048 into bfloat16 22.9 us (122 MB that cannot be done without; 256 threads 23.9, 512 25.4; one access 25.9,
+// four 24.3).
+constexpr int kLookThreads = 128, kLookUnroll = 2;
 
 // Eight columns a thread as 16-byte accesses, or (rows off 16 bytes) warps of 128 columns, four a lane.
 template <typename T, typename O, bool VEC>
@@ -166,11 +168,11 @@ struct SortShared {
   uint32_t scan[kSortWarps];
 };
 
-// Writes 0 to every row of the table, `part` of `parts`.
+// Writes 0 to the first `filled` rows of the table, `part` of `parts`.
 __device__ __forceinline__ void fill_rows(const SortParams& p, long long part, long long parts) {
   if (p.ldg == p.cols) {  // one run of floats: whole 16-byte accesses, and what is off them at either end
     float* base = p.grad;
-    const long long total = p.vocab * p.cols, head = (4 - (reinterpret_cast<uintptr_t>(base) / 4 & 3)) & 3;
+    const long long total = p.filled * p.cols, head = (4 - (reinterpret_cast<uintptr_t>(base) / 4 & 3)) & 3;
     const long long first = head < total ? head : total, units = (total - first) / 4;
     for (long long u = part * kSortThreads + threadIdx.x; u < units; u += parts * kSortThreads)
       reinterpret_cast<float4*>(base + first)[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -183,7 +185,7 @@ __device__ __forceinline__ void fill_rows(const SortParams& p, long long part, l
   }
   const int lane = threadIdx.x & 31;
   const bool wide = p.cols % 4 == 0 && p.ldg % 4 == 0 && (reinterpret_cast<uintptr_t>(p.grad) & 15) == 0;
-  for (long long r = part * kSortWarps + (threadIdx.x >> 5); r < p.vocab; r += parts * kSortWarps) {
+  for (long long r = part * kSortWarps + (threadIdx.x >> 5); r < p.filled; r += parts * kSortWarps) {
     float* row = p.grad + r * p.ldg;
     if (wide) {
       for (long long c = 4 * lane; c < p.cols; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -193,8 +195,8 @@ __device__ __forceinline__ void fill_rows(const SortParams& p, long long part, l
   }
 }
 
-// The first cluster sorts.  Where the table's gradient is written anew, the other SMs fill it with zeros meanwhile
-// (the sums then overwrite the rows that have tokens), which hides the sort behind the fill.
+// The first cluster sorts.  Where the table's gradient is written anew, the other SMs fill its first rows with
+// zeros meanwhile, as many as the sort takes time for (the sums then overwrite those that have tokens).
 __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ __align__(16) unsigned char raw[];
   SortShared& sh = *reinterpret_cast<SortShared*>(raw);
@@ -376,11 +378,42 @@ enum : int { kEnds = 1 << 16, kFinal = 1 << 17, kStarts = 1 << 18, kLive = 1 << 
 // A warp sums one piece over one slab of columns.  What becomes of an entry follows from its key and those around
 // the piece, so every row that a batch needs is asked for at once: the rows of dy, and those of the gradient
 // that a token's sum is added to.
+// Blocks behind those write 0 to the rows that no token names, from `zero_from` on.
+template <bool VEC>
+__device__ __forceinline__ void zero_absent(const EmbedGradParams& p, long long r0, int lane) {
+  // 32 rows a warp: each lane looks its row up in the sorted keys, then the warp writes the absent ones.
+  const long long r = r0 + lane;
+  int lo = 0, hi = p.n;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (p.keys[mid] < r)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  unsigned absent = __ballot_sync(0xffffffffu, r < p.vocab && !(lo < p.n && p.keys[lo] == r));
+  const int cols = static_cast<int>(p.cols);
+  while (absent != 0) {
+    const int i = __ffs(static_cast<int>(absent)) - 1;
+    absent &= absent - 1;
+    float* row = p.grad + (r0 + i) * p.ldg;
+    if constexpr (VEC) {
+      for (int c = 4 * lane; c < cols; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
+      for (int c = lane; c < cols; c += 32) row[c] = 0.0f;
+    }
+  }
+}
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_constant__ EmbedGradParams p) {
   constexpr int N = kSlabN<VEC>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   kernel_begin();
+  if (blockIdx.x >= p.sum_blocks) {
+    zero_absent<VEC>(p, p.zero_from + (static_cast<long long>(blockIdx.x - p.sum_blocks) * kSumWarps + warp) * 32, lane);
+    return;
+  }
   const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + warp;
   const int piece = static_cast<int>(item / p.slabs), slab = static_cast<int>(item - static_cast<long long>(piece) * p.slabs);
   const int begin = piece * p.piece;
@@ -535,8 +568,10 @@ cudaError_t launch_sums(EmbedGradParams& p, cudaStream_t st) {
   p.slabs = static_cast<int>((p.cols + cols - 1) / cols);
   p.ldparts = static_cast<long long>(p.slabs) * cols;
   const long long pieces = (p.n + p.piece - 1) / p.piece, items = pieces * p.slabs;
-  const cudaError_t e = launch_overlapped(embed_sum_kernel<T, VEC>, static_cast<unsigned>((items + kSumWarps - 1) / kSumWarps),
-                                          kSumThreads, 0, st, p);
+  p.sum_blocks = static_cast<unsigned>((items + kSumWarps - 1) / kSumWarps);
+  const long long absent = p.zero_from < p.vocab ? (p.vocab - p.zero_from + 32 * kSumWarps - 1) / (32 * kSumWarps) : 0;
+  const cudaError_t e =
+      launch_overlapped(embed_sum_kernel<T, VEC>, p.sum_blocks + static_cast<unsigned>(absent), kSumThreads, 0, st, p);
   if (e != cudaSuccess || pieces <= 1) return e;
   return launch_overlapped(embed_join_kernel<VEC>, static_cast<unsigned>((pieces + kJoinWarps - 1) / kJoinWarps * p.slabs),
                            32 * kJoinWarps, 0, st, p);
@@ -559,16 +594,14 @@ cudaError_t launch_sort_tokens(const SortParams& p, int sms, cudaStream_t st) {
   while ((p.vocab >> bits) != 0) ++bits;  // vocab itself is the key of tokens outside the table
   q.passes = (bits + kDigitBits - 1) / kDigitBits;
   q.bits = (bits + q.passes - 1) / q.passes;
-  // As few CTAs as hold the tokens where a long fill hides the sort (its clusters are small then, and fit on every
-  // SM: 822 MB and 16384 tokens 165 us, with eight CTAs 177); else two rounds of 32 a warp (13 us; eight rounds 22).
-  const long long table = p.grad != nullptr ? p.vocab * p.cols * 4 : 0;
-  const int each = kSortThreads * (table > (32 << 20) ? kSortRounds : 2);
+  // Two rounds of 32 a warp (16384 tokens: 13 us; with eight rounds, in two CTAs, 22).
+  const int each = 2 * kSortThreads;
   const int ctas = p.n <= each ? 1 : p.n <= 2 * each ? 2 : p.n <= 4 * each ? 4 : 8;
   cudaLaunchConfig_t cfg = {};
   // Three quarters of the SMs fill (clusters of eight do not fit on all of them at one time), 64 KB each at least.
   long long fill = 0;
-  if (p.grad != nullptr) {
-    const long long worth = (p.vocab * p.cols + 16383) / 16384, most = sms * 3 / 4 / ctas - 1;
+  if (p.filled > 0) {
+    const long long worth = (p.filled * p.cols + 16383) / 16384, most = sms * 3 / 4 / ctas - 1;
     fill = (worth + ctas - 1) / ctas;
     fill = fill < 1 || most < 1 ? 1 : fill < most ? fill : most;
   }

@@ -124,8 +124,8 @@ struct SortParams {
   int n, passes, bits;     // passes over digits of `bits`: set by the launcher
   int* keys;               // [n] sorted; vocab stands for tokens outside the table
   unsigned short* positions;  // [n], from the first token on
-  float* grad;                // not NULL: the table's gradient, filled with zeros meanwhile
-  long long cols, ldg;
+  float* grad;                // the table's gradient, whose first `filled` rows are filled with zeros meanwhile
+  long long cols, ldg, filled;
 };
 cudaError_t launch_sort_tokens(const SortParams& p, int sms, cudaStream_t st);
 struct EmbedGradParams {
@@ -135,11 +135,17 @@ struct EmbedGradParams {
   float* grad;
   float* parts;  // [pieces][2][ldparts]
   long long first, vocab, cols, lddy, ldg, ldparts;
+  long long zero_from;  // rows from here on that no token names are written 0; vocab for none
+  unsigned int sum_blocks;
   int n, piece, slabs, add;  // piece: 8, 16 or 32
   float scale;
 };
 cudaError_t launch_embed_grad(EmbedGradParams& p, int dtype, cudaStream_t st);
 cudaError_t prepare_embedding_kernels();
+
+// Bytes of the gradient that are filled while the tokens are sorted: 20 us of HBM, and what L2 holds (a table of 99 MB
+// filled there 29 us in all, with half of it left to the sums 46).
+constexpr long long kFillBytes = 128 << 20;
 
 // Sorted positions of a piece (one warp's work on 256 columns): 32, or fewer where those would leave an SM fewer
 // than three warps.  Sums and join, bfloat16 dy, us with 8 / 16 / 32 positions: 16384 x 2048 48 / 43 / 39, 4096 x

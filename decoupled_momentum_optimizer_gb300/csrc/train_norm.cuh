@@ -58,11 +58,11 @@ __device__ __forceinline__ uint32_t packed_max_abs(uint32_t m, uint32_t a) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A lane's N elements of a unit: whole accesses of 16 bits stay packed in words (as an array of 16-bit elements
-// they took a register each), all others are float32.
+// A lane's N elements of a unit: 16 bits stay packed in words (as an array of 16-bit elements they took a
+// register each), float32 is itself.
 template <typename T, bool VEC, int N>
 struct Unit {
-  static constexpr bool kPacked = VEC && sizeof(T) == 2;
+  static constexpr bool kPacked = sizeof(T) == 2;
   static constexpr int kWords = kPacked ? N / 2 : N;
   uint32_t w[kWords];
 
@@ -76,8 +76,8 @@ struct Unit {
     if constexpr (kPacked) {
       w[i] = narrow<T>(v);
     } else {
-      w[2 * i] = __float_as_uint(to_f32(from_f32<T>(v.x)));
-      w[2 * i + 1] = __float_as_uint(to_f32(from_f32<T>(v.y)));
+      w[2 * i] = __float_as_uint(v.x);
+      w[2 * i + 1] = __float_as_uint(v.y);
     }
   }
   __device__ __forceinline__ void add(const Unit& o) {
@@ -111,14 +111,18 @@ struct Unit {
         clear();
       }
     } else {
+      using Bits = std::conditional_t<kPacked, uint16_t, uint32_t>;
+      Bits b[N];
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        w[e] = 0u;
+        b[e] = 0;
         if (at.has<VEC, N>(j, e)) {
-          const T* q = p + at.offset<VEC, N>(j, e);
-          w[e] = __float_as_uint(to_f32(CONST ? __ldg(q) : *q));
+          const Bits* q = reinterpret_cast<const Bits*>(p + at.offset<VEC, N>(j, e));
+          b[e] = CONST ? __ldg(q) : *q;
         }
       }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = kPacked ? b[2 * i] | static_cast<uint32_t>(b[2 * i + 1]) << 16 : b[i];
     }
   }
   __device__ __forceinline__ void store(T* p, const Place& at, int j) const {
@@ -126,8 +130,14 @@ struct Unit {
       if (at.has<VEC, N>(j, 0)) *reinterpret_cast<uint4*>(p + at.offset<VEC, N>(j, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (at.has<VEC, N>(j, e)) p[at.offset<VEC, N>(j, e)] = from_f32<T>(__uint_as_float(w[e]));
+      for (int e = 0; e < N; ++e) {
+        if (at.has<VEC, N>(j, e)) {
+          if constexpr (kPacked)
+            reinterpret_cast<uint16_t*>(p)[at.offset<VEC, N>(j, e)] = static_cast<uint16_t>(e % 2 ? w[e / 2] >> 16 : w[e / 2]);
+          else
+            reinterpret_cast<uint32_t*>(p)[at.offset<VEC, N>(j, e)] = w[e];
+        }
+      }
     }
   }
 };

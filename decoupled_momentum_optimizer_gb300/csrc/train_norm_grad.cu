@@ -225,10 +225,11 @@ cudaError_t launch_norm_grad_u(NormGradParams& p, long long units, int sms, cuda
   p.lanes = U == 1 && units == 1 ? row_lanes((p.cols + kNormN<T, VEC> - 1) / kNormN<T, VEC>) : 32;
   p.per = static_cast<int>((units + p.warps - 1) / p.warps);
   const long long rows = (32 / p.lanes) * K;  // of a group
-  // As many groups as fit, but no more than give every SM a CTA.
+  // As many groups as fit, but no more than give every SM a CTA; rows that one CTA takes at once are one
+  // CTA's, which needs no second kernel.
   const long long most = THREADS == kGradThreads ? kGradThreads / 32 / p.warps : 1;
-  const long long spread = (p.rows + rows * sms - 1) / (rows * sms);
-  const long long groups = spread < 1 ? 1 : spread < most ? spread : most;
+  const long long turns = (p.rows + rows - 1) / rows, spread = (turns + sms - 1) / sms;
+  const long long groups = turns <= most ? (turns < 1 ? 1 : turns) : spread < most ? spread : most;
   long long grid = (p.rows + groups * rows - 1) / (groups * rows);
   if (grid > sms) grid = sms;
   if (grid > kNormParts) grid = kNormParts;
@@ -247,10 +248,10 @@ template <typename T, typename W, bool VEC>
 cudaError_t launch_norm_grad_v(NormGradParams& p, int sms, cudaStream_t st) {
   constexpr int n = kNormN<T, VEC>, most = kGradThreads / 32;
   constexpr int u = kGradUnits<T, VEC, kGradThreads>;
-  static_assert(u == 4, "four, two or one access of a row");
   const long long units = (p.cols + 32 * n - 1) / (32 * n);
   if (units == 1) return launch_norm_grad_u<T, W, VEC, 1, 4, kGradThreads>(p, units, sms, st);
   if (units == 2) return launch_norm_grad_u<T, W, VEC, 2, 2, kGradThreads>(p, units, sms, st);
+  if (u > 4 && units <= 4) return launch_norm_grad_u<T, W, VEC, 4, u / 4, kGradThreads>(p, units, sms, st);
   if (units <= u * most) return launch_norm_grad_u<T, W, VEC, u, 1, kGradThreads>(p, units, sms, st);
   return launch_norm_grad_u<T, W, VEC, kGradUnits<T, VEC, kGradWide>, 1, kGradWide>(p, units, sms, st);
 }

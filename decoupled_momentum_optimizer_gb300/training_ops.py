@@ -414,9 +414,14 @@ def rms_norm(x, weight, *, eps=1e-6, residual=None, values=True, form=None, fmt=
         if r.__class__ is tuple:
             if form is None:
                 return Normed(r[0], None, r[1], r[2])
-            by_rows = _made(r[3], r[4], *x.shape) if form != "cols" else None
-            by_cols = _made(r[5], r[6], x.shape[1], x.shape[0]) if form != "rows" else None
-            return Normed(r[0], (by_rows, by_cols) if form == "both" else by_cols if by_rows is None else by_rows, r[1], r[2])
+            out, total, rstd, codes, scales, codes_cols, scales_cols, rows, cols = r
+            if form == "rows":
+                q = _made(codes, scales, rows, cols)
+            elif form == "cols":
+                q = _made(codes_cols, scales_cols, cols, rows)
+            else:
+                q = _made(codes, scales, rows, cols), _made(codes_cols, scales_cols, cols, rows)
+            return Normed(out, q, total, rstd)
         if r is not NotImplemented:
             _refused(r, "demo_rms_norm")
     if stream is not None:
