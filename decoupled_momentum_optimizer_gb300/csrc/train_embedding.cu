@@ -59,47 +59,46 @@ __device__ __forceinline__ void store_wide(T* p, const float (&v)[N]) {
 // Lookup
 // ----------------------------------------------------------------------------
 
-// 16384 x 2048 into bfloat16 22.9 us (122 MB that cannot be done without; 256 threads 23.9, 512 25.4; one access 25.9,
-// four 24.3).
-constexpr int kLookThreads = 128, kLookUnroll = 2;
+// 16384 x 2048 into bfloat16 20.7 us (122 MB that cannot be done without: 17.9), two accesses of one row 22.9; 65536 x
+// 768 25.4 us and 31.
+constexpr int kLookThreads = 128, kLookRows = 4;
 
-// Eight columns a thread as 16-byte accesses, or (rows off 16 bytes) warps of 128 columns, four a lane.
+// A thread takes eight columns of kLookRows rows as 16-byte accesses, or (rows off 16 bytes) a warp 128 columns of
+// one row, four a lane.
 template <typename T, typename O, bool VEC>
 __global__ void __launch_bounds__(kLookThreads) lookup_kernel(const __grid_constant__ LookupParams p, long long per_row) {
   kernel_begin();
   const T* table = static_cast<const T*>(p.table);
   O* out = static_cast<O*>(p.out);
-  const long long units = p.n * per_row;
   const auto row_of = [&](long long u) {
     return u < (1ll << 32) ? static_cast<long long>(static_cast<uint32_t>(u) / static_cast<uint32_t>(per_row)) : u / per_row;
   };
   if constexpr (VEC) {
-    const long long first = static_cast<long long>(blockIdx.x) * (kLookThreads * kLookUnroll) + threadIdx.x;
-    float v[kLookUnroll][8];
-    long long row[kLookUnroll], col[kLookUnroll];
+    const long long u = static_cast<long long>(blockIdx.x) * kLookThreads + threadIdx.x;
+    const long long group = row_of(u), row0 = group * kLookRows, col = (u - group * per_row) * 8;
+    float v[kLookRows][8];
+    long long t[kLookRows];
 #pragma unroll
-    for (int j = 0; j < kLookUnroll; ++j) {
-      const long long u = first + j * kLookThreads;
-      row[j] = -1;
+    for (int j = 0; j < kLookRows; ++j) t[j] = row0 + j < p.n ? token_at(p.tokens, row0 + j) : -1;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
-      if (u < units) {
-        row[j] = row_of(u);
-        col[j] = (u - row[j] * per_row) * 8;
-        const long long t = token_at(p.tokens, row[j]);
-        if (t >= 0 && t < p.vocab) load_wide<T, 8>(table + t * p.ldt + col[j], v[j]);
+    for (int j = 0; j < kLookRows; ++j) {
+      if (t[j] >= 0 && t[j] < p.vocab) {
+        load_wide<T, 8>(table + t[j] * p.ldt + col, v[j]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
       }
     }
 #pragma unroll
-    for (int j = 0; j < kLookUnroll; ++j) {
-      if (row[j] < 0) continue;
+    for (int j = 0; j < kLookRows; ++j) {
+      if (row0 + j >= p.n) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] *= p.scale;
-      store_wide<O, 8>(out + row[j] * p.ldo + col[j], v[j]);
+      store_wide<O, 8>(out + (row0 + j) * p.ldo + col, v[j]);
     }
   } else {
     const long long u = static_cast<long long>(blockIdx.x) * (kLookThreads / 32) + (threadIdx.x >> 5);
-    if (u >= units) return;
+    if (u >= p.n * per_row) return;
     const int lane = threadIdx.x & 31;
     const long long row = row_of(u), col = (u - row * per_row) * 128 + lane;
     const long long t = token_at(p.tokens, row);
@@ -122,9 +121,9 @@ cudaError_t launch_lookup_t(const LookupParams& p, cudaStream_t st) {
     return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * static_cast<long long>(size) % 16 == 0;
   };
   if (p.cols % 8 == 0 && at(p.table, p.ldt, sizeof(T)) && at(p.out, p.ldo, sizeof(O))) {
-    const long long per = p.cols / 8, each = kLookThreads * kLookUnroll;
-    return launch_overlapped(lookup_kernel<T, O, true>, static_cast<unsigned>((p.n * per + each - 1) / each), kLookThreads, 0,
-                             st, p, per);
+    const long long per = p.cols / 8, units = (p.n + kLookRows - 1) / kLookRows * per;
+    return launch_overlapped(lookup_kernel<T, O, true>, static_cast<unsigned>((units + kLookThreads - 1) / kLookThreads),
+                             kLookThreads, 0, st, p, per);
   }
   const long long per = (p.cols + 127) / 128, each = kLookThreads / 32;
   return launch_overlapped(lookup_kernel<T, O, false>, static_cast<unsigned>((p.n * per + each - 1) / each), kLookThreads, 0,
