@@ -15,16 +15,17 @@
 // sixteen warps share an SM (8 warps of 16 rows with 120 registers: 72 us where this took 62).
 // A row's block is one warp's 128 elements (one warp-wide maximum each; lane i then works out row i's
 // scale for all), a column's block is 8 registers of a lane and the 16 warps' maxima in shared memory,
-// a thread per column.  Infinities and NaN are found by a multiply-add with 0 per element and mended
-// only where there are any.  Row codes leave as 128 contiguous bytes per row; column codes are packed 8
-// rows at a time from the same registers, and leave through a swizzled 16 KB tile in shared memory as
-// 128 contiguous bytes per column.
+// a thread per column.  Infinities and NaN are found in the rows' maxima, which keep a NaN, and mended only
+// where there are any.  Products take two columns at a time (an instruction each), maxima three values.  Row
+// codes leave as 128 contiguous bytes per row; column codes are packed 8 rows at a time from the same registers,
+// and leave through a swizzled 16 KB tile in shared memory as 128 contiguous bytes per column.
 //
-// Measured, both forms: 8192 x 2048 float32 tiles 16 us (6.2 TB/s, HBM's rate); 8192 x 8192 bfloat16 55 us
-// (4.8 TB/s; 62 with bounds checked in whole tiles too), with relu and dropout 82 us (68 without the
-// hash).  Nothing is saturated there: the integer and compare pipe is 65% busy (17 of 32 instructions an
-// element), issue slots 61%, HBM 33%; a tile is loaded, computed and stored in turn, and only the SM's
-// other CTA overlaps that.
+// Measured, both forms: 8192 x 2048 float32 tiles 15.8 us (6.3 TB/s, HBM's rate); 8192 x 8192 bfloat16 53.6 us
+// (5.1 TB/s; 62 with bounds checked in whole tiles too), with relu and dropout 80 us (68 without the hash); a
+// norm's result, 16384 x 2048 bfloat16, 32 us.  Nothing is saturated there: issue slots 50% busy, HBM 33%; a tile
+// is loaded, computed and stored in turn, and only the SM's other CTA overlaps that.  (CTAs that stay and copy
+// their next tile ahead: 48.6 us for 8192 x 8192, but 20 for the float32 tiles and 35 for the norm, whose tiles
+// do not divide by the CTAs.)
 #include "train_pairs.cuh"
 
 namespace demo {

@@ -314,9 +314,10 @@ int demo_adamw_step(float* theta, int64_t n, float beta1, float beta2, float eps
 /*
  * ---- Training operators: what makes the gradient the step consumes ----
  *
- * Dropout, matrices in 8-bit floating point with a scale for each block of 128, and their
- * products.  They follow the conventions above (device pointers, streams, statuses, no allocation
- * in the calls, graph capture, results that are the same to the bit from call to call) except that
+ * Dropout, matrices in 8-bit floating point with a scale for each block of 128, their products,
+ * root-mean-square norms, embedding tables, and the clipping of the gradients.  They follow the
+ * conventions above (device pointers, streams, statuses, no allocation in the calls, graph capture,
+ * results that are the same to the bit from call to call) except that
  *   - a matrix argument has a row stride `ld` in elements and needs only its element's alignment
  *     (whole 16-byte rows are faster); rows of an input may overlap or repeat (ld < cols, 0
  *     included), rows of an output may not (DEMO_EINVAL);
@@ -421,8 +422,8 @@ int demo_fp8_linear(const void* x, int64_t ldx, int dtype, const void* w_codes, 
  *               fmt; a pair may be NULL.  The column form needs rstd, and total where there is a residual
  * At least one result is asked for.  total may be x or residual itself (same stride), out too where no
  * column form is asked for; otherwise results overlap neither each other nor an input (DEMO_EINVAL).
- * cols is at most 32768.  A row with an infinity has r = 0, one with a NaN r = NaN; what is not finite in
- * v becomes a NaN code.
+ * cols is at most 32768; with rows or cols 0 nothing is written.  A row with an infinity has r = 0, one with
+ * a NaN r = NaN; what is not finite in v becomes a NaN code.
  */
 int demo_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype, const void* weight,
                   int weight_dtype, int64_t rows, int64_t cols, double eps, void* total, int64_t ldt, void* out,
@@ -440,7 +441,7 @@ int demo_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
  *   workspace     device, 16-byte aligned, at least demo_rms_norm_grad_workspace(rows, cols) bytes (host
  *                 only; 0 for one row, then it may be NULL, as it may without dweight), apart from the
  *                 other buffers; fewer bytes give DEMO_ENOSPACE.  Its contents mean nothing between calls.
- * Sums are float32.  cols is at most 32768.
+ * Sums are float32.  cols is at most 32768; with cols 0 nothing is written.
  */
 size_t demo_rms_norm_grad_workspace(int64_t rows, int64_t cols);
 int demo_rms_norm_grad(const void* dy, int64_t lddy, const void* total, int64_t ldt, int dtype, const void* weight,
