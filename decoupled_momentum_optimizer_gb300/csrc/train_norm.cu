@@ -263,6 +263,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS * K 
           q[e / 4] = p.fmt == kE4M3 ? codes4<kE4M3>(u[e], u[e + 1], u[e + 2], u[e + 3])
                                     : codes4<kE5M2>(u[e], u[e + 1], u[e + 2], u[e + 3]);
         const int off = mine.offset<VEC, N>(j, 0), c0 = mine.first + off;
+        if (UNITS == 1 && lanes < kSpan) {
+          // Short rows: the warp clears its rows' one block each before the lanes write what they hold (lane by
+          // lane, a row of three columns would take 124 stores of a byte).
+          const int row_lane = threadIdx.x & 31;
+          const long long first = row - row_lane / lanes, left = p.rows - first;
+          uint4* block = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.codes) + first * kBlock);
+          const int units16 = (left < share ? static_cast<int>(left < 0 ? 0 : left) : share) * (kBlock / 16);
+          for (int u = row_lane; u < units16; u += 32) block[u] = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+        }
         if (UNITS > 1 || row < p.rows) {
           uint8_t* codes = static_cast<uint8_t*>(p.codes) + row * kp + mine.first;
           if constexpr (VEC) {
@@ -272,12 +282,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormWide ? 1 : UNITS * K 
               else
                 *reinterpret_cast<uint32_t*>(codes + off) = q[0];
             }
+          } else if (UNITS == 1 && lanes == 1) {
+            *reinterpret_cast<uint32_t*>(codes) = q[0];
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) codes[off + lanes * e] = static_cast<uint8_t>(q[0] >> (8 * e));
           }
-          if (lanes < kSpan)  // a short row's lanes also clear the rest of its one block
-            for (int c = lanes * N + lane; c < kBlock; c += lanes) codes[c - mine.first] = 0;
           if ((lane & (kSpan - 1)) == 0 && c0 < kp) {
             float* scale = p.scales + static_cast<long long>(c0 / kBlock) * lds;
             scale[row] = pow2f(exponent);

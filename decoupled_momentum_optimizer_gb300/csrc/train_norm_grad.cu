@@ -18,8 +18,9 @@
 
 namespace demo {
 
-// U accesses a lane of one row, K rows at a time: 32 elements of packed 16 bits, 16 of float32 (32 would spill 276
-// bytes a thread).  Rows of more than 16 warps take a CTA of 1024 threads and 32 elements a lane of any type.
+// U accesses a lane of one row, K rows at a time: 32 elements of packed 16 bits, 16 of others (32 spill 100 to 316
+// bytes a thread).  Rows that 16 warps do not hold so have 32 elements a lane of any type, and then up to 32 warps, which
+// spill more: 2000 x 12288 float32 108 us (3.6 TB/s), 436 x 12255 bfloat16 36 us (61 with 32 warps).
 constexpr int kGradThreads = 512, kGradWide = 1024;
 template <typename T, bool VEC, int THREADS>
 constexpr int kGradUnits = ((VEC && sizeof(T) == 2) || THREADS == kGradWide ? 32 : 16) / kNormN<T, VEC>;
@@ -258,7 +259,9 @@ cudaError_t launch_norm_grad_v(NormGradParams& p, int sms, cudaStream_t st) {
   if (units == 2) return launch_norm_grad_u<T, W, VEC, 2, 2, kGradThreads>(p, units, sms, st);
   if (u > 4 && units <= 4) return launch_norm_grad_u<T, W, VEC, 4, u / 4, kGradThreads>(p, units, sms, st);
   if (units <= u * most) return launch_norm_grad_u<T, W, VEC, u, 1, kGradThreads>(p, units, sms, st);
-  return launch_norm_grad_u<T, W, VEC, kGradUnits<T, VEC, kGradWide>, 1, kGradWide>(p, units, sms, st);
+  constexpr int wide = kGradUnits<T, VEC, kGradWide>;
+  if (units <= wide * most) return launch_norm_grad_u<T, W, VEC, wide, 1, kGradThreads>(p, units, sms, st);
+  return launch_norm_grad_u<T, W, VEC, wide, 1, kGradWide>(p, units, sms, st);
 }
 
 template <typename T, typename W>

@@ -21,7 +21,7 @@ RSTD = 2.0 ** -24 * (1 + 2.0 ** -15)
 # one column, parts of an access, of a block and of a unit; a warp's registers full and one more; several warps
 # and the widest row; few rows and many
 SHAPES = [(1, 1), (3, 5), (7, 8), (5, 100), (9, 128), (2, 136), (6, 255), (40, 256), (11, 765), (4, 1023), (130, 1024),
-          (1, 2048), (5, 2056), (3, 4100), (2, 8192), (33, 5000), (2, 16384), (3, 20001), (2, 32768), (1300, 200),
+          (1, 2048), (5, 2056), (3, 4100), (2, 8192), (33, 5000), (2, 16384), (3, 20001), (2, 32768), (3, 9001), (5, 12288), (1300, 200),
           (2500, 2048)]
 
 
@@ -74,7 +74,7 @@ def test_strides(rows, cols, dtype, pad, offset):
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("form", ["rows", "cols", "both"])
 @pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (3, 128, 0), (5, 129, 0), (6, 136, 8), (133, 100, 3), (9, 765, 6),
-                                           (2, 2048, 0), (260, 384, 0), (3, 4100, 4), (2, 16384 + 8, 0)])
+                                           (2, 2048, 0), (260, 384, 0), (3, 4100, 4), (2, 16384 + 8, 0), (300, 3, 1), (77, 20, 0), (65, 40, 8)])
 def test_forms(rows, cols, pad, dtype, form):
     x, res = draw(rows, cols, dtype, 5, pad=pad), draw(rows, cols, dtype, 6, pad=pad)
     check(x, weight(cols, "f32"), dtype, res, form=form, values=rows % 2 == 1)
@@ -167,6 +167,35 @@ def test_past_32_bits():
     dx, dw = dm.rms_norm_grad(x, x, w, n.rstd, out=x)
     a, b = dm.rms_norm_grad(want.out, want.out, w, want.rstd)
     assert torch.equal(dx[-4:], a) and torch.allclose(dw, b, rtol=1e-5, atol=1e-6 * float(b.abs().max()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols,pad", [(1, 0), (3, 0), (3, 3), (20, 4), (64, 0), (100, 0), (128, 0), (130, 2)])
+def test_many_short_rows(cols, pad, dtype):
+    """Enough of them that a warp takes several at a time: every row is what it is in a call of a few rows, which the
+    other tests compare with the formula.  The weight's gradient sums over all of them: a sum of n terms of random
+    sign passes sums of the size of the result, each rounding 2^-24 of that, sqrt(n) of them together; eight times
+    over."""
+    lanes = 1
+    while lanes < 32 and lanes * 4 < cols:
+        lanes *= 2
+    rows = 256 // lanes * 32 * torch.cuda.get_device_properties(0).multi_processor_count + 1037
+    gen = torch.Generator(device="cuda").manual_seed(70)
+    x, r = (torch.randn(rows, cols + pad, generator=gen, device="cuda").to(DT[dtype])[:, :cols] for _ in range(2))
+    w = weight(cols, "f32")
+    n = dm.rms_norm(x, w, residual=r, form="rows", save=True)
+    dx, dw = dm.rms_norm_grad(x, n.total, w, n.rstd, past=r)
+    for begin in (0, 4099, rows // 2 + 1, rows - 515):
+        part = slice(begin, begin + 515)
+        m = dm.rms_norm(x[part], w, residual=r[part], form="rows", save=True)
+        for a, b in ((n.out, m.out), (n.total, m.total), (n.rstd, m.rstd)):
+            assert torch.equal(a[part], b)
+        assert torch.equal(n.quantized.codes[part].view(torch.uint8), m.quantized.codes.view(torch.uint8))
+        assert torch.equal(n.quantized.scales[:, part], m.quantized.scales[:, :515])
+        assert torch.equal(dx[part], dm.rms_norm_grad(x[part], m.total, w, m.rstd, past=r[part])[0])
+    want = (x.double() * n.total.double() * n.rstd.double()[:, None]).sum(0)
+    size = (x.double() * n.total.double() * n.rstd.double()[:, None]).square().sum(0).sqrt()
+    assert bool(((dw.double() - want).abs() <= 8 * 2.0 ** -24 * rows ** 0.5 * size).all())
 
 
 # ---- gradient ------------------------------------------------------------------------------------
