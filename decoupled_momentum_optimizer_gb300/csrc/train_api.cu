@@ -158,10 +158,10 @@ struct EmbedWorkspace {
   EmbedWorkspace(int64_t n, int64_t cols) {
     batch = n < kMaxSorted ? n : kMaxSorted;
     piece = embed_piece(batch, cols);
-    keys = up(4 * batch, 16);
-    positions = up(2 * batch, 16);
+    keys = n > kFewTokens ? up(4 * batch, 16) : 0;
+    positions = n > kFewTokens ? up(2 * batch, 16) : 0;
     const int64_t pieces = (batch + piece - 1) / piece;
-    parts = pieces > 1 ? pieces * 2 * up(cols, 256) * 4 : 0;
+    parts = n > kFewTokens ? pieces * 2 * up(cols, 256) * 4 : 0;
   }
 };
 
@@ -552,9 +552,9 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
     if ((s = check_matrix(dy, n, cols, lddy, dtype, false)) != DEMO_OK) return s;
     const int64_t need = w.keys + w.positions + w.parts;
     if (workspace_bytes < static_cast<size_t>(need)) return DEMO_ENOSPACE;
-    if (workspace == nullptr) return DEMO_EINVAL;
-    if (!at(workspace, 16)) return DEMO_EALIGN;
-    const Region rg = matrix(grad, vocab, cols, ldg, 4), rw = flat(workspace, need);
+    if (need > 0 && workspace == nullptr) return DEMO_EINVAL;
+    if (need > 0 && !at(workspace, 16)) return DEMO_EALIGN;
+    const Region rg = matrix(grad, vocab, cols, ldg, 4), rw = flat(need > 0 ? workspace : nullptr, need);
     for (const Region& in : {matrix(tokens, token_rows, token_cols, ldtokens, token_bytes),
                              matrix(dy, n, cols, lddy, elem_size(dtype))})
       if (overlap(rg, in) || overlap(rw, in)) return DEMO_EINVAL;
@@ -579,6 +579,10 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
   q.piece = w.piece;
   q.add = add;
   q.scale = scale;
+  if (n > 0 && n <= kFewTokens) {
+    q.n = static_cast<int>(n);
+    return to_status(launch_embed_grad(q, t.tokens, dtype, st));
+  }
   if (n > 0) {
     q.keys = t.keys = reinterpret_cast<int*>(work);
     q.positions = t.positions = reinterpret_cast<unsigned short*>(work + w.keys);
@@ -598,7 +602,7 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
     t.first = q.first = first;
     if ((s = to_status(launch_sort_tokens(t, dev.sms, st))) != DEMO_OK) return s;
     if (t.n == 0) break;  // no tokens: the table is filled, nothing is summed
-    if ((s = to_status(launch_embed_grad(q, dtype, st))) != DEMO_OK) return s;
+    if ((s = to_status(launch_embed_grad(q, t.tokens, dtype, st))) != DEMO_OK) return s;
     t.filled = 0;
     q.zero_from = vocab;
     q.add = 1;

@@ -322,7 +322,8 @@ cudaError_t prepare_embedding_kernels() {
 // ----------------------------------------------------------------------------
 
 constexpr int kSumThreads = 128, kSumWarps = kSumThreads / 32;
-constexpr int kAhead = 4;  // rows of dy, and of the gradient that is added to, in flight a warp
+constexpr int kAhead = 4;     // rows of dy, and of the gradient that is added to, in flight a warp
+constexpr int kAheadFew = 8;  // the same where few warps run: 26 positions 6.6 us, with four 7.2
 
 // A warp's columns of a row: eight a lane as 16-byte accesses, or four a lane 32 apart.
 template <bool VEC>
@@ -379,84 +380,66 @@ __device__ __forceinline__ void finish_row(const EmbedGradParams& p, long long t
 
 enum : int { kEnds = 1 << 16, kFinal = 1 << 17, kStarts = 1 << 18, kLive = 1 << 19 };
 
-// A warp sums one piece over one slab of columns.  What becomes of an entry follows from its key and those around
-// the piece, so every row that a batch needs is asked for at once: the rows of dy, and those of the gradient
-// that a token's sum is added to.
-// Blocks behind those write 0 to the rows that no token names, from `zero_from` on.
+// Columns of 32 rows that one warp zeroes: few where a row is looked for among 32 tokens, more where that is a search.
+constexpr int kZeroFew = 256, kZeroMany = 1024;
+
+// Writes 0 to columns c0 .. c0 + most - 1 of a warp's rows r0 + (the set bits).
 template <bool VEC>
-__device__ __forceinline__ void zero_absent(const EmbedGradParams& p, long long r0, int lane) {
-  // 32 rows a warp: each lane looks its row up in the sorted keys, then the warp writes the absent ones.
-  const long long r = r0 + lane;
-  int lo = 0, hi = p.n;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (p.keys[mid] < r)
-      lo = mid + 1;
-    else
-      hi = mid;
+__device__ __forceinline__ void zero_rows(const EmbedGradParams& p, long long r0, unsigned rows, int c0, int most, int lane) {
+  const int end = p.cols - c0 < most ? static_cast<int>(p.cols) : c0 + most;
+  // all 32, end to end from a 16-byte boundary: whole accesses whatever the width
+  float* run = p.grad + r0 * p.ldg;
+  if (rows == 0xffffffffu && p.cols <= most && p.ldg == p.cols && (reinterpret_cast<uintptr_t>(run) & 15) == 0) {
+    for (long long u = lane; u < 8 * p.cols; u += 32) reinterpret_cast<float4*>(run)[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return;
   }
-  unsigned absent = __ballot_sync(0xffffffffu, r < p.vocab && !(lo < p.n && p.keys[lo] == r));
-  const int cols = static_cast<int>(p.cols);
-  while (absent != 0) {
-    const int i = __ffs(static_cast<int>(absent)) - 1;
-    absent &= absent - 1;
+  while (rows != 0) {
+    const int i = __ffs(static_cast<int>(rows)) - 1;
+    rows &= rows - 1;
     float* row = p.grad + (r0 + i) * p.ldg;
     if constexpr (VEC) {
-      for (int c = 4 * lane; c < cols; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c = c0 + 4 * lane; c < end; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     } else {
-      for (int c = lane; c < cols; c += 32) row[c] = 0.0f;
+      for (int c = c0 + lane; c < end; c += 32) row[c] = 0.0f;
     }
   }
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_constant__ EmbedGradParams p) {
+// The sums of up to 32 sorted positions: lane i holds entry i's token and position; `before` and `after` are the
+// tokens around them.
+template <typename T, bool VEC, int AHEAD>
+__device__ __forceinline__ void sum_entries(const EmbedGradParams& p, int key, int info, int here, int before, int after,
+                                            int piece, int slab, int lane) {
   constexpr int N = kSlabN<VEC>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  kernel_begin();
-  if (blockIdx.x >= p.sum_blocks) {
-    zero_absent<VEC>(p, p.zero_from + (static_cast<long long>(blockIdx.x - p.sum_blocks) * kSumWarps + warp) * 32, lane);
-    return;
-  }
-  const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + warp;
-  const int piece = static_cast<int>(item / p.slabs), slab = static_cast<int>(item - static_cast<long long>(piece) * p.slabs);
-  const int begin = piece * p.piece;
-  if (begin >= p.n) return;
   const Place at = Place::of<VEC, N>(slab, 1, lane, 32, static_cast<int>(p.cols));
-  const int here = p.n - begin < p.piece ? p.n - begin : p.piece;  // at most 32
-  const int key = lane < here ? p.keys[begin + lane] : -1;
-  int info = lane < here ? p.positions[begin + lane] : 0;
-  {
-    const int before = begin > 0 ? p.keys[begin - 1] : -1, after = begin + here < p.n ? p.keys[begin + here] : -1;
-    const int next = __shfl_down_sync(0xffffffffu, key, 1);
-    if (lane < here && key < p.vocab) {
-      info |= kLive;
-      const bool ends = lane == here - 1 || next != key;
-      if (key != before) info |= kStarts;
-      if (ends) info |= kEnds;
-      if (ends && key != before && key != after) info |= kFinal;
-    }
+  const int next = __shfl_down_sync(0xffffffffu, key, 1);
+  if (lane < here && key < p.vocab) {
+    info |= kLive;
+    const bool ends = lane == here - 1 || next != key;
+    if (key != before) info |= kStarts;
+    if (ends) info |= kEnds;
+    if (ends && key != before && key != after) info |= kFinal;
   }
   const T* dy = static_cast<const T*>(p.dy) + at.first;
   F2 sum[N / 2];
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) sum[i] = f2(0.0f, 0.0f);
-  for (int i0 = 0; i0 < here; i0 += kAhead) {
-    Unit<T, VEC, N> v[kAhead];
-    Unit<float, VEC, N> old[kAhead];
-    int what[kAhead];
-    float* row[kAhead];
+  for (int i0 = 0; i0 < here; i0 += AHEAD) {
+    Unit<T, VEC, N> v[AHEAD];
+    Unit<float, VEC, N> old[AHEAD];
+    int what[AHEAD];
+    float* row[AHEAD];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       what[j] = __shfl_sync(0xffffffffu, info, i0 + j);
       row[j] = p.grad + static_cast<long long>(__shfl_sync(0xffffffffu, key, i0 + j)) * p.ldg + at.first;
       if (what[j] & kLive) v[j].load(dy + (p.first + (what[j] & 0xffff)) * p.lddy, at, 0);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
+    for (int j = 0; j < AHEAD; ++j)
       if (p.add && (what[j] & kFinal)) old[j].load(row[j], at, 0);
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       if (!(what[j] & kLive)) continue;
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) sum[i] = add2(sum[i], v[j].get2(i));
@@ -477,6 +460,74 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
       for (int i = 0; i < N / 2; ++i) sum[i] = f2(0.0f, 0.0f);
     }
   }
+}
+
+// A warp sums one piece over one slab of columns.  What becomes of an entry follows from its key and those around
+// the piece, so every row that a batch needs is asked for at once: the rows of dy, and those of the gradient
+// that a token's sum is added to.  Blocks behind those write 0 to the rows that no token names, from `zero_from` on.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_constant__ EmbedGradParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  kernel_begin();
+  if (blockIdx.x >= p.sum_blocks) {
+    // 32 rows a warp: each lane looks its row up in the sorted keys, then the warp writes the absent ones.
+    const long long z = static_cast<long long>(blockIdx.x - p.sum_blocks) * kSumWarps + warp, group = z / p.zero_slabs;
+    const long long r0 = p.zero_from + group * 32, r = r0 + lane;
+    int lo = 0, hi = p.n;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (p.keys[mid] < r)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    zero_rows<VEC>(p, r0, __ballot_sync(0xffffffffu, r < p.vocab && !(lo < p.n && p.keys[lo] == r)),
+                   static_cast<int>(z - group * p.zero_slabs) * kZeroMany, kZeroMany, lane);
+    return;
+  }
+  const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + warp;
+  const int piece = static_cast<int>(item / p.slabs), slab = static_cast<int>(item - static_cast<long long>(piece) * p.slabs);
+  const int begin = piece * p.piece;
+  if (begin >= p.n) return;
+  const int here = p.n - begin < p.piece ? p.n - begin : p.piece;  // at most 32
+  const int key = lane < here ? p.keys[begin + lane] : -1;
+  const int pos = lane < here ? p.positions[begin + lane] : 0;
+  const int before = begin > 0 ? p.keys[begin - 1] : -1, after = begin + here < p.n ? p.keys[begin + here] : -1;
+  sum_entries<T, VEC, kAhead>(p, key, pos, here, before, after, piece, slab, lane);
+}
+
+// Up to 32 positions in one kernel: every warp sorts them itself (a token's place is the number of those before it),
+// and finds the rows that none names by comparing.  A call of 26 positions: two launches and a workspace less.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kSumThreads) embed_few_kernel(const __grid_constant__ EmbedGradParams p,
+                                                                const __grid_constant__ Tokens tokens) {
+  __shared__ int keys[kSumWarps][32], positions[kSumWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  kernel_begin();
+  const long long t = lane < p.n ? token_at(tokens, lane) : -1;
+  const int key = t >= 0 && t < p.vocab ? static_cast<int>(t) : static_cast<int>(p.vocab);  // others last
+  if (blockIdx.x >= p.sum_blocks) {
+    const long long z = static_cast<long long>(blockIdx.x - p.sum_blocks) * kSumWarps + warp, group = z / p.zero_slabs;
+    const long long r0 = group * 32, r = r0 + lane;
+    bool named = false;
+    for (int j = 0; j < p.n; ++j) named |= __shfl_sync(0xffffffffu, key, j) == r;
+    zero_rows<VEC>(p, r0, __ballot_sync(0xffffffffu, r < p.vocab && !named),
+                   static_cast<int>(z - group * p.zero_slabs) * kZeroFew, kZeroFew, lane);
+    return;
+  }
+  const int slab = static_cast<int>(blockIdx.x) * kSumWarps + warp;
+  if (slab >= p.slabs) return;
+  int place = 0;
+  for (int j = 0; j < p.n; ++j) {
+    const int other = __shfl_sync(0xffffffffu, key, j);
+    place += other < key || (other == key && j < lane);
+  }
+  if (lane < p.n) {
+    keys[warp][place] = key;
+    positions[warp][place] = lane;
+  }
+  __syncwarp();
+  sum_entries<T, VEC, kAheadFew>(p, lane < p.n ? keys[warp][lane] : -1, lane < p.n ? positions[warp][lane] : 0, p.n, -1, -1, 0, slab, lane);
 }
 
 // A token that starts in a piece and goes on: its part there, then the following pieces', in their order.  A
@@ -566,28 +617,39 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const __gri
 
 namespace {
 
+// Blocks that zero rows from `from` on; sets how many warps share 32 rows.
+unsigned zero_blocks(EmbedGradParams& p, long long from, int cols) {
+  p.zero_slabs = static_cast<int>((p.cols + cols - 1) / cols);
+  const long long warps = from < p.vocab ? (p.vocab - from + 31) / 32 * p.zero_slabs : 0;
+  return static_cast<unsigned>((warps + kSumWarps - 1) / kSumWarps);
+}
+
 template <typename T, bool VEC>
-cudaError_t launch_sums(EmbedGradParams& p, cudaStream_t st) {
+cudaError_t launch_sums(EmbedGradParams& p, const Tokens& tokens, cudaStream_t st) {
   constexpr int cols = 32 * kSlabN<VEC>;
   p.slabs = static_cast<int>((p.cols + cols - 1) / cols);
+  if (p.keys == nullptr) {  // few positions, not sorted
+    p.sum_blocks = static_cast<unsigned>((p.slabs + kSumWarps - 1) / kSumWarps);
+    return launch_overlapped(embed_few_kernel<T, VEC>, p.sum_blocks + zero_blocks(p, p.add ? p.vocab : 0, kZeroFew), kSumThreads,
+                             0, st, p, tokens);
+  }
   p.ldparts = static_cast<long long>(p.slabs) * cols;
   const long long pieces = (p.n + p.piece - 1) / p.piece, items = pieces * p.slabs;
   p.sum_blocks = static_cast<unsigned>((items + kSumWarps - 1) / kSumWarps);
-  const long long absent = p.zero_from < p.vocab ? (p.vocab - p.zero_from + 32 * kSumWarps - 1) / (32 * kSumWarps) : 0;
-  const cudaError_t e =
-      launch_overlapped(embed_sum_kernel<T, VEC>, p.sum_blocks + static_cast<unsigned>(absent), kSumThreads, 0, st, p);
+  const unsigned zero = zero_blocks(p, p.zero_from, kZeroMany);
+  const cudaError_t e = launch_overlapped(embed_sum_kernel<T, VEC>, p.sum_blocks + zero, kSumThreads, 0, st, p);
   if (e != cudaSuccess || pieces <= 1) return e;
   return launch_overlapped(embed_join_kernel<VEC>, static_cast<unsigned>((pieces + kJoinWarps - 1) / kJoinWarps * p.slabs),
                            32 * kJoinWarps, 0, st, p);
 }
 
 template <typename T>
-cudaError_t launch_sums_t(EmbedGradParams& p, cudaStream_t st) {
+cudaError_t launch_sums_t(EmbedGradParams& p, const Tokens& tokens, cudaStream_t st) {
   const auto at = [](const void* q, long long ld, size_t size) {
     return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * static_cast<long long>(size) % 16 == 0;
   };
   const bool vec = p.cols % 8 == 0 && at(p.dy, p.lddy, sizeof(T)) && at(p.grad, p.ldg, sizeof(float));
-  return vec ? launch_sums<T, true>(p, st) : launch_sums<T, false>(p, st);
+  return vec ? launch_sums<T, true>(p, tokens, st) : launch_sums<T, false>(p, tokens, st);
 }
 
 }  // namespace
@@ -624,9 +686,9 @@ cudaError_t launch_sort_tokens(const SortParams& p, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, sort_tokens_kernel, q);
 }
 
-cudaError_t launch_embed_grad(EmbedGradParams& p, int dtype, cudaStream_t st) {
-  if (dtype == kF32) return launch_sums_t<float>(p, st);
-  return dtype == kBF16 ? launch_sums_t<__nv_bfloat16>(p, st) : launch_sums_t<__half>(p, st);
+cudaError_t launch_embed_grad(EmbedGradParams& p, const Tokens& tokens, int dtype, cudaStream_t st) {
+  if (dtype == kF32) return launch_sums_t<float>(p, tokens, st);
+  return dtype == kBF16 ? launch_sums_t<__nv_bfloat16>(p, tokens, st) : launch_sums_t<__half>(p, tokens, st);
 }
 
 }  // namespace demo

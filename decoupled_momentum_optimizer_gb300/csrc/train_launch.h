@@ -128,8 +128,9 @@ struct SortParams {
   long long cols, ldg, filled;
 };
 cudaError_t launch_sort_tokens(const SortParams& p, int sms, cudaStream_t st);
+constexpr int kFewTokens = 32;  // positions that need no sort before the sums
 struct EmbedGradParams {
-  const int* keys;
+  const int* keys;  // NULL: few positions, taken from the tokens themselves
   const unsigned short* positions;
   const void* dy;
   float* grad;
@@ -137,10 +138,11 @@ struct EmbedGradParams {
   long long first, vocab, cols, lddy, ldg, ldparts;
   long long zero_from;  // rows from here on that no token names are written 0; vocab for none
   unsigned int sum_blocks;
+  int zero_slabs;  // warps that share 32 rows
   int n, piece, slabs, add;  // piece: 8, 16 or 32
   float scale;
 };
-cudaError_t launch_embed_grad(EmbedGradParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_embed_grad(EmbedGradParams& p, const Tokens& tokens, int dtype, cudaStream_t st);
 cudaError_t prepare_embedding_kernels();
 
 // Bytes of the gradient that are filled while the tokens are sorted: 20 us of HBM, and what L2 holds (a table of 99 MB

@@ -216,6 +216,18 @@ def test_grad_past_32_bits():
     assert bool((g[0] == 1).all()) and not bool(g[1].any()) and bool((g[2] == 1).all())
 
 
+@pytest.mark.parametrize("n", [1, 5, 31, 32, 33])
+@pytest.mark.parametrize("vocab,cols", [(1, 5), (31, 3), (700, 1), (700, 24), (5000, 768), (3, 2056), (300000, 7)])
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("idx", ["i32", "i64"])
+def test_few_positions(n, vocab, cols, add, idx):
+    """Up to 32 are sorted by the warps that sum; one more takes the other kernels."""
+    t = tokens(n, vocab, "zipf", 0.2 if n > 4 else 0.0).to(IDX[idx])
+    if n > 4:
+        t[1], t[3] = t[0], vocab - 1
+    check_grad(t.cuda(), draw(n, cols, "bf16", 82, pad=cols % 2), vocab, 1.5, add)
+
+
 def test_gradient_is_that_of_the_lookup():
     """sum(w * embedding) is linear in the table: a difference over a finite step is its derivative."""
     table, w = draw(30, 20, "f32", 74), draw(80, 20, "f32", 75)
@@ -296,7 +308,7 @@ def test_refusals():
                       (ValueError, lambda: dm.embedding_grad(t, dy)), (ValueError, lambda: dm.embedding_grad(t, dy, 20, add=True)),
                       (ValueError, lambda: dm.embedding_grad(t[:9], dy, 20)), (ValueError, lambda: dm.embedding_grad(t, dy, 21, out=table)),
                       (TypeError, lambda: dm.embedding_grad(t, dy, out=table.half())),
-                      (dm.DemoError, lambda: dm.embedding_grad(t, dy, 20, workspace=small)),
+                      (dm.DemoError, lambda: dm.embedding_grad(t.repeat(4), dy.repeat(4, 1), 20, workspace=small)),
                       (dm.DemoError, lambda: dm.embedding_grad(t, dy, out=dy))):
         with pytest.raises(err):
             call()

@@ -155,7 +155,8 @@ def test_embedding_grad_refusals(L):
     ws = L.demo_embedding_grad_workspace
     # keys, positions, two parts of 512 columns for each of 125 pieces of 8
     assert need == 4000 + 2000 + 125 * 2 * 512 * 4
-    assert ws(1, 300) == 32 and ws(0, 5) == ws(-1, 5) == ws(5, 0) == 0
+    assert ws(33, 300) == 144 + 80 + 5 * 2 * 512 * 4 and ws(32, 300) == ws(1, 300) == 0
+    assert embed_grad(L, tc=32, work=None) in NODEV and ws(0, 5) == ws(-1, 5) == ws(5, 0) == 0
     assert ws(1 << 30, 2048) == ws(65536, 2048) == 65536 * 6 + 2048 * 2 * 2048 * 4
 
 
