@@ -231,10 +231,11 @@ int check_grads(int count, const void* const* g, const int64_t* n, int dtype, vo
 }
 
 // The tensors of one launch, from `from` on; returns the next one's index.
-int fill_clip(ClipParams* q, int from, int count, const void* const* g, const int64_t* n, void* const* out, int64_t size) {
+template <int CAP>
+int fill_clip(ClipParams<CAP>* q, int from, int count, const void* const* g, const int64_t* n, void* const* out, int64_t size) {
   q->count = 0;
   q->chunks = 0;
-  for (; from < count && q->count < kClipTensors; ++from) {
+  for (; from < count && q->count < CAP; ++from) {
     if (n[from] == 0) continue;
     q->g[q->count] = g[from];
     q->out[q->count] = out != nullptr ? out[from] : nullptr;
@@ -245,19 +246,71 @@ int fill_clip(ClipParams* q, int from, int count, const void* const* g, const in
   return from;
 }
 
+// Whether all tensors fit one launch of a few chunks; fills it if so.
+bool fill_small(ClipParams<kClipFew>* q, int count, const void* const* g, const int64_t* n, void* const* out, int64_t size,
+                float* norm) {
+  int64_t left = (int64_t(kSmallChunks) << 15) / size;  // chunks are 32 KB
+  if (count > kClipFew) return false;
+  for (int i = 0; i < count; ++i)
+    if ((left -= n[i]) < 0) return false;
+  fill_clip(q, 0, count, g, n, out, size);
+  q->given = 0;
+  q->norm = norm;
+  return q->count > 0 && q->chunks <= kSmallChunks;
+}
+
+template <int CAP>
+bool all_in_place(const ClipParams<CAP>& q) {
+  for (int i = 0; i < q.count; ++i)
+    if (q.out[i] != q.g[i]) return false;
+  return true;
+}
+
 // Launches the sums of squares of all tensors; *parts_used sums are left in `parts`.
-int launch_all_squares(ClipParams* q, int count, const void* const* g, const int64_t* n, int dtype, int sms, double* parts,
+template <int CAP>
+int launch_all_squares(ClipParams<CAP>* q, int count, const void* const* g, const int64_t* n, int dtype, int sms, double* parts,
                        int* parts_used, cudaStream_t st) {
   *parts_used = 0;
   for (int from = 0; from < count;) {
     from = fill_clip(q, from, count, g, n, nullptr, elem_size(dtype));
     if (q->count == 0) break;
     q->parts = parts + *parts_used;
-    *parts_used += clip_parts(*q, dtype, sms);
+    *parts_used += clip_parts(q->chunks, dtype, sms);
     const int s = to_status(launch_squares(*q, dtype, sms, st));
     if (s != DEMO_OK) return s;
   }
   return DEMO_OK;
+}
+
+template <int CAP>
+int norm_of_list(ClipParams<CAP>* q, int count, const void* const* g, const int64_t* n, int dtype, int sms, double* parts,
+                 float* norm, cudaStream_t st) {
+  int used = 0;
+  const int s = launch_all_squares(q, count, g, n, dtype, sms, parts, &used, st);
+  return s != DEMO_OK ? s : to_status(launch_norm_of_parts(parts, used, norm, st));
+}
+
+template <int CAP>
+int clip_list(ClipParams<CAP>* q, int count, const void* const* g, const int64_t* n, int dtype, void* const* to, int out_dtype,
+              double max_norm, int sms, double* parts, float* norm, int norm_given, cudaStream_t st) {
+  int used = 0, s;
+  if (!norm_given && (s = launch_all_squares(q, count, g, n, dtype, sms, parts, &used, st)) != DEMO_OK) return s;
+  bool any = false;
+  for (int from = 0; from < count;) {
+    from = fill_clip(q, from, count, g, n, to, elem_size(dtype));
+    if (q->count == 0) break;
+    q->part_count = used;
+    q->all_parts = parts;
+    q->given = norm_given;
+    q->first_launch = !any;
+    q->in_place = all_in_place(*q);
+    q->max_norm = max_norm;
+    q->norm = norm;
+    if ((s = to_status(launch_scale(*q, dtype, out_dtype, sms, st))) != DEMO_OK) return s;
+    any = true;
+  }
+  // Nothing to scale: the norm over nothing.
+  return any || norm_given ? DEMO_OK : to_status(launch_norm_of_parts(parts, 0, norm, st));
 }
 
 // One row has no stride (whatever is given must not decide how it is read).
@@ -621,12 +674,18 @@ int demo_grad_norm(int count, const void* const* g, const int64_t* n, int dtype,
   if (s != DEMO_OK) return s;
   DeviceInfo dev;
   if ((s = device_info(&dev)) != DEMO_OK) return s;
-  ClipParams q;
   double* parts = static_cast<double*>(workspace);
-  int used = 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((s = launch_all_squares(&q, count, g, n, dtype, dev.sms, parts, &used, st)) != DEMO_OK) return s;
-  return to_status(launch_norm_of_parts(parts, used, norm, st));
+  if (count > kClipFew) {
+    ClipParams<kClipTensors> q;
+    return norm_of_list(&q, count, g, n, dtype, dev.sms, parts, norm, st);
+  }
+  ClipParams<kClipFew> q;
+  if (fill_small(&q, count, g, n, nullptr, elem_size(dtype), norm)) {
+    q.only_norm = 1;
+    return to_status(launch_small_clip(q, dtype, dtype, st));
+  }
+  return norm_of_list(&q, count, g, n, dtype, dev.sms, parts, norm, st);
 }
 
 int demo_clip_grads(int count, const void* const* g, const int64_t* n, int dtype, void* const* out, int out_dtype,
@@ -640,28 +699,20 @@ int demo_clip_grads(int count, const void* const* g, const int64_t* n, int dtype
   if (s != DEMO_OK) return s;
   DeviceInfo dev;
   if ((s = device_info(&dev)) != DEMO_OK) return s;
-  ClipParams q;
   double* parts = static_cast<double*>(workspace);
-  int used = 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!norm_given && (s = launch_all_squares(&q, count, g, n, dtype, dev.sms, parts, &used, st)) != DEMO_OK) return s;
-  bool any = false;
-  for (int from = 0; from < count;) {
-    from = fill_clip(&q, from, count, g, n, to, elem_size(dtype));
-    if (q.count == 0) break;
-    q.part_count = used;
-    q.all_parts = parts;
-    q.given = norm_given;
-    q.first_launch = !any;
-    q.in_place = 1;
-    for (int i = 0; i < q.count; ++i) q.in_place = q.in_place && q.out[i] == q.g[i];
-    q.max_norm = max_norm;
-    q.norm = norm;
-    if ((s = to_status(launch_scale(q, dtype, out_dtype, dev.sms, st))) != DEMO_OK) return s;
-    any = true;
+  if (count > kClipFew) {
+    ClipParams<kClipTensors> q;
+    return clip_list(&q, count, g, n, dtype, to, out_dtype, max_norm, dev.sms, parts, norm, norm_given, st);
   }
-  // Nothing to scale: the norm over nothing.
-  return any || norm_given ? DEMO_OK : to_status(launch_norm_of_parts(parts, 0, norm, st));
+  ClipParams<kClipFew> q;
+  if (!norm_given && fill_small(&q, count, g, n, to, elem_size(dtype), norm)) {
+    q.only_norm = 0;
+    q.in_place = all_in_place(q);
+    q.max_norm = max_norm;
+    return to_status(launch_small_clip(q, dtype, out_dtype, st));
+  }
+  return clip_list(&q, count, g, n, dtype, to, out_dtype, max_norm, dev.sms, parts, norm, norm_given, st);
 }
 
 int demo_fp8_matmul(const void* a_codes, const float* a_scales, int a_fmt, const void* b_codes, const float* b_scales,

@@ -159,27 +159,37 @@ constexpr int embed_piece(long long n, long long cols) {
   return piece;
 }
 
-// The gradients' norm and their scaling (see train_clip.cu): a launch takes up to kClipTensors tensors.
-constexpr int kClipTensors = 512;
-constexpr int kClipParts = 640;  // most CTAs of a launch, each of which leaves a sum
+// The gradients' norm and their scaling (see train_clip.cu): a launch takes up to CAP tensors.  The block is copied
+// with every launch (14 KB for 512 tensors), so short lists have a smaller one.
+template <int CAP>
 struct ClipParams {
-  const void* g[kClipTensors];
-  void* out[kClipTensors];
-  long long n[kClipTensors];
-  unsigned int start[kClipTensors];  // the tensor's first chunk; empty tensors are left out
+  static constexpr int kCap = CAP;
+  const void* g[CAP];
+  void* out[CAP];
+  long long n[CAP];
+  unsigned int start[CAP];  // the tensor's first chunk; empty tensors are left out
   int count, part_count;
   unsigned int chunks;
-  int given, first_launch, in_place;
+  int given, first_launch, in_place, only_norm;
   double max_norm;
   double* parts;            // this launch's sums
   const double* all_parts;  // every launch's
   float* norm;
 };
+constexpr int kClipTensors = 512, kClipFew = 64;
+constexpr int kClipParts = 640;  // most CTAs of a launch, each of which leaves a sum
 long long clip_chunks(uintptr_t address, long long n, int size);  // chunks of a tensor
-int clip_parts(const ClipParams& p, int dtype, int sms);                    // CTAs of its launch
-cudaError_t launch_squares(const ClipParams& p, int dtype, int sms, cudaStream_t st);
+int clip_parts(unsigned chunks, int dtype, int sms);              // CTAs of a launch
+// Norm and scaling of at most kSmallChunks chunks in one launch (the norm alone: `only_norm`).
+constexpr unsigned kSmallChunks = 64;
+static_assert(kSmallChunks <= kClipFew, "a chunk for each tensor at least");
+cudaError_t launch_small_clip(const ClipParams<kClipFew>& p, int dtype, int out_dtype, cudaStream_t st);
+// CAP kClipFew or kClipTensors
+template <int CAP>
+cudaError_t launch_squares(const ClipParams<CAP>& p, int dtype, int sms, cudaStream_t st);
+template <int CAP>
+cudaError_t launch_scale(const ClipParams<CAP>& p, int dtype, int out_dtype, int sms, cudaStream_t st);
 cudaError_t launch_norm_of_parts(const double* parts, int count, float* norm, cudaStream_t st);
-cudaError_t launch_scale(const ClipParams& p, int dtype, int out_dtype, int sms, cudaStream_t st);
 
 // out = a b^T (+ out): a [m][k], b [n][k] quantized by rows.
 struct MatmulParams {

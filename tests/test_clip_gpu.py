@@ -48,7 +48,10 @@ def grads(sizes, dtype, gap=0, offset=0, std=1.0, seed=90):
 
 # nothing, one element, parts of an access, a chunk of either width and one more, several chunks
 SIZES = [[1], [3], [4], [9], [0, 5, 0], [8191], [8192], [8193], [16384, 16385], [100000], [1, 2, 3, 4, 5, 6, 7, 8, 9],
-         [768, 768 * 768, 1, 40000, 768], [64] * 511, [7] * 513, [33] * 1100, [3000000, 5]]
+         [768, 768 * 768, 1, 40000, 768], [64] * 511, [7] * 513, [33] * 1100, [3000000, 5],
+         # around the longest list of one launch: 64 tensors, 64 chunks
+         [9] * 64, [9] * 65, [8192] * 64, [8191] * 64, [8192] * 63 + [8193], [524288], [524289], [1048576], [1048577],
+         [8192] * 65, [16384] * 63 + [0, 16384]]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
