@@ -14,8 +14,9 @@
 //
 // 16384 positions of bfloat16 added to 100352 x 2048: 51 us, 13 of them the sort (its launch, and two passes of
 // barriers and remote stores on eight SMs, with the others idle) and 38 the sums, 177 MB that cannot be done
-// without (26 us); written anew 163 us, 889 MB (131 us).  4096 positions into 32128 x 768 anew 31 us, 105 MB (15).
-// (L2 asked for dy by the idle SMs during the sort: no difference.)
+// without (26 us).  Written anew 138 us, 889 MB (131 us): zeros beside the sort, and beside the sums where no token
+// is.  4096 positions into 32128 x 768 anew 26 us, 105 MB (15).  (L2 asked for dy by the idle SMs during the sort: no
+// difference.)
 #include <cooperative_groups.h>
 
 #include "train_norm.cuh"
@@ -380,17 +381,17 @@ __device__ __forceinline__ void finish_row(const EmbedGradParams& p, long long t
 
 enum : int { kEnds = 1 << 16, kFinal = 1 << 17, kStarts = 1 << 18, kLive = 1 << 19 };
 
-// Columns of 32 rows that one warp zeroes: few where a row is looked for among 32 tokens, more where that is a search.
-constexpr int kZeroFew = 256, kZeroMany = 1024;
+constexpr int kZeroCols = 1024;  // columns of a warp's rows that it zeroes
 
-// Writes 0 to columns c0 .. c0 + most - 1 of a warp's rows r0 + (the set bits).
+// Writes 0 to columns c0 .. c0 + kZeroCols - 1 of a warp's rows r0 + (the set bits).
 template <bool VEC>
-__device__ __forceinline__ void zero_rows(const EmbedGradParams& p, long long r0, unsigned rows, int c0, int most, int lane) {
-  const int end = p.cols - c0 < most ? static_cast<int>(p.cols) : c0 + most;
-  // all 32, end to end from a 16-byte boundary: whole accesses whatever the width
+__device__ __forceinline__ void zero_rows(const EmbedGradParams& p, long long r0, unsigned rows, int c0, int lane) {
+  const int end = p.cols - c0 < kZeroCols ? static_cast<int>(p.cols) : c0 + kZeroCols;
+  // all of them, end to end from a 16-byte boundary: whole accesses whatever the width
   float* run = p.grad + r0 * p.ldg;
-  if (rows == 0xffffffffu && p.cols <= most && p.ldg == p.cols && (reinterpret_cast<uintptr_t>(run) & 15) == 0) {
-    for (long long u = lane; u < 8 * p.cols; u += 32) reinterpret_cast<float4*>(run)[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (rows == 0xffffffffu >> (32 - p.zero_rows) && p.cols <= kZeroCols && p.ldg == p.cols &&
+      (reinterpret_cast<uintptr_t>(run) & 15) == 0) {
+    for (long long u = lane; u < p.zero_rows * p.cols / 4; u += 32) reinterpret_cast<float4*>(run)[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     return;
   }
   while (rows != 0) {
@@ -462,6 +463,19 @@ __device__ __forceinline__ void sum_entries(const EmbedGradParams& p, int key, i
   }
 }
 
+// The first of the sorted keys lo .. hi - 1 that is not below `row`, hi if none: a warp looks at 32 at a time.
+__device__ __forceinline__ int first_key(const int* keys, int lo, int hi, long long row, int lane) {
+  while (lo < hi) {
+    const int step = (hi - lo + 32) / 33, at = lo + (lane + 1) * step - 1;  // the last of 32 runs of `step`
+    const unsigned below = __ballot_sync(0xffffffffu, at < hi && keys[at] < row);
+    const int runs = __popc(below);
+    lo += runs * step;
+    if (step == 1 && runs < 32) break;
+    if (runs < 32 && lo + step - 1 < hi) hi = lo + step - 1;
+  }
+  return lo;
+}
+
 // A warp sums one piece over one slab of columns.  What becomes of an entry follows from its key and those around
 // the piece, so every row that a batch needs is asked for at once: the rows of dy, and those of the gradient
 // that a token's sum is added to.  Blocks behind those write 0 to the rows that no token names, from `zero_from` on.
@@ -470,19 +484,20 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   kernel_begin();
   if (blockIdx.x >= p.sum_blocks) {
-    // 32 rows a warp: each lane looks its row up in the sorted keys, then the warp writes the absent ones.
+    // A few rows a warp: it finds their part of the sorted keys, each lane its row there; then it writes the absent ones.
     const long long z = static_cast<long long>(blockIdx.x - p.sum_blocks) * kSumWarps + warp, group = z / p.zero_slabs;
-    const long long r0 = p.zero_from + group * 32, r = r0 + lane;
-    int lo = 0, hi = p.n;
-    while (lo < hi) {
+    const long long r0 = p.zero_from + group * p.zero_rows, r = r0 + lane;
+    int lo = first_key(p.keys, 0, p.n, r0, lane);
+    const int end = first_key(p.keys, lo, p.n, r0 + p.zero_rows, lane);
+    for (int hi = end; lo < hi;) {
       const int mid = (lo + hi) / 2;
       if (p.keys[mid] < r)
         lo = mid + 1;
       else
         hi = mid;
     }
-    zero_rows<VEC>(p, r0, __ballot_sync(0xffffffffu, r < p.vocab && !(lo < p.n && p.keys[lo] == r)),
-                   static_cast<int>(z - group * p.zero_slabs) * kZeroMany, kZeroMany, lane);
+    zero_rows<VEC>(p, r0, __ballot_sync(0xffffffffu, lane < p.zero_rows && r < p.vocab && !(lo < end && p.keys[lo] == r)),
+                   static_cast<int>(z - group * p.zero_slabs) * kZeroCols, lane);
     return;
   }
   const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + warp;
@@ -508,11 +523,11 @@ __global__ void __launch_bounds__(kSumThreads) embed_few_kernel(const __grid_con
   const int key = t >= 0 && t < p.vocab ? static_cast<int>(t) : static_cast<int>(p.vocab);  // others last
   if (blockIdx.x >= p.sum_blocks) {
     const long long z = static_cast<long long>(blockIdx.x - p.sum_blocks) * kSumWarps + warp, group = z / p.zero_slabs;
-    const long long r0 = group * 32, r = r0 + lane;
+    const long long r0 = group * p.zero_rows, r = r0 + lane;
     bool named = false;
     for (int j = 0; j < p.n; ++j) named |= __shfl_sync(0xffffffffu, key, j) == r;
-    zero_rows<VEC>(p, r0, __ballot_sync(0xffffffffu, r < p.vocab && !named),
-                   static_cast<int>(z - group * p.zero_slabs) * kZeroFew, kZeroFew, lane);
+    zero_rows<VEC>(p, r0, __ballot_sync(0xffffffffu, lane < p.zero_rows && r < p.vocab && !named),
+                   static_cast<int>(z - group * p.zero_slabs) * kZeroCols, lane);
     return;
   }
   const int slab = static_cast<int>(blockIdx.x) * kSumWarps + warp;
@@ -617,10 +632,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const __gri
 
 namespace {
 
-// Blocks that zero rows from `from` on; sets how many warps share 32 rows.
-unsigned zero_blocks(EmbedGradParams& p, long long from, int cols) {
-  p.zero_slabs = static_cast<int>((p.cols + cols - 1) / cols);
-  const long long warps = from < p.vocab ? (p.vocab - from + 31) / 32 * p.zero_slabs : 0;
+// Blocks that zero rows from `from` on; sets what their warps take: 16 KB (8 to 24), as wide as the rows are, up to 32
+// rows.  4096 positions into 32128 x 768 25.6 us, 16384 into 100352 x 2048 138; warps with 1024 columns of 32 rows 42
+// and 146 (a few long ones are left at the end), with 128 columns of them 27 and 155 (pieces of 512 bytes).
+unsigned zero_blocks(EmbedGradParams& p, long long from) {
+  p.zero_rows = p.cols >= 1024 ? 4 : p.cols >= 512 ? 8 : p.cols >= 256 ? 16 : 32;
+  p.zero_slabs = static_cast<int>((p.cols + kZeroCols - 1) / kZeroCols);
+  const long long warps = from < p.vocab ? (p.vocab - from + p.zero_rows - 1) / p.zero_rows * p.zero_slabs : 0;
   return static_cast<unsigned>((warps + kSumWarps - 1) / kSumWarps);
 }
 
@@ -630,13 +648,13 @@ cudaError_t launch_sums(EmbedGradParams& p, const Tokens& tokens, cudaStream_t s
   p.slabs = static_cast<int>((p.cols + cols - 1) / cols);
   if (p.keys == nullptr) {  // few positions, not sorted
     p.sum_blocks = static_cast<unsigned>((p.slabs + kSumWarps - 1) / kSumWarps);
-    return launch_overlapped(embed_few_kernel<T, VEC>, p.sum_blocks + zero_blocks(p, p.add ? p.vocab : 0, kZeroFew), kSumThreads,
+    return launch_overlapped(embed_few_kernel<T, VEC>, p.sum_blocks + zero_blocks(p, p.add ? p.vocab : 0), kSumThreads,
                              0, st, p, tokens);
   }
   p.ldparts = static_cast<long long>(p.slabs) * cols;
   const long long pieces = (p.n + p.piece - 1) / p.piece, items = pieces * p.slabs;
   p.sum_blocks = static_cast<unsigned>((items + kSumWarps - 1) / kSumWarps);
-  const unsigned zero = zero_blocks(p, p.zero_from, kZeroMany);
+  const unsigned zero = zero_blocks(p, p.zero_from);
   const cudaError_t e = launch_overlapped(embed_sum_kernel<T, VEC>, p.sum_blocks + zero, kSumThreads, 0, st, p);
   if (e != cudaSuccess || pieces <= 1) return e;
   return launch_overlapped(embed_join_kernel<VEC>, static_cast<unsigned>((pieces + kJoinWarps - 1) / kJoinWarps * p.slabs),

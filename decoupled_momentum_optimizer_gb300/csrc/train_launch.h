@@ -138,16 +138,18 @@ struct EmbedGradParams {
   long long first, vocab, cols, lddy, ldg, ldparts;
   long long zero_from;  // rows from here on that no token names are written 0; vocab for none
   unsigned int sum_blocks;
-  int zero_slabs;  // warps that share 32 rows
+  int zero_rows, zero_slabs;  // rows that warps share (4 to 32), and those warps
   int n, piece, slabs, add;  // piece: 8, 16 or 32
   float scale;
 };
 cudaError_t launch_embed_grad(EmbedGradParams& p, const Tokens& tokens, int dtype, cudaStream_t st);
 cudaError_t prepare_embedding_kernels();
 
-// Bytes of the gradient that are filled while the tokens are sorted: 20 us of HBM, and what L2 holds (a table of 99 MB
-// filled there 29 us in all, with half of it left to the sums 46).
-constexpr long long kFillBytes = 128 << 20;
+// Bytes of the gradient that are filled while n tokens are sorted, about as many as take as long; the rest is left to
+// the sums' kernel, which asks of a few rows at a time whether a token is there.  4096 tokens into 32128 x 768: 25.7 us
+// with 48 MB filled beside the sort, 34.6 with none, 30.8 with all 99 MB; 65536 into 50304 x 768 72 us with 142 MB, 80
+// with 48.  Narrow rows make that question dear: 16384 into 500000 x 64 38 us with all filled, 44 with half.
+constexpr long long fill_bytes(long long n, long long cols) { return ((44ll << 20) + 1536 * n) * (cols < 128 ? 2 : 1); }
 
 // Sorted positions of a piece (one warp's work on 256 columns): 32, or fewer where those would leave an SM fewer
 // than three warps.  Sums and join, bfloat16 dy, us with 8 / 16 / 32 positions: 16384 x 2048 48 / 43 / 39, 4096 x

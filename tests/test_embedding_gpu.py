@@ -199,6 +199,19 @@ def test_grad_sums_as_float32_does():
     assert np.linalg.norm(got - want) <= 4 * 2.0 ** -24 * np.sqrt(n) * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("cols", [33, 128, 255, 300, 512, 767, 1000, 1024, 1033, 2056])
+@pytest.mark.parametrize("n,pad", [(40, 0), (3000, 0), (3000, 4), (9000, 3), (20, 5)])
+def test_grad_of_tables_longer_than_what_is_filled_first(n, pad, cols):
+    """Rows without a token that the sums' kernel writes: alone, in runs, at the end; beside the rows, nothing."""
+    vocab = (120 << 20) // (4 * cols) + 3
+    t = torch.randint(0, vocab, (n,), generator=torch.Generator().manual_seed(74))
+    t[: n // 2] = vocab - 1 - t[: n // 2] % 999  # a dense part at the end
+    buf = torch.full((vocab, cols + pad), float("nan"), device="cuda")
+    buf[:, cols:] = 5.0
+    check_grad(t.cuda(), draw(n, cols, "bf16", 75), vocab, out=buf[:, :cols])
+    assert bool((buf[:, cols:] == 5.0).all())
+
+
 def test_grad_past_32_bits():
     vocab, cols = (1 << 20) + 9, 4104
     t = torch.tensor([3, vocab - 1, vocab - 1, 3, 3]).cuda()
