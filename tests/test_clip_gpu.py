@@ -79,8 +79,9 @@ def test_norm_and_clip(sizes, gap, offset, dtype):
 @pytest.mark.parametrize("dtype,odt", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
 @pytest.mark.parametrize("gap,offset", [(0, 0), (1, 2), (8, 8), (3, 1)])
 @pytest.mark.parametrize("ratio", [0.25, 3.0])
-def test_clip_into_other_tensors(dtype, odt, gap, offset, ratio):
-    sizes = [5000, 1, 70001, 16, 9]
+@pytest.mark.parametrize("longest", [70001, 1500001])  # one launch, two
+def test_clip_into_other_tensors(dtype, odt, gap, offset, ratio, longest):
+    sizes = [5000, 1, longest, 16, 9]
     gs, buf = grads(sizes, dtype, offset, gap)
     before = buf.clone()
     out, obuf = grads(sizes, odt, gap, offset, seed=91)
@@ -178,8 +179,9 @@ def test_the_same_gradient_twice():
     assert bool((g == 1).all())
 
 
-def test_streams_repeats_and_graphs():
-    gs, buf = grads([768, 768 * 768, 40000, 5], "bf16", 3)
+@pytest.mark.parametrize("sizes", [[768, 768 * 768, 40000, 5], [768, 1500 * 1024, 40000, 5]], ids=["one launch", "two"])
+def test_streams_repeats_and_graphs(sizes):
+    gs, buf = grads(sizes, "bf16", 3)
     fresh = buf.clone()
     want = dm.grad_norm(gs)
     side = torch.cuda.Stream()
@@ -198,7 +200,7 @@ def test_streams_repeats_and_graphs():
     for k in (1.0, 2.0):
         buf.copy_(fresh * k)
         second.replay(), first.replay()
-        assert torch.equal(b, dm.grad_norm([(g * 1) for g in grads([768, 768 * 768, 40000, 5], "bf16", 3)[0][1:]]) * k)
+        assert torch.equal(b, dm.grad_norm([(g * 1) for g in grads(sizes, "bf16", 3)[0][1:]]) * k)
         assert torch.equal(a, want * k)
         if k == 1.0:
             assert torch.equal(buf, torch.where(torch.ones_like(buf, dtype=torch.bool), clipped, buf))
