@@ -468,8 +468,8 @@ int demo_embedding(const void* tokens, int token_bytes, int64_t token_rows, int6
  * Sums are float32 in an order that the tokens alone decide: no atomics, the same bits from call to call.
  *   dy          [positions, cols] of dtype;  grad float32 [vocab, cols];  tokens as above
  *   workspace   device, 16-byte aligned, at least demo_embedding_grad_workspace(positions, cols) bytes (host
- *               only; 0 for up to 32 positions, then it may be NULL), apart from the other buffers; fewer bytes give DEMO_ENOSPACE.  Its contents mean
- *               nothing between calls.
+ *               only; 0 for up to 32 positions, then it may be NULL), apart from the other buffers; fewer
+ *               bytes give DEMO_ENOSPACE.  Its contents mean nothing between calls.
  * More than 65536 positions are taken in runs of that many, the later ones added.
  */
 size_t demo_embedding_grad_workspace(int64_t n, int64_t cols);
