@@ -16,6 +16,7 @@ recorded (a result without history would end the branch's training without a wor
 import collections
 import ctypes
 import functools
+import warnings
 
 import torch
 
@@ -39,21 +40,34 @@ class _Library:
 _lib = _Library()
 
 
+@functools.lru_cache(maxsize=1)
+def _extension():
+    """The extension module (csrc/bind_ops.cpp), or None, with one warning, where it cannot be imported."""
+    import decoupled_momentum_optimizer_gb300 as dm
+
+    dm.lib()
+    try:
+        from decoupled_momentum_optimizer_gb300 import _bind_ops
+    except ImportError as e:
+        warnings.warn(f"the extension module is missing or was built for another torch ({e}): norm, embedding and "
+                      "clipping calls go through ctypes, which costs small ones several times as much.  Build it with "
+                      "python -m decoupled_momentum_optimizer_gb300.build", RuntimeWarning, stacklevel=4)
+        return None
+    return _bind_ops
+
+
+def _declined(*args):
+    return NotImplemented
+
+
 class _Bindings:
-    """The extension module's functions (csrc/bind_ops.cpp), bound on first use.  They take the plain calls,
-    several times faster than ctypes does, and answer NotImplemented to all others, which the Python code
-    below each of their calls then takes or refuses."""
+    """The extension module's functions, bound on first use.  They take the plain calls, several times faster than
+    ctypes does, and answer NotImplemented to all others, which the Python code below each of their calls then
+    takes or refuses; without the module that code takes every call."""
 
     def __getattr__(self, name):
-        import decoupled_momentum_optimizer_gb300 as dm
-
-        dm.lib()
-        try:
-            from decoupled_momentum_optimizer_gb300 import _bind_ops
-        except ImportError as e:
-            raise RuntimeError("the extension module is missing or was built for another torch: build it with "
-                               "python -m decoupled_momentum_optimizer_gb300.build") from e
-        setattr(self, name, getattr(_bind_ops, name))
+        module = _extension()
+        setattr(self, name, _declined if module is None else getattr(module, name))
         return getattr(self, name)
 
 
