@@ -9,6 +9,7 @@ generator first, so the constants always come from gen_dct_factors.py.
 import concurrent.futures
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -53,19 +54,31 @@ def _compile(src, build_dir, verbose):
     return obj, r.stderr
 
 
+def _cuda_include(nvcc):
+    """The folder of CUDA's headers beside nvcc, wherever PATH finds it (a link, say); None where there is none."""
+    path = shutil.which(nvcc)
+    for tool in (path, os.path.realpath(path)) if path else ():
+        include = os.path.join(os.path.dirname(os.path.dirname(tool)), "include")
+        if os.path.exists(os.path.join(include, "cuda_runtime.h")):
+            return include
+    return None
+
+
 def _bind(verbose):
     """Compile and link the extension module against the library and the torch that is installed."""
     import torch
 
+    if torch.version.cuda is None:
+        raise RuntimeError("the torch that is installed has no CUDA")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     tmp = BIND_PATH + ".tmp"
+    headers = [h for h in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), _cuda_include(_nvcc())) if h]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
-           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
-           os.path.join(CSRC, "bind_ops.cpp"), "-o", tmp, "-L", HERE, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN", "-L", lib,
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+           *[a for h in headers for a in ("-isystem", h)], os.path.join(CSRC, "bind_ops.cpp"), "-o", tmp, "-L", HERE,
+           f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the extension module did not build:\n{r.stdout}\n{r.stderr}")
@@ -74,13 +87,24 @@ def _bind(verbose):
     os.replace(tmp, BIND_PATH)
 
 
+def _try_bind(verbose):
+    """Build the extension module.  The library is complete without it (Python's calls then go through ctypes), so what
+    keeps it from being built is reported and not raised; an older one does not stay beside a newer library."""
+    try:
+        _bind(verbose)
+    except Exception as e:
+        if os.path.exists(BIND_PATH):
+            os.remove(BIND_PATH)
+        sys.stderr.write(f"{os.path.basename(BIND_PATH)} was not built, calls go through ctypes: {e}\n")
+
+
 def _torch():
     """Whether torch is installed (the library itself does without)."""
     return importlib.util.find_spec("torch") is not None
 
 
 def build(verbose=False, force=False):
-    """Compile and link the library, and the extension module where torch is installed; returns the library's path."""
+    """Compile and link the library, and the extension module where torch and g++ allow it; returns the library's path."""
     _regen_factors()
     build_dir = os.path.join(os.path.dirname(HERE), "_build")
     os.makedirs(build_dir, exist_ok=True)
@@ -92,7 +116,7 @@ def build(verbose=False, force=False):
 
     if current(LIB_PATH):
         if _torch() and not current(BIND_PATH):
-            _bind(verbose)
+            _try_bind(verbose)
         return LIB_PATH
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(lambda s: _compile(s, build_dir, verbose), SOURCES))
@@ -107,7 +131,7 @@ def build(verbose=False, force=False):
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
     if _torch():
-        _bind(verbose)
+        _try_bind(verbose)
     return LIB_PATH
 
 
