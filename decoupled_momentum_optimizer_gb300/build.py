@@ -19,7 +19,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_NAME = "libdemo_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-BIND_PATH = os.path.join(HERE, "_bind_ops.so")  # Python's way to the norm, embedding and clipping calls
+# Python's way to the norm, embedding and clipping calls, of one interpreter and one torch; which torch stands beside
+# the objects.
+BIND_PATH = os.path.join(HERE, "_bind_ops" + sysconfig.get_config_var("EXT_SUFFIX"))
+BIND_STAMP = os.path.join(os.path.dirname(HERE), "_build", "bind_ops_torch.txt")
 SOURCES = ["demo_api.cu", "demo_step.cu", "demo_encode.cu", "demo_decode.cu", "demo_decode_lanes.cu",
            "demo_decode_groups.cu", "demo_dense.cu", "demo_adamw.cu", "train_api.cu", "train_dropout.cu",
            "train_quantize.cu", "train_matmul.cu", "train_linear.cu", "train_norm.cu", "train_norm_grad.cu",
@@ -76,15 +79,24 @@ def _bind(verbose):
     headers = [h for h in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), _cuda_include(_nvcc())) if h]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
-           *[a for h in headers for a in ("-isystem", h)], os.path.join(CSRC, "bind_ops.cpp"), "-o", tmp, "-L", HERE,
+           f'-DDEMO_TORCH="{torch_tag(torch)}"', *[a for h in headers for a in ("-isystem", h)], os.path.join(CSRC, "bind_ops.cpp"), "-o", tmp, "-L", HERE,
            f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch_python"]
+    _forget_bind()
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the extension module did not build:\n{r.stdout}\n{r.stderr}")
     if verbose:
         sys.stderr.write(r.stderr)
     os.replace(tmp, BIND_PATH)
+    with open(BIND_STAMP, "w") as f:
+        f.write(_torch())
+
+
+def _forget_bind():
+    for path in (BIND_STAMP, BIND_PATH):
+        if os.path.exists(path):
+            os.remove(path)
 
 
 def _try_bind(verbose):
@@ -93,14 +105,35 @@ def _try_bind(verbose):
     try:
         _bind(verbose)
     except Exception as e:
-        if os.path.exists(BIND_PATH):
-            os.remove(BIND_PATH)
+        _forget_bind()
         sys.stderr.write(f"{os.path.basename(BIND_PATH)} was not built, calls go through ctypes: {e}\n")
 
 
+def torch_tag(torch):
+    """What names a torch whose tensors the module reads: compiled into it, and compared when it is imported."""
+    return f"{torch.__version__} {torch.version.git_version}"
+
+
 def _torch():
-    """Whether torch is installed (the library itself does without)."""
-    return importlib.util.find_spec("torch") is not None
+    """What the installed torch says of its version (read without importing it); None without one (the library itself does
+    without)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    try:
+        with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+            return f.read()
+    except OSError:
+        return spec.origin
+
+
+def _bound():
+    """The torch that the module was built against, None without one."""
+    try:
+        with open(BIND_STAMP) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def build(verbose=False, force=False):
@@ -115,7 +148,7 @@ def build(verbose=False, force=False):
         return not force and os.path.exists(path) and os.path.getmtime(path) >= newest
 
     if current(LIB_PATH):
-        if _torch() and not current(BIND_PATH):
+        if _torch() and (not current(BIND_PATH) or _bound() != _torch()):
             _try_bind(verbose)
         return LIB_PATH
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:

@@ -468,4 +468,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind_ops", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind_ops() { return PyModule_Create(&module); }
+// `torch` is the version that this file was compiled against: tensors are read through inlined accessors, so the module
+// is for that one alone.
+PyMODINIT_FUNC PyInit__bind_ops() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch", DEMO_TORCH) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

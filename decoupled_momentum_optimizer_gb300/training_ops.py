@@ -42,18 +42,24 @@ _lib = _Library()
 
 @functools.lru_cache(maxsize=1)
 def _extension():
-    """The extension module (csrc/bind_ops.cpp), or None, with one warning, where it cannot be imported."""
+    """The extension module (csrc/bind_ops.cpp), or None, with one warning, where there is none for this torch."""
     import decoupled_momentum_optimizer_gb300 as dm
+    from decoupled_momentum_optimizer_gb300 import build
 
     dm.lib()
     try:
         from decoupled_momentum_optimizer_gb300 import _bind_ops
     except ImportError as e:
-        warnings.warn(f"the extension module is missing or was built for another torch ({e}): norm, embedding and "
-                      "clipping calls go through ctypes, which costs small ones several times as much.  Build it with "
-                      "python -m decoupled_momentum_optimizer_gb300.build", RuntimeWarning, stacklevel=4)
-        return None
-    return _bind_ops
+        why = str(e)
+    else:  # it reads tensors as the torch that it was built against lays them out
+        built, here = getattr(_bind_ops, "torch", "another torch"), build.torch_tag(torch)
+        if built == here:
+            return _bind_ops
+        why = f"built against torch {built}, not {here}"
+    warnings.warn(f"no extension module for this torch ({why}): norm, embedding and clipping calls go through ctypes, which "
+                  "costs small ones several times as much.  Build it with python -m decoupled_momentum_optimizer_gb300.build",
+                  RuntimeWarning, stacklevel=4)
+    return None
 
 
 def _declined(*args):

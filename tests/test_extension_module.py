@@ -2,6 +2,8 @@
 
 import os
 import sys
+import sysconfig
+import types
 import warnings
 
 import pytest
@@ -61,6 +63,32 @@ def test_results_without_the_module(unbound):
     assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
 
 
+def test_a_module_for_another_torch_is_left_alone(unbound):
+    """It can be imported, and would read tensors by another layout: it takes no call."""
+    def call(*args):
+        raise AssertionError("the module was called")
+
+    stale = types.ModuleType(PACKAGE + "._bind_ops")
+    stale.rms_norm, stale.torch = call, "1.0 abc"
+    unbound.setattr(dm, "_bind_ops", stale, raising=False)
+    unbound.setitem(sys.modules, stale.__name__, stale)
+    for torch_of in ("1.0 abc", None):
+        if torch_of is None:
+            del stale.torch
+        ops._extension.cache_clear()
+        unbound.setattr(ops, "_bind", ops._Bindings())
+        with pytest.warns(RuntimeWarning, match="no extension module for this torch"):
+            with pytest.raises(ValueError, match="must be on a CUDA device"):
+                dm.rms_norm(X, X[0])
+
+
+def test_the_module_names_its_torch(unbound):
+    build.build()
+    if not os.path.exists(build.BIND_PATH):
+        pytest.skip("the module could not be built here")
+    assert ops._extension().torch == build.torch_tag(torch)
+
+
 # ---- building it ---------------------------------------------------------------------------------
 
 @pytest.fixture
@@ -71,7 +99,30 @@ def elsewhere(monkeypatch, tmp_path):
     path.write_bytes(b"")
     os.utime(path, (1, 1))
     monkeypatch.setattr(build, "BIND_PATH", str(path))
+    monkeypatch.setattr(build, "BIND_STAMP", str(tmp_path / "torch.txt"))
     return path
+
+
+def test_the_module_is_built_anew_for_another_torch(elsewhere, monkeypatch, tmp_path):
+    """The one and only reason here: its own torch is another than the one installed."""
+    built = []
+
+    def bind(verbose):
+        built.append(1)
+        (tmp_path / "torch.txt").write_text(build._torch())
+
+    monkeypatch.setattr(build, "_bind", bind)
+    os.utime(elsewhere)
+    (tmp_path / "torch.txt").write_text("__version__ = '1.0'")
+    build.build(), build.build()
+    assert len(built) == 1
+    (tmp_path / "torch.txt").unlink()  # not known: anew
+    build.build(), build.build()
+    assert len(built) == 2 and build._torch() != "__version__ = '1.0'"
+
+
+def test_a_module_is_of_one_interpreter():
+    assert build.BIND_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 @pytest.mark.parametrize("missing", ["compiler", "CUDA in torch", "torch that loads"])
@@ -82,7 +133,7 @@ def test_the_library_is_built_without_the_module(elsewhere, monkeypatch, capfd, 
     elif missing == "CUDA in torch":
         monkeypatch.setattr(torch.version, "cuda", None)
     else:
-        monkeypatch.setattr(build, "_torch", lambda: True)
+        monkeypatch.setattr(build, "_torch", lambda: "2")
         monkeypatch.setitem(sys.modules, "torch", None)
     assert build.build() == build.LIB_PATH
     assert not elsewhere.exists()
