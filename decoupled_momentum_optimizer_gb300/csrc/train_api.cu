@@ -647,8 +647,7 @@ int demo_embedding_grad(const void* tokens, int token_bytes, int64_t token_rows,
   t.cols = cols;
   t.ldg = q.ldg;
   // Written anew: what no token names is 0.  Without tokens the first kernel fills everything.
-  const int64_t fill = fill_bytes(std::min<int64_t>(n, w.batch), cols);
-  if (!add) t.filled = n == 0 ? vocab : std::min<int64_t>(vocab, (fill / 4 + cols - 1) / cols);
+  if (!add) t.filled = n == 0 ? vocab : filled_rows(w.batch, vocab, cols);
   q.zero_from = add ? vocab : t.filled;
   do {
     const int64_t left = n - first;

@@ -632,9 +632,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const __gri
 
 namespace {
 
-// Blocks that zero rows from `from` on; sets what their warps take: 16 KB (8 to 24), as wide as the rows are, up to 32
-// rows.  4096 positions into 32128 x 768 25.6 us, 16384 into 100352 x 2048 138; warps with 1024 columns of 32 rows 42
-// and 146 (a few long ones are left at the end), with 128 columns of them 27 and 155 (pieces of 512 bytes).
+// Blocks that zero rows from `from` on; sets what their warps take: 4, 8, 16 or 32 rows of up to 1024 columns, 16 to 32 KB
+// from 128 columns on, less where rows are narrower or a wide row's last columns are few.  4096 positions into 32128 x
+// 768 25.6 us, 16384 into 100352 x 2048 138; warps with 1024 columns of 32 rows 42 and 146 (a few long ones are left at the
+// end), with 128 columns of them 27 and 155 (pieces of 512 bytes).
 unsigned zero_blocks(EmbedGradParams& p, long long from) {
   p.zero_rows = p.cols >= 1024 ? 4 : p.cols >= 512 ? 8 : p.cols >= 256 ? 16 : 32;
   p.zero_slabs = static_cast<int>((p.cols + kZeroCols - 1) / kZeroCols);

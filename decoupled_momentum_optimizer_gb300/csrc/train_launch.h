@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "train_embed_plan.h"
 #include "train_plan.h"
 
 namespace demo {
@@ -144,22 +145,6 @@ struct EmbedGradParams {
 };
 cudaError_t launch_embed_grad(EmbedGradParams& p, const Tokens& tokens, int dtype, cudaStream_t st);
 cudaError_t prepare_embedding_kernels();
-
-// Bytes of the gradient that are filled while n tokens are sorted, about as many as take as long; the rest is left to
-// the sums' kernel, which asks of a few rows at a time whether a token is there.  4096 tokens into 32128 x 768: 25.7 us
-// with 48 MB filled beside the sort, 34.6 with none, 30.8 with all 99 MB; 65536 into 50304 x 768 72 us with 142 MB, 80
-// with 48.  Narrow rows make that question dear: 16384 into 500000 x 64 38 us with all filled, 44 with half.
-constexpr long long fill_bytes(long long n, long long cols) { return ((44ll << 20) + 1536 * n) * (cols < 128 ? 2 : 1); }
-
-// Sorted positions of a piece (one warp's work on 256 columns): 32, or fewer where those would leave an SM fewer
-// than three warps.  Sums and join, bfloat16 dy, us with 8 / 16 / 32 positions: 16384 x 2048 48 / 43 / 39, 4096 x
-// 768 10.3 / 10.8 / 11.7, 128 x 768 7.2 / 9.2 / 12.7; three tokens, 16384 x 32, 19 / 15 / 14.
-constexpr int embed_piece(long long n, long long cols) {
-  const long long slabs = (cols + 255) / 256;
-  int piece = 32;
-  while (piece > 8 && (n + piece - 1) / piece * slabs < 152 * 3) piece /= 2;
-  return piece;
-}
 
 // The gradients' norm and their scaling (see train_clip.cu): a launch takes up to CAP tensors.  The block is copied
 // with every launch (14 KB for 512 tensors), so short lists have a smaller one.
