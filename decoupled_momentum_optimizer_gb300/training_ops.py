@@ -608,7 +608,8 @@ def _embedding_workspace(n, cols):
 
 def embedding_grad(tokens, dy, vocab=None, *, scale=1.0, out=None, add=False, workspace=None, stream=None):
     """The gradient of :func:`embedding`'s table (demo_embedding_grad), float32 [vocab, cols]: ``scale`` times the
-    sum of the rows of ``dy`` [*tokens.shape, cols] for each token, in a fixed order.
+    sum of the rows of ``dy`` [*tokens.shape, cols] for each token, in an order that the tokens, their number and cols
+    decide.
 
     ``out``   a float32 [vocab, cols] to write (a slice of the flat gradient, say); a new tensor otherwise.  With
               ``add`` the sums are added to it, and rows that no token names stay as they are.

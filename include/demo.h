@@ -465,7 +465,9 @@ int demo_embedding(const void* tokens, int token_bytes, int64_t token_rows, int6
  * demo_embedding_grad -- the gradient of demo_embedding's table: for every token v in [0, vocab)
  *   grad[v] = scale * (the sum of dy[i] over the positions i with t_i = v)
  * added to what grad holds if add (rows that no token names are then not touched; otherwise they are 0).
- * Sums are float32 in an order that the tokens alone decide: no atomics, the same bits from call to call.
+ * Sums are float32 in an order that the tokens, their number and cols decide: no atomics, the same bits from call to
+ * call, whatever vocab, the strides, the tokens' width, add and the device are.  (A table cut by columns is summed
+ * in the order of its own cols: its bits need not be those of the whole table's columns.)
  *   dy          [positions, cols] of dtype;  grad float32 [vocab, cols];  tokens as above
  *   workspace   device, 16-byte aligned, at least demo_embedding_grad_workspace(positions, cols) bytes (host
  *               only; 0 for up to 32 positions, then it may be NULL), apart from the other buffers; fewer

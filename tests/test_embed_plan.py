@@ -43,3 +43,12 @@ def test_no_more_rows_are_filled_than_there_are(plan):
     sizes = [(4096, vocab, cols) for vocab in (1, 2, 3, 5, 1001, 32128) for cols in (1, 3, 64, 765)]
     assert all(rows <= vocab for (_, vocab, _), (rows, _) in zip(sizes, plan(sizes)))
     assert plan([(4096, 1001, 3)])[0][0] == 1001
+
+
+def test_pieces_follow_from_the_positions_and_the_columns(plan):
+    """The order of the sums is decided by both: columns of a table need not be summed as the whole table is."""
+    sizes = [(n, vocab, cols) for n in (33, 128, 4096, 65536) for vocab in (5, 32128, 2 ** 31 - 512) for cols in (1, 256, 768, 1024, 2048)]
+    pieces = {}
+    for (n, _, cols), (_, piece) in zip(sizes, plan(sizes)):
+        assert piece in (8, 16, 32) and pieces.setdefault((n, cols), piece) == piece
+    assert [pieces[4096, cols] for cols in (256, 768, 1024)] == [8, 16, 32]
