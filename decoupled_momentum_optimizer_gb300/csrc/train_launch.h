@@ -150,7 +150,6 @@ cudaError_t prepare_embedding_kernels();
 // with every launch (14 KB for 512 tensors), so short lists have a smaller one.
 template <int CAP>
 struct ClipParams {
-  static constexpr int kCap = CAP;
   const void* g[CAP];
   void* out[CAP];
   long long n[CAP];

@@ -254,10 +254,10 @@ template <typename T, typename W, bool VEC>
 cudaError_t launch_norm_grad_v(NormGradParams& p, int sms, cudaStream_t st) {
   constexpr int n = kNormN<T, VEC>, most = kGradThreads / 32;
   constexpr int u = kGradUnits<T, VEC, kGradThreads>;
+  static_assert(u == 4, "four accesses a lane: rows of one or two units are taken four or two at a time");
   const long long units = (p.cols + 32 * n - 1) / (32 * n);
   if (units == 1) return launch_norm_grad_u<T, W, VEC, 1, 4, kGradThreads>(p, units, sms, st);
   if (units == 2) return launch_norm_grad_u<T, W, VEC, 2, 2, kGradThreads>(p, units, sms, st);
-  if (u > 4 && units <= 4) return launch_norm_grad_u<T, W, VEC, 4, u / 4, kGradThreads>(p, units, sms, st);
   if (units <= u * most) return launch_norm_grad_u<T, W, VEC, u, 1, kGradThreads>(p, units, sms, st);
   constexpr int wide = kGradUnits<T, VEC, kGradWide>;
   if (units <= wide * most) return launch_norm_grad_u<T, W, VEC, wide, 1, kGradThreads>(p, units, sms, st);
