@@ -114,6 +114,11 @@ def _on_stream(stream, device, f, *args, **kw):
         return f(*args, **kw)
 
 
+def _followed(name):
+    raise ValueError(f"{name} requires a gradient, and this call records none: detach it, or call under "
+                     "torch.no_grad() or from a torch.autograd.Function")
+
+
 def _matrix(t, name, like=None, shape=None):
     """(pointer, row stride, rows, columns) of a tensor seen as rows of its last dimension."""
     try:
@@ -123,8 +128,7 @@ def _matrix(t, name, like=None, shape=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
     if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient, and this call records none: detach it, or call under "
-                         "torch.no_grad() or from a torch.autograd.Function")
+        _followed(name)
     if like is not None:
         if dt != like.dtype:
             raise TypeError(f"{name} has dtype {dt}, expected {like.dtype}")
@@ -398,6 +402,8 @@ def _row_values(t, name, rows, beside):
         raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} elements")
     if t.get_device() != beside.get_device():
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {beside.device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        _followed(name)
     return t.data_ptr()
 
 
@@ -671,16 +677,13 @@ def _refuse(g, name, dtype, device):
         raise ValueError(f"{name} is on {g.device}, the call's other tensors on {device}")
     if not g.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} requires a gradient, and this call records none: detach it, or call under "
-                     "torch.no_grad() or from a torch.autograd.Function")
+    _followed(name)
 
 
 def _scalar(t, name, beside):
     """(tensor, pointer) of a float32 scalar on the device, a new one where none is given."""
     if t is None:
         t = torch.empty((), dtype=torch.float32, device=beside.device)
-    elif t.requires_grad and torch.is_grad_enabled():
-        _refuse(t, name, t.dtype, t.device)
     return t, _row_values(t, name, 1, beside)
 
 
