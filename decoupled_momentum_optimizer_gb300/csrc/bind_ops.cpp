@@ -3,17 +3,19 @@
 // 12 to 35 us, most of it between the tensors and the C entry point; clipping 193 tensors took 300).
 //
 // These functions take the plain calls only.  Whatever they do not take (a wrong type, shape, device or
-// stride, a tensor that requires a gradient, another current device, an uninitialised library, no memory) they
+// stride, a tensor that autograd follows, another current device, an uninitialised library, no memory) they
 // leave to the Python bindings by returning NotImplemented, so every refusal and every error is raised in one
 // place.  A status that the library returns comes back as an int.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
@@ -41,11 +43,15 @@ const at::Tensor& tensor(PyObject* o) {
 // One call: its device (the first tensor's), which must be the current one.
 struct Call {
   bool recorded = c10::GradMode::is_enabled();
+  // A level of forward-mode tangents is open, and they are followed (they are not within an autograd.Function).
+  bool tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode() &&
+                  torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr;
   int device = -1;
 
   const at::Tensor& take(PyObject* o) {
     const at::Tensor& t = tensor(o);
     if (!t.is_cuda() || (recorded && t.requires_grad())) throw Other();
+    if (tangents && t._fw_grad(0).defined()) throw Other();
     const int d = static_cast<int>(t.get_device());
     if (device < 0) {
       if (c10::cuda::current_device() != d) throw Other();

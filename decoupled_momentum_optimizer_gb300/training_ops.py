@@ -8,9 +8,9 @@ torch unless an ``out`` is given, the call runs on torch's current stream (or on
 were the current one) and raises :class:`DemoError` on a negative status.
 
 The calls record nothing for autograd.  A tensor that requires a gradient is refused while gradients are
-recorded (a result without history would end the branch's training without a word): call them from a
-``torch.autograd.Function``, whose backward is the call that each docstring names, or under
-``torch.no_grad()``.
+recorded (a result without history would end the branch's training without a word), and so is one with a
+forward-mode tangent: call them from a ``torch.autograd.Function``, whose backward is the call that each docstring
+names, or, without a tangent, under ``torch.no_grad()``.
 """
 
 import collections
@@ -19,6 +19,7 @@ import functools
 import warnings
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 FP8_FORMATS = {"e4m3": (0, torch.float8_e4m3fn), "e5m2": (1, torch.float8_e5m2)}
@@ -114,9 +115,14 @@ def _on_stream(stream, device, f, *args, **kw):
         return f(*args, **kw)
 
 
-def _followed(name):
-    raise ValueError(f"{name} requires a gradient, and this call records none: detach it, or call under "
-                     "torch.no_grad() or from a torch.autograd.Function")
+def _unfollowed(t, name):
+    """Refuses a tensor that autograd follows: backward, or forward while a level of tangents is open."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, and this call records none: detach it, or call under "
+                         "torch.no_grad() or from a torch.autograd.Function")
+    if _forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled() and _forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} has a forward-mode tangent, and this call computes none: detach it, or call from a "
+                         "torch.autograd.Function")
 
 
 def _matrix(t, name, like=None, shape=None):
@@ -127,8 +133,8 @@ def _matrix(t, name, like=None, shape=None):
         raise TypeError(f"{name} must be a torch.Tensor") from None
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
-    if t.requires_grad and torch.is_grad_enabled():
-        _followed(name)
+    if t.requires_grad or _forward_ad._current_level >= 0:
+        _unfollowed(t, name)
     if like is not None:
         if dt != like.dtype:
             raise TypeError(f"{name} has dtype {dt}, expected {like.dtype}")
@@ -402,8 +408,8 @@ def _row_values(t, name, rows, beside):
         raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} elements")
     if t.get_device() != beside.get_device():
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {beside.device}")
-    if t.requires_grad and torch.is_grad_enabled():
-        _followed(name)
+    if t.requires_grad or _forward_ad._current_level >= 0:
+        _unfollowed(t, name)
     return t.data_ptr()
 
 
@@ -659,10 +665,10 @@ def _grads(gs, name):
     dt, index = gs[0].dtype, gs[0].get_device()
     if dt not in _DTYPES:
         raise TypeError(f"{name} have dtype {dt}, expected float32, bfloat16 or float16")
-    recorded = torch.is_grad_enabled()
+    open_level = _forward_ad._current_level >= 0
     for r, g in enumerate(gs):
         if g.dtype != dt or g.get_device() != index or not g.is_cuda or not g.is_contiguous() or \
-                (recorded and g.requires_grad):
+                g.requires_grad or open_level:
             _refuse(g, f"{name}[{r}]", dt, gs[0].device)
     return gs, count, (ctypes.c_void_p * count)(*[g.data_ptr() for g in gs]), \
         (ctypes.c_int64 * count)(*[g.numel() for g in gs])
@@ -677,7 +683,7 @@ def _refuse(g, name, dtype, device):
         raise ValueError(f"{name} is on {g.device}, the call's other tensors on {device}")
     if not g.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    _followed(name)
+    _unfollowed(g, name)
 
 
 def _scalar(t, name, beside):
