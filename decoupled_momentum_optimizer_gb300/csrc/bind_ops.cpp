@@ -47,6 +47,7 @@ struct Call {
   bool tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode() &&
                   torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr;
   int device = -1;
+  std::vector<c10::TensorImpl*> written;  // given tensors that the call writes
 
   const at::Tensor& take(PyObject* o) {
     const at::Tensor& t = tensor(o);
@@ -60,6 +61,16 @@ struct Call {
       throw Other();
     }
     return t;
+  }
+  const at::Tensor& take_written(PyObject* o) {
+    const at::Tensor& t = take(o);
+    written.push_back(t.unsafeGetTensorImpl());
+    return t;
+  }
+  // What autograd saved of them before is out of date (tensors of inference mode have no count).
+  void count_written() const {
+    for (c10::TensorImpl* t : written)
+      if (!t->is_inference()) t->bump_version();
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream(); }
   at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const {
@@ -92,8 +103,7 @@ Matrix matrix(const at::Tensor& t) {
   return m;
 }
 
-Matrix like(Call& call, PyObject* o, const at::Tensor& x) {
-  const at::Tensor& t = call.take(o);
+Matrix like(const at::Tensor& t, const at::Tensor& x) {
   if (t.scalar_type() != x.scalar_type() || t.sizes() != x.sizes()) throw Other();
   return matrix(t);
 }
@@ -173,11 +183,12 @@ struct Results {
   ~Results() { Py_XDECREF(p); }
   void set(Py_ssize_t i, PyObject* o) { PyTuple_SET_ITEM(p, i, o); }
   // The results where the library took the call; its status otherwise, or NotImplemented where it was not ready.
-  PyObject* after(int status) {
+  PyObject* after(const Call& call, int status) {
     if (status != DEMO_OK) {
       if (status == DEMO_ENOTINIT) throw Other();
       return PyLong_FromLong(status);
     }
+    call.count_written();
     PyObject* o = p;
     p = nullptr;
     return o;
@@ -211,9 +222,9 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Matrix mr, mt, mo;
     at::Tensor total, out, rstd, codes[2], scales[2];
     if (given(a[3])) {
-      mr = like(call, a[3], x);
+      mr = like(call.take(a[3]), x);
       if (given(a[9])) {
-        mt = like(call, a[9], x);
+        mt = like(call.take_written(a[9]), x);
       } else {
         total = call.empty(x.sizes(), x.scalar_type());
         mt = Matrix{total.data_ptr(), mx.cols};
@@ -222,7 +233,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       throw Other();
     }
     if (given(a[8])) {
-      mo = like(call, a[8], x);
+      mo = like(call.take_written(a[8]), x);
     } else if (truth(a[4])) {
       out = call.empty(x.sizes(), x.scalar_type());
       mo = Matrix{out.data_ptr(), mx.cols};
@@ -239,7 +250,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* factors = nullptr;
     const bool save = truth(a[7]);
     if (given(a[10])) {
-      factors = floats(call.take(a[10]), mx.rows);
+      factors = floats(call.take_written(a[10]), mx.rows);
     } else if (save || (form & 2)) {
       rstd = call.empty({mx.rows}, at::kFloat);
       factors = static_cast<float*>(rstd.data_ptr());
@@ -254,10 +265,10 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       r.set(4 + 2 * f, wrap_or_none(scales[f]));
       r.set(7 + f, whole_number(sizes[f]));
     }
-    return r.after(demo_rms_norm(mx.p, mx.ld, mr.p, mr.ld, dtype, weight, weight_dtype, mx.rows, mx.cols, eps, mt.p, mt.ld, mo.p,
-                                 mo.ld, factors, static_cast<int>(fmt), at_ptr(codes[0]),
-                                 static_cast<float*>(at_ptr(scales[0])), at_ptr(codes[1]),
-                                 static_cast<float*>(at_ptr(scales[1])), call.stream()));
+    return r.after(call, demo_rms_norm(mx.p, mx.ld, mr.p, mr.ld, dtype, weight, weight_dtype, mx.rows, mx.cols, eps, mt.p,
+                                       mt.ld, mo.p, mo.ld, factors, static_cast<int>(fmt), at_ptr(codes[0]),
+                                       static_cast<float*>(at_ptr(scales[0])), at_ptr(codes[1]),
+                                       static_cast<float*>(at_ptr(scales[1])), call.stream()));
   });
 }
 
@@ -267,15 +278,15 @@ PyObject* rms_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call call;
     const at::Tensor& dy = call.take(a[0]);
     const int dtype = code_of(dy.scalar_type());
-    const Matrix md = matrix(dy), mt = like(call, a[1], dy);
+    const Matrix md = matrix(dy), mt = like(call.take(a[1]), dy);
     int weight_dtype;
     const void* weight = weight_of(call, a[2], dy, md.cols, &weight_dtype);
     const float* rstd = floats(call.take(a[3]), md.rows);
     Matrix mp, mo;
-    if (given(a[4])) mp = like(call, a[4], dy);
+    if (given(a[4])) mp = like(call.take(a[4]), dy);
     at::Tensor out, dweight, work;
     if (given(a[5])) {
-      mo = like(call, a[5], dy);
+      mo = like(call.take_written(a[5]), dy);
     } else {
       out = call.empty(dy.sizes(), dy.scalar_type());
       mo = Matrix{out.data_ptr(), md.cols};
@@ -285,7 +296,7 @@ PyObject* rms_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     size_t need = 0;
     if (truth(a[8])) {
       if (given(a[6])) {
-        dw = floats(call.take(a[6]), md.cols);
+        dw = floats(call.take_written(a[6]), md.cols);
       } else {
         if (add) throw Other();
         dweight = call.empty({md.cols}, at::kFloat);
@@ -299,9 +310,9 @@ PyObject* rms_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Results r(2);
     r.set(0, passed(a[5], out));
     r.set(1, passed(a[6], dweight));
-    return r.after(demo_rms_norm_grad(md.p, md.ld, mt.p, mt.ld, dtype, weight, weight_dtype, rstd, md.rows, md.cols, mp.p,
-                                      mp.ld, mo.p, mo.ld, dw, add, need > 0 ? work.data_ptr() : nullptr, need,
-                                      call.stream()));
+    return r.after(call, demo_rms_norm_grad(md.p, md.ld, mt.p, mt.ld, dtype, weight, weight_dtype, rstd, md.rows, md.cols,
+                                            mp.p, mp.ld, mo.p, mo.ld, dw, add, need > 0 ? work.data_ptr() : nullptr, need,
+                                            call.stream()));
   });
 }
 
@@ -326,7 +337,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Matrix mo;
     at::ScalarType type = table.scalar_type();
     if (given(a[4])) {
-      const at::Tensor& o = call.take(a[4]);
+      const at::Tensor& o = call.take_written(a[4]);
       if (given(a[3]) || o.sizes() != at::IntArrayRef(rows_shape(tokens, mt.cols))) throw Other();
       type = o.scalar_type();
       mo = matrix(o);
@@ -341,8 +352,8 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const int table_code = code_of(table.scalar_type()), code = code_of(type);
     Results r(passed(a[4], out));
-    return r.after(demo_embedding(t.p, t.bytes, t.rows, t.cols, t.ld, mt.p, mt.ld, table_code, mt.rows, mt.cols, scale, mo.p,
-                                  mo.ld, code, call.stream()));
+    return r.after(call, demo_embedding(t.p, t.bytes, t.rows, t.cols, t.ld, mt.p, mt.ld, table_code, mt.rows, mt.cols, scale,
+                                        mo.p, mo.ld, code, call.stream()));
   });
 }
 
@@ -368,7 +379,7 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out;
     Matrix mo;
     if (given(a[4])) {
-      const at::Tensor& o = call.take(a[4]);
+      const at::Tensor& o = call.take_written(a[4]);
       if (o.dim() != 2 || o.scalar_type() != at::kFloat || o.size(1) != md.cols || (vocab >= 0 && o.size(0) != vocab)) throw Other();
       mo = matrix(o);
     } else {
@@ -381,9 +392,9 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (need > 0) work = call.empty({static_cast<int64_t>(need)}, at::kByte);
     const int code = code_of(dy.scalar_type());
     Results r(passed(a[4], out));
-    return r.after(demo_embedding_grad(t.p, t.bytes, t.rows, t.cols, t.ld, md.p, md.ld, code, mo.rows, mo.cols, scale,
-                                       static_cast<float*>(mo.p), mo.ld, add, need > 0 ? work.data_ptr() : nullptr, need,
-                                       call.stream()));
+    return r.after(call, demo_embedding_grad(t.p, t.bytes, t.rows, t.cols, t.ld, md.p, md.ld, code, mo.rows, mo.cols, scale,
+                                             static_cast<float*>(mo.p), mo.ld, add,
+                                             need > 0 ? work.data_ptr() : nullptr, need, call.stream()));
   });
 }
 
@@ -393,9 +404,9 @@ struct List {
   std::vector<int64_t> n;
   int dtype = 0;
 
-  List(Call& call, PyObject* o) {
+  List(Call& call, PyObject* o, bool written) {
     if (THPVariable_Check(o)) {
-      add(call, o);
+      add(call, o, written);
       return;
     }
     if (!PyList_Check(o) && !PyTuple_Check(o)) throw Other();
@@ -403,10 +414,11 @@ struct List {
     if (count == 0) throw Other();
     p.reserve(static_cast<size_t>(count));
     n.reserve(static_cast<size_t>(count));
-    for (Py_ssize_t i = 0; i < count; ++i) add(call, PySequence_Fast_GET_ITEM(o, i));
+    if (written) call.written.reserve(static_cast<size_t>(count));
+    for (Py_ssize_t i = 0; i < count; ++i) add(call, PySequence_Fast_GET_ITEM(o, i), written);
   }
-  void add(Call& call, PyObject* o) {
-    const at::Tensor& t = call.take(o);
+  void add(Call& call, PyObject* o, bool written) {
+    const at::Tensor& t = written ? call.take_written(o) : call.take(o);
     const int code = code_of(t.scalar_type());
     if (p.empty())
       dtype = code;
@@ -423,9 +435,9 @@ struct List {
 PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return plain(n, 2, [&]() -> PyObject* {
     Call call;
-    const List g(call, a[0]);
+    const List g(call, a[0], false);
     at::Tensor norm;
-    float* np = given(a[1]) ? floats(call.take(a[1]), 1) : nullptr;
+    float* np = given(a[1]) ? floats(call.take_written(a[1]), 1) : nullptr;
     if (np == nullptr) {
       norm = call.empty({}, at::kFloat);
       np = static_cast<float*>(norm.data_ptr());
@@ -433,7 +445,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t need = demo_grad_workspace(g.count());
     const at::Tensor work = call.empty({static_cast<int64_t>(need)}, at::kByte);
     Results r(passed(a[1], norm));
-    return r.after(demo_grad_norm(g.count(), g.p.data(), g.n.data(), g.dtype, np, work.data_ptr(), need, call.stream()));
+    return r.after(call, demo_grad_norm(g.count(), g.p.data(), g.n.data(), g.dtype, np, work.data_ptr(), need, call.stream()));
   });
 }
 
@@ -441,7 +453,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return plain(n, 4, [&]() -> PyObject* {
     Call call;
-    const List g(call, a[0]);
+    const List g(call, a[0], !given(a[3]));
     const double max_norm = number(a[1]);
     at::Tensor norm, work;
     float* np = given(a[2]) ? floats(call.take(a[2]), 1) : nullptr;
@@ -456,14 +468,14 @@ PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int out_dtype = g.dtype;
     std::optional<List> o;
     if (given(a[3])) {
-      o.emplace(call, a[3]);
+      o.emplace(call, a[3], true);
       if (o->n != g.n) throw Other();
       to = o->p.data();
       out_dtype = o->dtype;
     }
     Results r(passed(a[2], norm));
-    return r.after(demo_clip_grads(g.count(), g.p.data(), g.n.data(), g.dtype, to, out_dtype, max_norm, np, given(a[2]),
-                                   need > 0 ? work.data_ptr() : nullptr, need, call.stream()));
+    return r.after(call, demo_clip_grads(g.count(), g.p.data(), g.n.data(), g.dtype, to, out_dtype, max_norm, np,
+                                         given(a[2]), need > 0 ? work.data_ptr() : nullptr, need, call.stream()));
   });
 }
 

@@ -10,7 +10,8 @@ were the current one) and raises :class:`DemoError` on a negative status.
 The calls record nothing for autograd.  A tensor that requires a gradient is refused while gradients are
 recorded (a result without history would end the branch's training without a word), and so is one with a
 forward-mode tangent: call them from a ``torch.autograd.Function``, whose backward is the call that each docstring
-names, or, without a tangent, under ``torch.no_grad()``.
+names, or, without a tangent, under ``torch.no_grad()``.  What a call writes of the tensors that it is given counts as
+modified in place, as with torch's own ``out=`` (slices of a buffer share the count).
 """
 
 import collections
@@ -84,6 +85,17 @@ _bind = _Bindings()
 def _refused(status, name):
     """Raises for the status that a call of the extension module came back with."""
     _lib.dm__check(status, name)
+
+
+# What a call writes of the tensors that it is given counts as modified in place, so that autograd notices where it saved
+# one of them before.
+_wrote = torch.autograd.graph.increment_version
+
+
+def _written(*given):
+    for t in given:
+        if t is not None:
+            _wrote((t.codes, t.scales) if isinstance(t, Fp8Matrix) else t)
 
 
 _FORM_CODES = {None: 0, "rows": 1, "cols": 2, "both": 3}
@@ -178,6 +190,7 @@ def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
         return _on_stream(stream, x.device, dropout, x, p, seed=seed, step=step, site=site, residual=residual, out=out)
     xp, ldx, rows, cols = _matrix(x, "x")
     rp, ldr = _matrix(residual, "residual", x)[:2] if residual is not None else (None, 0)
+    given = out
     if out is None:
         out = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
         op, ldo = out.data_ptr(), cols
@@ -185,6 +198,8 @@ def dropout(x, p, *, seed, step, site=0, residual=None, out=None, stream=None):
         op, ldo = _matrix(out, "out", x)[:2]
     _run("demo_dropout", (xp, ldx, rp, ldr, op, ldo, _DTYPES[x.dtype], rows, cols, p, seed, step, site),
          x.get_device())
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -282,6 +297,7 @@ def fp8_quantize(x, *, fmt="e4m3", form="rows", scales="rows", relu=False, gate=
     else:
         raise ValueError(f"form is {form!r}, expected rows, cols or both")
     cr = sr = cc = sc = None
+    given = by_rows, by_cols
     if form != "cols":
         by_rows = _form(by_rows, rows, cols, fmt, tiles, x)
         cr, sr = by_rows.codes.data_ptr(), by_rows.scales.data_ptr()
@@ -290,6 +306,8 @@ def fp8_quantize(x, *, fmt="e4m3", form="rows", scales="rows", relu=False, gate=
         cc, sc = by_cols.codes.data_ptr(), by_cols.scales.data_ptr()
     _run("demo_fp8_quantize", (xp, ldx, _DTYPES[x.dtype], rows, cols, bool(relu), gp, ldg, p, seed, step, site,
                                FP8_FORMATS[fmt][0], tiles, cr, sr, cc, sc), x.get_device())
+    if out is not None:
+        _written(*given)
     return (by_rows, by_cols) if form == "both" else by_rows if by_cols is None else by_cols
 
 
@@ -342,9 +360,12 @@ def fp8_matmul(a, b, *, out=None, dtype=None, add=False, stream=None):
         raise ValueError(f"a is on {ac.device}, b on {bc.device}")
     if add and out is None:
         raise ValueError("add needs an out to add to")
+    given = out
     out, op, ldo, dt = _out(out, (m, n), _result_dtype(out, dtype, torch.bfloat16), ac)
     _run("demo_fp8_matmul", (ac.data_ptr(), a.scales.data_ptr(), _FMT_OF[ac.dtype], bc.data_ptr(),
                              b.scales.data_ptr(), _FMT_OF[bc.dtype], m, n, k, op, ldo, dt, bool(add)), index)
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -371,6 +392,7 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
     lead = x.shape[:-1]
     if k == 0:
         m = lead.numel()
+    given = out
     out, op, ldo, odt = _out(out, (*lead, n), _result_dtype(out, dtype, x.dtype), x)
     need = _linear_workspace(m, n, k)
     wp = None
@@ -382,6 +404,8 @@ def fp8_linear(x, w, *, out=None, dtype=None, workspace=None, stream=None):
         wp, need = workspace.data_ptr(), workspace.numel()
     _run("demo_fp8_linear", (xp, ldx, _DTYPES[x.dtype], wc.data_ptr(), w.scales.data_ptr(), _FMT_OF[wc.dtype], m, n, k,
                              op, ldo, odt, wp, need), index)
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -464,6 +488,7 @@ def rms_norm(x, weight, *, eps=1e-6, residual=None, values=True, form=None, fmt=
     xp, ldx, rows, cols = _matrix(x, "x")
     wp, wdt = _weight(weight, x, cols)
     rp, ldr, tp, ldt = None, 0, None, 0
+    given = [out, total, rstd]
     if residual is not None:
         rp, ldr = _matrix(residual, "residual", x)[:2]
         if total is None:
@@ -491,6 +516,7 @@ def rms_norm(x, weight, *, eps=1e-6, residual=None, values=True, form=None, fmt=
             by_cols = quantized
         else:
             raise ValueError(f"form is {form!r}, expected rows, cols or both")
+        given += by_rows, by_cols
         if form != "cols":
             by_rows = _form(by_rows, rows, cols, fmt, False, x)
             cr, sr = by_rows.codes.data_ptr(), by_rows.scales.data_ptr()
@@ -505,6 +531,7 @@ def rms_norm(x, weight, *, eps=1e-6, residual=None, values=True, form=None, fmt=
     sp = _row_values(factors, "rstd", _flat_rows(x), x) if factors is not None else None
     _run("demo_rms_norm", (xp, ldx, rp, ldr, _DTYPES[x.dtype], wp, wdt, rows, cols, eps, tp, ldt, op, ldo, sp,
                            FP8_FORMATS[fmt][0], cr, sr, cc, sc), x.get_device())
+    _written(*given)
     return Normed(out, (by_rows, by_cols) if form == "both" else by_cols if by_rows is None else by_rows,
                   x if residual is None else total, factors if save or rstd is not None else None)
 
@@ -538,6 +565,7 @@ def rms_norm_grad(dy, total, weight, rstd, *, past=None, out=None, dweight=None,
     wp, wdt = _weight(weight, dy, cols)
     sp = _row_values(rstd, "rstd", _flat_rows(dy), dy)
     pp, ldp = _matrix(past, "past", dy)[:2] if past is not None else (None, 0)
+    given = out, dweight
     if out is None:
         out = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
         op, ldo = out.data_ptr(), cols
@@ -556,6 +584,7 @@ def rms_norm_grad(dy, total, weight, rstd, *, past=None, out=None, dweight=None,
         raise ValueError("dweight is given, and weight_grad is False")
     _run("demo_rms_norm_grad", (dp, ldd, tp, ldt, _DTYPES[dy.dtype], wp, wdt, sp, rows, cols, pp, ldp, op, ldo, gp, bool(add),
                                 wsp, need), dy.get_device())
+    _written(*given)
     return out, dweight
 
 
@@ -607,9 +636,11 @@ def embedding(tokens, table, *, scale=1.0, dtype=None, out=None, stream=None):
         raise ValueError(f"table has {table.dim()} dimensions, expected 2")
     if tokens.get_device() != table.get_device():
         raise ValueError(f"tokens are on {tokens.device}, the table on {table.device}")
+    given = out
     out, op, ldo, odt = _out(out, (*tokens.shape, cols), _result_dtype(out, dtype, table.dtype), table)
     _run("demo_embedding", (kp, size, krows, kcols, ldk, tp, ldt, _DTYPES[table.dtype], vocab, cols, scale, op, ldo, odt),
          table.get_device())
+    _written(given)
     return out
 
 
@@ -649,10 +680,12 @@ def embedding_grad(tokens, dy, vocab=None, *, scale=1.0, out=None, add=False, wo
         raise ValueError(f"out has shape {tuple(out.shape)}, expected [{'vocab' if vocab is None else vocab}, {cols}]")
     else:
         vocab = out.shape[0]
+    given = out
     out, gp, ldg, _ = _out(out, (vocab, cols), torch.float32, dy)
     workspace, wsp, need = _workspace(workspace, _embedding_workspace(n, cols), dy)
     _run("demo_embedding_grad", (kp, size, krows, kcols, ldk, dp, ldd, _DTYPES[dy.dtype], vocab, cols, scale, gp, ldg,
                                  bool(add), wsp, need), dy.get_device())
+    _written(given)
     return out
 
 
@@ -711,9 +744,11 @@ def grad_norm(gs, *, out=None, workspace=None, stream=None):
         first = gs if isinstance(gs, torch.Tensor) else gs[0]
         return _on_stream(stream, first.device, grad_norm, gs, out=out, workspace=workspace)
     gs, count, ptrs, sizes = _grads(gs, "gradients")
+    given = out
     out, op = _scalar(out, "out", gs[0])
     workspace, wsp, need = _workspace(workspace, _grad_workspace(count), gs[0])
     _run("demo_grad_norm", (count, ptrs, sizes, _DTYPES[gs[0].dtype], op, wsp, need), gs[0].get_device())
+    _written(given)
     return out
 
 
@@ -749,4 +784,5 @@ def clip_grads(gs, max_norm, *, norm=None, out=None, workspace=None, stream=None
     workspace, wsp, need = _workspace(workspace, 0 if given else _grad_workspace(count), gs[0])
     _run("demo_clip_grads", (count, ptrs, sizes, _DTYPES[gs[0].dtype], outs, _DTYPES[odt], max_norm, normp, given, wsp, need),
          gs[0].get_device())
+    _wrote(list(gs if out is None else out))
     return norm
