@@ -18,7 +18,7 @@
 // 193 float32 tensors of 157 million elements: the norm 94 us (6.7 TB/s), clipped into others 300 us; in bfloat16 157
 // us.  (The second read starts at the first one's end, for what L2 still holds: in order 302 and 165 us.)
 // 2^27 bfloat16 elements that need no clipping 46.5 us, of 39.4 for their bytes.  Lists of up to 64 chunks are one
-// cluster's, in one launch.
+// cluster's, in one launch: shorter calls where nothing is scaled, longer ones where something is and in graphs.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -243,10 +243,9 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas<T>) scale_kernel(const
     scale_chunk<T, O>(p, Chunk<T>(p, p.chunks - 1 - i, threadIdx.x), f);
 }
 
-// A few chunks in one launch: a cluster's CTAs add up each other's sums in CTA order, and scale what they read.
-// 17 tensors, 70,000 elements: 5.4 us on the device against 4.6 for two launches, which overlap; but a call takes the
-// longer of that and of its issue, 6.5 us against 7.9, so 5.9 us against 7.9.  57 tensors of 2 to 1,310 elements 8.5 us
-// against 12.
+// A few chunks in one launch: a cluster's CTAs add up each other's sums in CTA order, and scale what they read.  A call of
+// a short list takes the longer of the device's time and its issue, about 3 us a launch; from a graph two launches are
+// faster, as they overlap and have a CTA for each chunk (see kSmallChunks for both sides).
 constexpr int kSmallThreads = 512, kSmallCtas = 8, kSmallTeams = kSmallCtas * (kSmallThreads / kClipThreads);
 
 template <typename T, typename O>

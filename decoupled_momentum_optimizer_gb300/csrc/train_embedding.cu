@@ -65,8 +65,8 @@ __device__ __forceinline__ void store_wide(T* p, const float (&v)[N]) {
 // Lookup
 // ----------------------------------------------------------------------------
 
-// 16384 x 2048 into bfloat16 20.7 us (122 MB that cannot be done without: 17.9), two accesses of one row 22.9; 65536 x
-// 768 25.4 us and 31.
+// 16384 x 2048 into bfloat16 20.5 us (122 MB that cannot be done without: 17.9), two accesses of one row 22.9; 65536 x
+// 768 25.2 us and 31.  Rows off 16 bytes, by accesses of one element: 16384 x 2051 71 us, 65536 x 765 100 (floors 17.9, 21.9).
 constexpr int kLookThreads = 128, kLookRows = 4;
 
 // A thread takes eight columns of kLookRows rows as 16-byte accesses, or (rows off 16 bytes) a warp 128 columns of

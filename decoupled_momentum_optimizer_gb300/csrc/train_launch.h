@@ -166,7 +166,17 @@ constexpr int kClipTensors = 512, kClipFew = 64;
 constexpr int kClipParts = 640;  // most CTAs of a launch, each of which leaves a sum
 long long clip_chunks(uintptr_t address, long long n, int size);  // chunks of a tensor
 int clip_parts(unsigned chunks, int dtype, int sms);              // CTAs of a launch
-// Norm and scaling of at most kSmallChunks chunks in one launch (the norm alone: `only_norm`).
+// Norm and scaling of at most kSmallChunks chunks in one launch (the norm alone: `only_norm`).  us with one launch / with
+// two, float32 from L2; "clipped": into other tensors, "unclipped": in place, nothing to scale:
+//                             norm, called   from a graph  clipped, called  from a graph  unclipped, called  from a graph
+//   1 chunk, 1 tensor         4.1 / 6.2      3.9 / 4.3     5.6 / 6.7        5.4 / 6.4     4.2 / 6.5          4.0 / 5.0
+//   16 chunks, 1 tensor       4.8 / 6.1      4.5 / 4.2     6.9 / 7.1        6.6 / 6.4     4.9 / 6.4          4.6 / 5.0
+//   17 chunks, 17 tensors     6.0 / 7.0      5.5 / 4.4     9.3 / 8.0        8.9 / 7.0     6.1 / 7.4          5.6 / 5.3
+//   32 chunks, 1 tensor       5.5 / 6.0      5.2 / 4.2     8.9 / 7.4        8.6 / 6.5     5.6 / 6.4          5.3 / 5.3
+//   57 chunks, 57 tensors     8.0 / 7.8      7.6 / 4.6     13.4 / 10.5      13.0 / 7.0    8.1 / 9.6          7.7 / 5.6
+//   64 chunks, 1 tensor       6.7 / 6.1      6.4 / 4.2     12.6 / 8.5       12.7 / 7.0    6.8 / 6.4          6.6 / 5.8
+// So the limit suits calls whose gradients need no scaling.  What it gives up: calls that scale 17 chunks or more take 16 to
+// 50% longer than with two launches, graphs of them up to 86%; which of them a list meets is not known at its launch.
 constexpr unsigned kSmallChunks = 64;
 static_assert(kSmallChunks <= kClipFew, "a chunk for each tensor at least");
 cudaError_t launch_small_clip(const ClipParams<kClipFew>& p, int dtype, int out_dtype, cudaStream_t st);

@@ -74,8 +74,8 @@ __device__ __forceinline__ float rsqrt_pair(Pair m) {
 
 // A row is the registers of W warps with up to UNITS accesses a lane: one warp (eight rows to a CTA of 256
 // threads), or one CTA for the row.  UNITS 1 and 4 leave room for more warps an SM where rows are short (65536 x
-// 768 bfloat16: 44 us), and K = 4 rows at a time where they are shorter than a unit (1048576 x 64: 68 us; one at a
-// time 79).
+// 768 bfloat16: 44 us), and K = 4 rows at a time where they are shorter than a unit (1048576 x 64: 68 us, of
+// 39.4 for its bytes; one at a time 79).
 constexpr int kNormUnits = 8;
 constexpr int kNormThreads = 256, kNormWide = 1024;
 
