@@ -95,7 +95,7 @@ _wrote = torch.autograd.graph.increment_version
 def _written(*given):
     for t in given:
         if t is not None:
-            _wrote((t.codes, t.scales) if isinstance(t, Fp8Matrix) else t)
+            _wrote(t if isinstance(t, torch.Tensor) else (t.codes, t.scales))
 
 
 _FORM_CODES = {None: 0, "rows": 1, "cols": 2, "both": 3}

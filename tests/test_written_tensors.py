@@ -1,5 +1,7 @@
 """What a call writes of the tensors that it is given counts as modified in place: autograd notices a saved one."""
 
+import types
+
 import pytest
 import torch
 
@@ -13,6 +15,9 @@ def test_counts():
         c = torch.ones(2)
     ops._written(a, None, b, c)
     assert a._version == 1 and b._version == 1
+    q = types.SimpleNamespace(codes=a, scales=b)  # whatever has a quantized matrix's buffers
+    ops._written(q, q)
+    assert a._version == 3 and b._version == 3
 
 
 class Declines:
