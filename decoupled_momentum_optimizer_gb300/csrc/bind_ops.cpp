@@ -43,16 +43,21 @@ const at::Tensor& tensor(PyObject* o) {
 // One call: its device (the first tensor's), which must be the current one.
 struct Call {
   bool recorded = c10::GradMode::is_enabled();
-  // A level of forward-mode tangents is open, and they are followed (they are not within an autograd.Function).
-  bool tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode() &&
-                  torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr;
+  int tangents = -1;  // whether forward-mode tangents are followed: a level is open, and this is no autograd.Function
   int device = -1;
   std::vector<c10::TensorImpl*> written;  // given tensors that the call writes
 
+  // Few tensors have any autograd data, and only then is it worth to ask for the level (a lock).
+  bool has_tangent(const at::Tensor& t) {
+    if (t.unsafeGetTensorImpl()->autograd_meta() == nullptr) return false;
+    if (tangents < 0)
+      tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode() &&
+                 torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr;
+    return tangents != 0 && t._fw_grad(0).defined();
+  }
   const at::Tensor& take(PyObject* o) {
     const at::Tensor& t = tensor(o);
-    if (!t.is_cuda() || (recorded && t.requires_grad())) throw Other();
-    if (tangents && t._fw_grad(0).defined()) throw Other();
+    if (!t.is_cuda() || (recorded && t.requires_grad()) || has_tangent(t)) throw Other();
     const int d = static_cast<int>(t.get_device());
     if (device < 0) {
       if (c10::cuda::current_device() != d) throw Other();

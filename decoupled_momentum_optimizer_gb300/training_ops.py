@@ -95,7 +95,7 @@ _wrote = torch.autograd.graph.increment_version
 def _written(*given):
     for t in given:
         if t is not None:
-            _wrote(t if isinstance(t, torch.Tensor) else (t.codes, t.scales))
+            _wrote((t.codes, t.scales) if t.__class__ is Fp8Matrix or not isinstance(t, torch.Tensor) else t)
 
 
 _FORM_CODES = {None: 0, "rows": 1, "cols": 2, "both": 3}
